@@ -530,6 +530,180 @@ spec_status spec_vp_chain_finish(int B, int gamma, int V_shard, const int32_t* t
                                  void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * The cache around a verify round
+ * -------------------------------
+ * [atlas] §2 "tree attention", [origins] "SpecInfer" (token tree flattened,
+ * ancestor-only mask): the round that a verify call judges scores every
+ * drafted node against the sequence's cached tokens and the node's own
+ * ancestors, and only the accepted path's keys and values stay.  Four calls:
+ *   1. spec_tree_plan, once per round: positions and ancestor masks;
+ *   2. spec_qk_norm_rope, per layer: per-head norm and rotation of q and k;
+ *   3. spec_tree_attention, per layer: the nodes' attention;
+ *   4. spec_kv_append, per layer after the verify call: the accepted rows
+ *      (out_accept_index / out_num_accepted of a tree call, out_num_accepted
+ *      of a chain call) into the cache.  A prompt enters the same way.
+ *
+ * The cache holds, per layer, blocks of page_size consecutive tokens.  A full
+ * block of a kv head is a page in 8 bits (e4m3) with one f32 scale for keys
+ * and one for values; it is written once, when its last token arrives.  The
+ * tokens of the unfilled last block stay in bf16 in a ring of two blocks per
+ * sequence slot.  So what the cache holds of a token depends neither on
+ * rejected drafts nor on how the tokens were split over calls, and pages can
+ * be shared between sequences.
+ *
+ * k_pages, v_pages  [num_pages, kv_heads, page_size, head_dim] e4m3 bytes,
+ *                contiguous, 16-byte aligned.  value = e4m3 * scale.
+ * k_scale, v_scale  [num_pages, kv_heads] f32, positive and finite (a
+ *                scale written by spec_kv_append is a power of two).
+ * k_open, v_open [num_slots, kv_heads, 2 * page_size, head_dim] bf16,
+ *                contiguous, 16-byte aligned: token t of the unfilled block is
+ *                row t mod (2 * page_size).
+ * page_table     [B, page_table_stride] int32: entry j of sequence b is the
+ *                page of its tokens [j * page_size, (j + 1) * page_size).  Only
+ *                the entries of full blocks are read.  NULL iff max_pages = 0.
+ * slots          [B] int32, nullable (NULL: slot b): the sequence's ring.  Two
+ *                sequences of a call must not share a ring.
+ * lengths        [B] int32: tokens in the cache; negative = no sequence in this
+ *                row (its outputs are zeros, nothing is appended).
+ * head_dim 64 or 128; page_size 16, 32, 64 or 128; lengths up to
+ * max_pages * page_size + page_size - 1 and below 2^30.
+ *
+ * Sequences whose device-side inputs are invalid (a page id outside
+ * [0, num_pages) where it is read, a slot outside [0, num_slots), a length above
+ * the limit) get NaN in every attention output, or length -1 and no write from
+ * an append; the SPEC_ERR_DEVICE_INPUT bit is set in the workspace.
+ *
+ * One workspace of spec_cache_workspace_bytes serves all four calls of a round,
+ * for one stream at a time; spec_workspace_init clears it once.
+ */
+typedef struct spec_kv_cache {
+    void* k_pages;
+    void* v_pages;
+    float* k_scale;
+    float* v_scale;
+    void* k_open;
+    void* v_open;
+    const int32_t* page_table;
+    const int32_t* slots;
+    const int32_t* lengths;
+    int64_t num_pages;
+    int64_t page_table_stride;
+    int32_t num_slots;
+    int32_t max_pages;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t page_size;
+} spec_kv_cache;
+
+#define SPEC_MAX_CACHE_LEN (1 << 30)
+#define SPEC_MAX_HEADS 1024
+
+/*
+ * spec_cache_workspace_bytes -- workspace of the cache calls for B sequences
+ * of N nodes with q_heads query heads of head_dim elements (covers smaller B and
+ * N).  0 for out-of-range arguments.  Pure host function.
+ */
+size_t spec_cache_workspace_bytes(int B, int N, int q_heads, int head_dim);
+
+/*
+ * spec_tree_plan -- positions and ancestor masks of B draft trees.
+ * parents        [B, N] int32 as in spec_verify_tree_*; NULL = chains (the
+ *                parent of n is n - 1, max_depth is not looked at).
+ * lengths        [B] int32: cached tokens (the root's position); negative =
+ *                no sequence in this row.
+ * out_positions  [B, N] int32: lengths[b] + depth(n); -1 in every node of a row
+ *                without a sequence or with an invalid one.
+ * out_ancestors  [B, N, ceil(N/32)] int32 words: bit (m mod 32) of word m / 32 of
+ *                row n is set iff m is n or an ancestor of n; zeros where the
+ *                position is -1.
+ * A malformed parent array, a depth above max_depth or a length of 2^30 or more
+ * makes the sequence invalid (SPEC_ERR_DEVICE_INPUT).
+ */
+spec_status spec_tree_plan(int B, int N, int max_depth, const int32_t* parents, const int32_t* lengths,
+                           int32_t* out_positions, int32_t* out_ancestors,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * spec_qk_norm_rope -- per-head RMS norm and rotary positions of the queries
+ * and keys of B x N nodes, in one pass.  For each head row x of D elements at
+ * position p (all in f32, the angle in f64, one rounding at the end):
+ *   y = x * (mean(x^2) + eps)^(-1/2) * weight        (skipped: weight NULL)
+ *   y_a, y_b = y_a cos - y_b sin, y_b cos + y_a sin, angle p * inv_freq[j]
+ * for the pairs j < rot_dim / 2: (a, b) = (j, j + rot_dim/2), or (2j, 2j + 1)
+ * with interleaved = 1; elements from rot_dim on are not rotated.
+ * q              [B, N, q_heads, D] of dt, strides in elements for the batch,
+ *                node and head axes, unit stride in D; 16-byte aligned rows.
+ * k              [B, N, kv_heads, D] likewise (kv_heads = 0: none).
+ * positions      [B, N] int32, contiguous; negative: zeros are written.
+ * inv_freq       [rot_dim / 2] f32; rot_dim = 0: no rotation.
+ * q_weight, k_weight  [D] of wdt, nullable.
+ * q_out, k_out   strides of their own; may be q and k themselves, else must not
+ *                overlap them.
+ * D a multiple of 8 up to 256, rot_dim a multiple of 16 up to D.
+ */
+spec_status spec_qk_norm_rope(int B, int N, int q_heads, int kv_heads, int D,
+                              const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides,
+                              spec_dtype dt, const int32_t* positions,
+                              const float* inv_freq, int rot_dim, int interleaved,
+                              const void* q_weight, const void* k_weight, spec_dtype wdt, float eps,
+                              void* q_out, const int64_t* q_out_strides,
+                              void* k_out, const int64_t* k_out_strides, void* stream);
+
+/*
+ * spec_tree_attention -- attention of B x N nodes over the cache and each
+ * other.  Query head h reads kv head h / (q_heads / kv_heads).  Row (b, n, h):
+ *   keys = the lengths[b] cached tokens and the nodes m whose bit is set in
+ *   ancestors[b, n];  out = sum softmax(scale * q.k) v,
+ *   lse = log sum exp(scale * q.k).
+ * A row without any key gets out = 0 and lse = -inf.  A non-finite key or value
+ * of a node reaches only the rows whose mask holds that node.
+ * q, k, v        [B, N, heads, D] bf16, strides in elements (batch, node, head),
+ *                unit stride in D, 16-byte aligned rows; k and v have the
+ *                cache's kv_heads.
+ * ancestors      [B, N, ceil(N/32)] int32 words (any mask, bits past N are not
+ *                read); NULL = every node sees nodes 0..n (chains).
+ * out            [B, N, q_heads, D] bf16, contiguous.
+ * lse            nullable, [B, N, q_heads] f32.
+ * 1 <= N <= SPEC_MAX_NODES; q_heads a multiple of kv_heads.
+ * workspace      >= spec_cache_workspace_bytes(B, N, q_heads, D).
+ * Products and sums in f32 (the probabilities enter the second product as f16).
+ */
+spec_status spec_tree_attention(int B, int N, int q_heads, const spec_kv_cache* cache,
+                                const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides,
+                                const void* v, const int64_t* v_strides,
+                                const int32_t* ancestors, float scale, void* out, float* lse,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * spec_kv_append -- add the first num_accepted[b] + 1 rows of sequence b's
+ * path to its cache: the root and the accepted drafts of a verify round, or a
+ * prompt.
+ * k, v           [B, T, kv_heads, D] of dt (bf16 or f32), strides in elements
+ *                (batch, token, head), unit stride in D, 16-byte aligned rows.
+ * num_accepted   [B] int32, nullable (NULL: width - 1): -1 appends nothing.
+ * accept_index   [B, width] int32, nullable (NULL: rows 0..width-1, width <= T):
+ *                row i of the path is row accept_index[b, i] of k and v.
+ * Row i becomes token lengths[b] + i.  With k_weight and / or rot_dim > 0 its key
+ * is normed and rotated to that position on the way as by spec_qk_norm_rope.
+ * Keys and values are rounded to bf16; when a block fills, each head's block is
+ * scaled by the least power of two that brings its largest finite magnitude
+ * within 448 (1 for a block of zeros) and rounded to e4m3 (nearest, ties to
+ * even); NaN and infinities become NaN.
+ * out_lengths    [B] int32: lengths[b] + rows; may be the lengths themselves.
+ *                -1 for an invalid sequence (a bad page, slot or length, a row
+ *                outside [0, T), num_accepted >= width or < -1, no room), whose
+ *                cache is left as it was; a negative length is passed on.
+ * 1 <= T, width <= 2^20.
+ */
+spec_status spec_kv_append(int B, int T, int width, const spec_kv_cache* cache,
+                           const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                           spec_dtype dt, const int32_t* num_accepted, const int32_t* accept_index,
+                           const float* inv_freq, int rot_dim, int interleaved,
+                           const void* k_weight, spec_dtype wdt, float eps,
+                           int32_t* out_lengths,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * spec_workspace_bytes -- workspace size for one entry point and shape.
  * rows = gamma for SPEC_ENTRY_CHAIN (sized for draft logits, which also
  * covers draft probabilities), N for the tree entry points.  Returns 0 for

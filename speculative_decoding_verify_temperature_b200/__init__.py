@@ -1,9 +1,18 @@
 """B200-native verify/accept step of speculative decoding.
 
 ``spec_verify`` is the Python binding of ``libspecverify.so`` (C ABI in
-``include/spec_verify.h``); ``workloads`` makes the seeded synthetic inputs.
+``include/spec_verify.h``); ``kv_cache`` binds the cache calls around a verify
+round; ``workloads`` makes the seeded synthetic inputs.
 """
 from . import workloads  # noqa: F401
+from .kv_cache import (  # noqa: F401
+    KvCache,
+    spec_cache_workspace_bytes,
+    spec_kv_append,
+    spec_qk_norm_rope,
+    spec_tree_attention,
+    spec_tree_plan,
+)
 from .spec_verify import (  # noqa: F401
     SpecError,
     Workspace,

@@ -1,0 +1,122 @@
+// cache_device.cuh -- device helpers of the cache kernels: rows of 8-element
+// vectors, the RMS norm and the rotation of a head row, e4m3.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "spec_verify.h"
+
+namespace svc {
+
+constexpr unsigned FULL = 0xffffffffu;
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {   // round to nearest, ties to even
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Two e4m3 bytes (lo in bits 0-7), round to nearest even, NaN -> 0x7F.
+__device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Eight consecutive elements as they lie in memory.
+template <int DT> struct Vec8;
+template <> struct Vec8<SPEC_BF16> {
+    static constexpr int ESZ = 2;
+    uint4 a;
+    __device__ __forceinline__ void load(const char* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void load_plain(const char* p) { a = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        x[0] = bf_lo(a.x); x[1] = bf_hi(a.x); x[2] = bf_lo(a.y); x[3] = bf_hi(a.y);
+        x[4] = bf_lo(a.z); x[5] = bf_hi(a.z); x[6] = bf_lo(a.w); x[7] = bf_hi(a.w);
+    }
+    __device__ __forceinline__ void set(const float (&x)[8]) {
+        a = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+    }
+    __device__ __forceinline__ void store(char* p) const { *reinterpret_cast<uint4*>(p) = a; }
+};
+template <> struct Vec8<SPEC_F32> {
+    static constexpr int ESZ = 4;
+    float4 a, b;
+    __device__ __forceinline__ void load(const char* p) {
+        a = __ldg(reinterpret_cast<const float4*>(p));
+        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void load_plain(const char* p) {
+        a = reinterpret_cast<const float4*>(p)[0];
+        b = reinterpret_cast<const float4*>(p)[1];
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+    __device__ __forceinline__ void set(const float (&x)[8]) {
+        a = make_float4(x[0], x[1], x[2], x[3]);
+        b = make_float4(x[4], x[5], x[6], x[7]);
+    }
+    __device__ __forceinline__ void store(char* p) const {
+        reinterpret_cast<float4*>(p)[0] = a;
+        reinterpret_cast<float4*>(p)[1] = b;
+    }
+};
+
+// cos and sin of pos * f.  The angle is formed in f64, in turns, and reduced to
+// [-1/2, 1/2] there: f32 would lose a far position's angle (at 2^20 its spacing
+// is 2^-4 rad).
+__device__ __forceinline__ float2 cos_sin(int pos, float f) {
+    double t = (double)pos * ((double)f * 0.15915494309189533577);
+    t -= rint(t);
+    float s, c;
+    sincospif((float)(2.0 * t), &s, &c);
+    return make_float2(c, s);
+}
+
+// A head row of D elements lies in D / 8 consecutive lanes of an aligned group
+// of GW lanes, eight elements each; the lanes behind hold zeros.  l: lane of the group.
+// 1 / rms of the row, in every lane of the group; all lanes of the warp call it.
+__device__ __forceinline__ float row_rms(const float (&x)[8], int GW, float inv_d, float eps) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+    for (int o = GW >> 1; o; o >>= 1) ss += __shfl_xor_sync(FULL, ss, o);
+    return rsqrtf(fmaf(ss, inv_d, eps));
+}
+
+// First index of the eight (split halves) or four (interleaved) pairs whose
+// angles lane l uses.
+__device__ __forceinline__ int pair_base(int l, int rot, bool interleaved) {
+    return interleaved ? 4 * l : (8 * l < rot / 2 ? 8 * l : 8 * l - rot / 2);
+}
+
+// Rotate the row's first `rot` elements; c, s are the angles of the lane's pairs.
+// All lanes of the warp call it.
+__device__ __forceinline__ void row_rotate(float (&x)[8], const float (&c)[8], const float (&s)[8], int l, int lane,
+                                           int rot, bool interleaved) {
+    if (interleaved) {
+        if (8 * l < rot) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = x[2 * i], b = x[2 * i + 1];
+                x[2 * i] = a * c[i] - b * s[i];
+                x[2 * i + 1] = b * c[i] + a * s[i];
+            }
+        }
+        return;
+    }
+    const bool first = 8 * l < rot / 2;
+    const int src = 8 * l < rot ? (first ? lane + rot / 16 : lane - rot / 16) : lane;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float o = __shfl_sync(FULL, x[i], src);
+        if (8 * l < rot) x[i] = first ? x[i] * c[i] - o * s[i] : x[i] * c[i] + o * s[i];
+    }
+}
+
+}  // namespace svc

@@ -83,6 +83,17 @@ def lib():
                                            P, P, P, P, P, P, sz, P]
         L.spec_vp_chain_finish.restype = i32
         L.spec_vp_chain_finish.argtypes = [i32, i32, i32, P, P, P, sz, P]
+        L.spec_cache_workspace_bytes.restype = sz
+        L.spec_cache_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.spec_tree_plan.restype = i32
+        L.spec_tree_plan.argtypes = [i32, i32, i32, P, P, P, P, P, sz, P]
+        L.spec_qk_norm_rope.restype = i32
+        L.spec_qk_norm_rope.argtypes = [i32, i32, i32, i32, i32, P, P, P, P, i32, P, P, i32, i32, P, P, i32, f32,
+                                        P, P, P, P, P]
+        L.spec_tree_attention.restype = i32
+        L.spec_tree_attention.argtypes = [i32, i32, i32, P, P, P, P, P, P, P, P, f32, P, P, P, sz, P]
+        L.spec_kv_append.restype = i32
+        L.spec_kv_append.argtypes = [i32, i32, i32, P, P, P, P, P, i32, P, P, P, i32, i32, P, i32, f32, P, P, sz, P]
         L.spec_workspace_bytes.restype = sz
         L.spec_workspace_bytes.argtypes = [i32, i32, i32, i32]
         L.spec_workspace_init.restype = i32
