@@ -9,16 +9,1035 @@ using namespace svc;
 
 namespace {
 
+constexpr int TILE = 128;                 // keys of one step
+constexpr float NEG_INF = -INFINITY;
+constexpr float LN2 = 0.69314718055994530942f;
+
 struct Att {
-    int B, N, Hq, Hkv, G, D, page;
+    int B, N, Hq, Hkv, G, page, R;        // R = N * G rows of a kv head
+    int mtiles;                           // items per (sequence, kv head)
     sv_host::Rows q, k, v;
     spec_kv_cache c;
-    const uint32_t* anc;          // nullable: chains
-    float scale;                  // scale * log2(e)
+    const uint32_t* anc;                  // nullable: chains
+    float scale;                          // scale * log2(e)
     char* out;
     float* lse;
     unsigned* status;
+    unsigned* item_cnt;                   // [gridDim.x] arrivals at an item that several CTAs share
+    float* partial;                       // [gridDim.x][2][rows of an item][D + 2]
 };
+
+// ----------------------------------------------------------------------------- the work and its split
+
+// The keys of a sequence: `full` cached tokens in 8-bit blocks, then a tail of
+// `open` tokens of the unfilled block and the N nodes.  Each part is cut into
+// tiles of TILE keys.
+struct Seq {
+    int len, slot, full, open, nct, ntiles;
+    bool bad;
+};
+
+__device__ __forceinline__ Seq seq_of(const Att& P, int b) {
+    Seq s;
+    s.len = P.c.lengths[b];
+    s.slot = P.c.slots ? P.c.slots[b] : b;
+    const int64_t most = (int64_t)P.c.max_pages * P.page + P.page - 1;
+    s.bad = s.len >= 0 && (s.len > most || s.len >= SPEC_MAX_CACHE_LEN || s.slot < 0 || s.slot >= P.c.num_slots);
+    const bool live = s.len >= 0 && !s.bad;
+    s.full = live ? s.len / P.page * P.page : 0;
+    s.open = live ? s.len - s.full : 0;
+    s.nct = (s.full + TILE - 1) / TILE;
+    s.ntiles = s.nct + (s.open + P.N + TILE - 1) / TILE;
+    if (!live) s.nct = 0, s.ntiles = 1;   // one step that writes the rows' zeros or NaN
+    return s;
+}
+
+// The tiles of all items (sequence, kv head, rows), in that order, are one line;
+// every CTA takes an equal stretch of it, whatever the lengths are.  An item
+// that a stretch border cuts is put together by the last of its CTAs.
+struct Stretch {
+    long long lo, hi, total;              // tiles
+    int ctas;                             // CTAs that share the line: each has at least one tile
+    int b;                                // sequence of tile lo
+    long long b_lo;                       // first tile of that sequence
+};
+
+__device__ __forceinline__ long long stretch_at(long long total, int cta, int ctas) { return total * cta / ctas; }
+// CTA that holds tile x.
+__device__ __forceinline__ int cta_of(long long x, long long total, int ctas) {
+    int c = (int)(x * ctas / total);
+    while (stretch_at(total, c + 1, ctas) <= x) ++c;
+    while (stretch_at(total, c, ctas) > x) --c;
+    return c;
+}
+
+// All threads of the CTA (BT of them).  Two passes over the lengths: the total, then the sequence
+// where the stretch begins.
+template <int BT>
+__device__ Stretch find_stretch(const Att& P) {
+    __shared__ long long wsum[BT / 32 + 1];
+    __shared__ int hit_b;
+    __shared__ long long hit_lo;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int items = P.Hkv * P.mtiles;
+    Stretch s{};
+    long long mine = 0, first = 0;
+    for (int b = tid; b < P.B; b += BT) {
+        const long long n = (long long)seq_of(P, b).ntiles * items;
+        if (b == tid) first = n;
+        mine += n;
+    }
+    long long sum = mine;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+    if (lane == 0) wsum[warp] = sum;
+    __syncthreads();
+    for (int w = 0; w < BT / 32; ++w) s.total += wsum[w];
+    s.ctas = (int)min((long long)gridDim.x, s.total);
+    if ((int)blockIdx.x >= s.ctas) return s;               // the same in every thread; lo = hi
+    s.lo = stretch_at(s.total, blockIdx.x, s.ctas);
+    s.hi = stretch_at(s.total, blockIdx.x + 1, s.ctas);
+    long long before = 0;
+    for (int base = 0; base < P.B; base += BT) {
+        const int b = base + tid;
+        const long long n = base == 0 ? first : b < P.B ? (long long)seq_of(P, b).ntiles * items : 0;
+        long long inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(FULL, inc, o);
+            if (lane >= o) inc += up;
+        }
+        __syncthreads();
+        if (lane == 31) wsum[warp] = inc;
+        __syncthreads();
+        long long off = before, all = 0;
+        for (int w = 0; w < BT / 32; ++w) {
+            if (w < warp) off += wsum[w];
+            all += wsum[w];
+        }
+        inc += off;
+        if (s.lo < inc && s.lo >= inc - n) {
+            hit_b = b;
+            hit_lo = inc - n;
+        }
+        before += all;
+        if (before > s.lo) break;
+    }
+    __syncthreads();
+    s.b = hit_b;
+    s.b_lo = hit_lo;
+    return s;
+}
+
+// A CTA's part of one item.
+struct Seg {
+    Seq q;
+    int b, h, mt;
+    int t0, t1;                           // tiles of the item
+    long long item_lo;                    // the item's first tile on the line
+};
+
+struct SegIter {
+    Stretch s;
+    long long at, b_lo;
+    int b;
+    Seq q;
+    __device__ __forceinline__ void begin(const Att& P, const Stretch& st) {
+        s = st;
+        at = st.lo;
+        b = st.b;
+        b_lo = st.b_lo;
+        if (at < s.hi) q = seq_of(P, b);
+    }
+    __device__ __forceinline__ bool next(const Att& P, Seg& g) {
+        if (at >= s.hi) return false;
+        const int items = P.Hkv * P.mtiles;
+        while (at >= b_lo + (long long)q.ntiles * items) {
+            b_lo += (long long)q.ntiles * items;
+            q = seq_of(P, ++b);
+        }
+        const int item = (int)((at - b_lo) / q.ntiles);
+        g.q = q;
+        g.b = b;
+        g.h = item / P.mtiles;
+        g.mt = item % P.mtiles;
+        g.item_lo = b_lo + (long long)item * q.ntiles;
+        g.t0 = (int)(at - g.item_lo);
+        g.t1 = (int)min((long long)q.ntiles, s.hi - g.item_lo);
+        at = g.item_lo + g.t1;
+        return true;
+    }
+};
+
+// 32 bits of the mask of node n over the tail's keys [e0, e0 + 32): the open
+// tokens are seen by every node, node m by the rows whose mask holds it.
+__device__ __forceinline__ uint32_t tail_bits(const Att& P, int b, int n, int open, int e0) {
+    uint32_t bits = 0;
+    if (e0 < open) bits = open - e0 >= 32 ? 0xffffffffu : (1u << (open - e0)) - 1u;
+    const int m0 = e0 - open;             // node of bit 0 (negative: an open token)
+    if (m0 > -32 && m0 < P.N) {
+        uint32_t nodes;
+        if (P.anc) {
+            const int W = (P.N + 31) / 32;
+            const uint32_t* a = P.anc + ((int64_t)b * P.N + n) * W;
+            const int w = m0 >> 5, sh = m0 & 31;           // arithmetic shift: w = -1 for m0 < 0
+            const uint32_t lo = w >= 0 ? __ldg(a + w) : 0u, hi = w + 1 < W ? __ldg(a + w + 1) : 0u;
+            nodes = __funnelshift_r(lo, hi, sh);
+        } else {
+            const int last = n - m0;      // nodes 0..n
+            nodes = last < 0 ? 0u : last >= 31 ? 0xffffffffu : (2u << last) - 1u;
+            if (m0 < 0) nodes &= 0xffffffffu << -m0;
+        }
+        const int left = P.N - m0;
+        if (left < 32) nodes &= (1u << left) - 1u;
+        bits |= nodes;
+    }
+    return bits;
+}
+
+// ----------------------------------------------------------------------------- tensor-core kernel (tcgen05)
+
+// Roles of the CTA's warps: 0-3 and 4-7 the softmax of one stream each, 8-15 the
+// loads, 16 the matrix instructions (one thread).
+//
+// An item holds up to 256 rows.  With more than 128 the two streams are its two
+// halves and both take every tile; with 128 or fewer both streams hold the same
+// rows and take the tiles in turn, and their sums are joined at the end.  While
+// one stream's softmax works on its scores, the tensor cores work for the other.
+//
+//   S_i = Q_i K^T    f16 operands from shared memory, f32 in tensor memory
+//   P_i              f16, over S_i's columns
+//   O_i += P_i V     P from tensor memory, V from shared memory
+//
+// The f16 operands are exact: an e4m3 value is an f16 value, and a bf16 row of q
+// or of the tail's k and v is divided by a power of two that brings its largest
+// magnitude to [1, 2) (what f16 then cannot hold is below 2^-25 of it).  The
+// scales come back in f32: with a_j the key's scale times the row's and s_v,j
+// the value's, x_j = S_j a_j is the score in base 2 and
+//   w_j = x_j + log2 s_v,j,  M = max w_j,  P_j = 2^(w_j - M),
+//   O = sum P_j v_j,  l = sum P_j / s_v,j,  out = O / l.
+// M follows the weight with which a value enters O, so that f16 holds the
+// leading P whatever the blocks' scales are.  O is rescaled only when M grows by
+// more than 2^4; P_BIAS lifts P to at most 2^15, so that f16's smallest step is
+// 2^-35 of the leading one.
+constexpr int TC_SOFTMAX = 256, TC_LOAD = 256, TC_BT = TC_SOFTMAX + TC_LOAD + 32;
+constexpr int TC_META = 4;                // tiles whose scales are kept
+constexpr float P_BIAS = 11.f, M_SLACK = 4.f;
+
+template <int D> struct Tc {
+    static constexpr int HALVES = D / 64;                 // 128-byte rows of 64 f16
+    static constexpr uint32_t HALF = 128 * 128;           // 128 such rows
+    static constexpr uint32_t TILE_B = HALVES * HALF;     // an operand tile
+    static constexpr uint32_t Q = 0, K = 2 * TILE_B, V = 4 * TILE_B, END = 6 * TILE_B;
+    static constexpr int O_COL = 256;                     // tensor memory columns: S0 S1 (128 each), O0 O1 (D each)
+};
+struct TcShared {
+    float meta[TC_META][3][TILE];                         // per key (tail) or group of 16 (cached): a, log2 s_v, 1 / s_v
+    float rq[4][256];                                     // per row: its power of two * scale * log2(e)
+    float xm[2][TILE], xl[2][TILE];                       // M and l of the streams that are joined
+    uint32_t bad_v[4][12];                                // tail keys whose value is not finite
+    int bad_seg[4];                                       // 1 + segment that met a bad page
+    uint64_t kf[2], ke[2], vf[2], ve[2], sf[2], pf[2], pv[2], qf, qe, drain;
+    uint32_t tmem;
+    int abort;
+    int last[2];
+};
+// 1 KB of alignment slack; at least what keeps a second CTA, and its tensor memory, off the SM
+template <int D> constexpr size_t tc_smem() {
+    const size_t need = Tc<D>::END + sizeof(TcShared) + 1024;
+    return need > 120 * 1024 ? need : 120 * 1024;
+}
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Four e4m3 bytes to two pairs of f16 (exact).
+__device__ __forceinline__ uint2 e4m3_f16(uint32_t w) {
+    uint2 r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}" : "=r"(r.x), "=r"(r.y) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Barriers.  Every wait is bounded: when one gives up, the CTA's `abort` is set
+// and all waits return at once; every role then runs through its (finite) loops
+// with whatever is there, and the status word says that the results are void.
+constexpr unsigned WAIT_TRIES = 1u << 24;
+constexpr unsigned long long WAIT_NS = 1000000000ull;
+__device__ __forceinline__ void bar_init(uint64_t* b, unsigned n) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(smem_u32(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(b)) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(b)), "r"(parity) : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ unsigned long long global_ns() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+__device__ __noinline__ bool bar_wait_slow(uint64_t* b, uint32_t parity, volatile int* abort) {
+    const unsigned long long t0 = global_ns();
+    for (unsigned i = 0; i < WAIT_TRIES; ++i) {
+        if (bar_try(b, parity)) return true;
+        if (abort && *abort) return false;
+        if (global_ns() - t0 > WAIT_NS) break;
+    }
+    return false;
+}
+__device__ __forceinline__ void bar_wait(uint64_t* b, uint32_t parity, TcShared& sh) {
+    if (bar_try(b, parity)) return;
+    if (!bar_wait_slow(b, parity, &sh.abort)) *reinterpret_cast<volatile int*>(&sh.abort) = 1;
+}
+
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* b) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(smem_u32(b)) : "memory");
+}
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t (&r)[32]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+                 "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(a));
+}
+__device__ __forceinline__ void tc_st32(uint32_t a, const uint32_t (&r)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+                 "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};"
+                 :: "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                    "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+                    "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+                    "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+                 "%14, %15};"
+                 :: "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                    "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(a)
+                 : "memory");
+}
+
+// Shared-memory operand descriptor: 128-byte swizzle, 8-row groups 1024 bytes
+// apart; `lead` is the step between 64-element column groups (only looked at
+// where the contiguous axis is not the one summed over).
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lead) {
+    return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 |
+           2ull << 61;
+}
+// f16 x f16 -> f32, M = 128; bit 16: the second operand's contiguous axis is N
+__host__ __device__ constexpr uint32_t tc_idesc(int n, bool b_n_major) {
+    return 1u << 4 | (b_n_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
+}
+
+// Address of 16-byte chunk q (0-7) of row r within a 64-column half.
+__device__ __forceinline__ uint32_t swz(uint32_t half, int r, int q) { return half + r * 128 + ((q ^ (r & 7)) << 4); }
+
+// Power of two that brings the finite magnitude amax to [1, 2) (to [2, 4) at the
+// very top of f32's range); 1 for zero.
+__device__ __forceinline__ int pow2_of(float amax) {
+    const int e = (int)(__float_as_uint(amax) >> 23) - 127;
+    return amax > 0.f ? min(max(e, -126), 126) : 0;
+}
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126..127
+
+__device__ __forceinline__ float finite_abs(float x) {
+    const float a = fabsf(x);
+    return a <= 3.402823466e38f ? a : 0.f;
+}
+
+// One tile as the loading warps see it.
+struct LoadTile {
+    int b, h, mt, t, kind;                // kind: 0 none left, 1 cached, 2 tail, 3 no keys at all
+    bool first;                           // of its segment
+};
+
+template <int D>
+struct TcLoader {
+    static constexpr int CPR = D / 16;                    // 16-byte chunks of a cached row
+    static constexpr int RPP = TC_LOAD / CPR;             // rows per pass
+    static constexpr int NP = TILE / RPP;                 // passes
+    const Att& P;
+    TcShared& sh;
+    const uint32_t base;
+    const int tid, lane, c, r0;
+    SegIter it;
+    Seg g;
+    int t, seg;                                           // next tile of g; segments begun
+    bool have;
+    int ids[NP], ids_b, ids_t;                            // page ids fetched ahead
+
+    __device__ __forceinline__ TcLoader(const Att& P_, TcShared& s, uint32_t b, int tid_)
+        : P(P_), sh(s), base(b), tid(tid_), lane(tid_ & 31), c(tid_ % CPR), r0(tid_ / CPR) {}
+
+    __device__ __forceinline__ void begin(const Stretch& st) {
+        it.begin(P, st);
+        have = it.next(P, g);
+        t = have ? g.t0 : 0;
+        ids_b = -1;
+        ids_t = -1;
+    }
+    __device__ __forceinline__ LoadTile next() {
+        LoadTile x{};
+        if (have && t == g.t1) {
+            have = it.next(P, g);
+            if (have) t = g.t0;
+        }
+        if (!have) return x;
+        x.b = g.b; x.h = g.h; x.mt = g.mt; x.t = t;
+        x.kind = t < g.q.nct ? 1 : g.q.len >= 0 && !g.q.bad ? 2 : 3;
+        x.first = t == g.t0;
+        ++t;
+        return x;
+    }
+    __device__ __forceinline__ int page_id(int b, int t, int i) {
+        const int tok = t * TILE + r0 + i * RPP;
+        return tok < g.q.full ? __ldg(P.c.page_table + b * P.c.page_table_stride + tok / P.page) : -2;
+    }
+    // Bytes of a cached tile, and the scales of its groups of 16 keys (threads 0-7), on their way to registers.
+    // Called right after next(): g is the tile's item.
+    __device__ __forceinline__ void fetch(const LoadTile& x, uint4 (&k)[NP], uint4 (&v)[NP], float& ks, float& vs, bool& bad) {
+        bad = false;
+        if (x.kind != 1) return;
+        if (ids_b != x.b || ids_t != x.t) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) ids[i] = page_id(x.b, x.t, i);
+        }
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int tok = x.t * TILE + r0 + i * RPP;
+            const bool ok = ids[i] >= 0 && ids[i] < P.c.num_pages;
+            bad |= ids[i] != -2 && !ok;
+            k[i] = v[i] = make_uint4(0, 0, 0, 0);
+            if (ok) {
+                const int64_t at = (((int64_t)ids[i] * P.Hkv + x.h) * P.page + tok % P.page) * D + c * 16;
+                k[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(P.c.k_pages) + at));
+                v[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(P.c.v_pages) + at));
+            }
+        }
+        ks = vs = 1.f;
+        if (tid < 8) {
+            const int tok = x.t * TILE + tid * 16;
+            const int id = tok < g.q.full ? __ldg(P.c.page_table + x.b * P.c.page_table_stride + tok / P.page) : -2;
+            if (id >= 0 && id < P.c.num_pages) {
+                ks = __ldg(P.c.k_scale + (int64_t)id * P.Hkv + x.h);
+                vs = __ldg(P.c.v_scale + (int64_t)id * P.Hkv + x.h);
+            }
+        }
+        ids_b = x.b;
+        ids_t = x.t + 1;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) ids[i] = page_id(x.b, ids_t, i);
+    }
+    __device__ __forceinline__ void arrive(uint64_t* bar) {
+        proxy_fence();
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar);
+    }
+    // A cached tile's bytes as f16 rows.  The upper half of the lanes that share rows stores its two
+    // chunks in the other order, so that eight lanes meet all 32 banks.
+    __device__ __forceinline__ void put(uint32_t dst, const uint4 (&x)[NP]) {
+        const uint32_t half = dst + (c / 4) * Tc<D>::HALF;
+        const int q = (c % 4) * 2, flip = c / 4;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const uint2 a = e4m3_f16(x[i].x), b = e4m3_f16(x[i].y), d = e4m3_f16(x[i].z), e = e4m3_f16(x[i].w);
+            const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, e.x, e.y);
+            const int r = r0 + i * RPP;
+            sts128(swz(half, r, q + flip), flip ? hi : lo);
+            sts128(swz(half, r, q + 1 - flip), flip ? lo : hi);
+        }
+    }
+    // Rows of eight bf16 elements per lane, D / 8 lanes per row; returns the row's power of two.
+    __device__ __forceinline__ int put_row(uint32_t dst, int r, int l, uint4 raw, bool& nonfinite, bool zero_nonfinite) {
+        Vec8<SPEC_BF16> w;
+        w.a = raw;
+        float x[8], amax = 0.f;
+        w.get(x);
+        nonfinite = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float a = finite_abs(x[i]);
+            if (!(fabsf(x[i]) <= 3.402823466e38f)) {
+                nonfinite = true;
+                if (zero_nonfinite) x[i] = 0.f;
+            }
+            amax = fmaxf(amax, a);
+        }
+#pragma unroll
+        for (int o = D / 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, o));
+        const int e = pow2_of(amax);
+        const float s = exp2i(-e);
+        sts128(swz(dst + (l / 8) * Tc<D>::HALF, r, l % 8),
+               make_uint4(pack_f16(x[0] * s, x[1] * s), pack_f16(x[2] * s, x[3] * s), pack_f16(x[4] * s, x[5] * s),
+                          pack_f16(x[6] * s, x[7] * s)));
+        return e;
+    }
+    __device__ __forceinline__ void put_q(const LoadTile& x) {
+        constexpr int LPR = D / 8, RP = TC_LOAD / LPR;
+        const int l = tid % LPR;
+        const int rows = min(256, P.R - x.mt * 256);
+        const int upto = rows > 128 ? 256 : 128;
+        for (int r = tid / LPR; r < upto; r += RP) {
+            const int row = x.mt * 256 + r, n = row / P.G, h = x.h * P.G + row % P.G;
+            uint4 raw = make_uint4(0, 0, 0, 0);
+            if (r < rows)
+                raw = __ldg(reinterpret_cast<const uint4*>(P.q.p + x.b * P.q.b + n * P.q.n + h * P.q.h) + l);
+            bool nf;
+            const int e = put_row(base + Tc<D>::Q + (r / 128) * Tc<D>::TILE_B, r % 128, l, raw, nf, false);
+            if (l == 0) sh.rq[seg & 3][r] = exp2i(e) * P.scale;
+        }
+    }
+    // One of k and v of a tail tile: open tokens from the ring, then the nodes.
+    __device__ __forceinline__ void put_tail(const LoadTile& x, uint32_t dst, int which, float* a, float* b, float* c2) {
+        constexpr int LPR = D / 8, RP = TC_LOAD / LPR;
+        const int l = tid % LPR;
+        const Seq q = seq_of(P, x.b);
+        const char* ring = static_cast<const char*>(which ? P.c.v_open : P.c.k_open) +
+                           ((int64_t)q.slot * P.Hkv + x.h) * 2 * P.page * D * 2;
+        const sv_host::Rows& src = which ? P.v : P.k;
+        const int e0 = (x.t - q.nct) * TILE, keys = q.open + P.N;
+        for (int r = tid / LPR; r < TILE; r += RP) {
+            const int e = e0 + r;
+            uint4 raw = make_uint4(0, 0, 0, 0);
+            if (x.kind == 2 && e < q.open)
+                raw = *reinterpret_cast<const uint4*>(ring + ((int64_t)((q.full + e) % (2 * P.page)) * D + 8 * l) * 2);
+            else if (x.kind == 2 && e < keys)
+                raw = __ldg(reinterpret_cast<const uint4*>(src.p + x.b * src.b + (e - q.open) * src.n + x.h * src.h) + l);
+            bool nf;
+            const int p = put_row(dst, r, l, raw, nf, which == 1);
+            if (which == 1) {
+                if (nf) atomicOr(&sh.bad_v[seg & 3][e >> 5], 1u << (e & 31));
+                if (l == 0) {
+                    b[r] = (float)p;
+                    c2[r] = exp2i(-p);
+                }
+            } else if (l == 0) {
+                a[r] = exp2i(p);
+            }
+        }
+    }
+    // Hands tile number `gt` of the CTA to the tensor cores.
+    __device__ __forceinline__ void give(const LoadTile& x, int gt, const uint4 (&k)[NP], const uint4 (&v)[NP], float ks, float vs,
+                                         bool bad) {
+        const int st = gt & 1;
+        const uint32_t par = ((gt >> 1) & 1) ^ 1;
+        if (x.first) {
+            bar_wait(&sh.qe, (seg & 1) ^ 1, sh);
+            if (tid < 12) sh.bad_v[seg & 3][tid] = 0;
+            asm volatile("bar.sync 2, %0;" :: "n"(TC_LOAD) : "memory");
+            put_q(x);
+            arrive(&sh.qf);
+        }
+        if (bad) sh.bad_seg[seg & 3] = seg + 1;
+        float* m = sh.meta[gt & (TC_META - 1)][0];
+        bar_wait(&sh.ke[st], par, sh);
+        const uint32_t kd = base + Tc<D>::K + st * Tc<D>::TILE_B, vd = base + Tc<D>::V + st * Tc<D>::TILE_B;
+        if (x.kind == 1) {
+            if (tid < 8) {
+                m[tid] = ks;
+                m[TILE + tid] = log2f(vs);
+                m[2 * TILE + tid] = 1.f / vs;
+            }
+            put(kd, k);
+        } else {
+            // the value rows' scales belong to the same record: they are known before the keys are handed over
+            bar_wait(&sh.ve[st], par, sh);
+            put_tail(x, vd, 1, m, m + TILE, m + 2 * TILE);
+            put_tail(x, kd, 0, m, m + TILE, m + 2 * TILE);
+        }
+        arrive(&sh.kf[st]);
+        if (x.kind == 1) {
+            bar_wait(&sh.ve[st], par, sh);
+            put(vd, v);
+        }
+        arrive(&sh.vf[st]);
+    }
+};
+
+// A row's bits of a tile's keys, 32 per word.
+__device__ __forceinline__ void tile_mask(const Att& P, const Seg& g, int t, int n, uint32_t (&mk)[4]) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        if (t < g.q.nct) {
+            const int left = g.q.full - t * TILE - 32 * w;
+            mk[w] = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
+        } else {
+            mk[w] = g.q.len < 0 || g.q.bad ? 0u : tail_bits(P, g.b, n, g.q.open, (t - g.q.nct) * TILE + 32 * w);
+        }
+    }
+}
+
+// MODE 0: cached tile, all keys; 1: cached tile, masked; 2: tail (masked, scales per key).
+template <int MODE>
+__device__ __forceinline__ float tile_max(uint32_t s_col, const float* meta, float rq, const uint32_t (&mk)[4]) {
+    float mx = NEG_INF;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t r[32];
+        tc_ld32(s_col + 32 * c, r);
+        tc_wait_ld();
+        if (MODE > 0) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (!((mk[c] >> j) & 1)) r[j] = 0xff800000u;
+        }
+        if (MODE < 2) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float gm = __uint_as_float(r[16 * u]);
+#pragma unroll
+                for (int j = 1; j < 16; ++j) gm = fmaxf(gm, __uint_as_float(r[16 * u + j]));
+                mx = fmaxf(mx, fmaf(gm, fmaxf(meta[2 * c + u] * rq, 1.2e-38f), meta[TILE + 2 * c + u]));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                mx = fmaxf(mx, fmaf(__uint_as_float(r[j]), fmaxf(meta[32 * c + j] * rq, 1.2e-38f), meta[TILE + 32 * c + j]));
+        }
+    }
+    return mx;
+}
+template <int MODE>
+__device__ __forceinline__ float tile_probs(uint32_t s_col, const float* meta, float rq, const uint32_t (&mk)[4], float sub) {
+    float l = 0.f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t r[32], p[16];
+        tc_ld32(s_col + 32 * c, r);
+        tc_wait_ld();
+        if (MODE > 0) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (!((mk[c] >> j) & 1)) r[j] = 0xff800000u;
+        }
+        if (MODE < 2) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const float a = fmaxf(meta[2 * c + u] * rq, 1.2e-38f), b = meta[TILE + 2 * c + u] + sub;
+                float gs = 0.f;
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                    const float x = ex2(fmaf(__uint_as_float(r[16 * u + j]), a, b));
+                    const float y = ex2(fmaf(__uint_as_float(r[16 * u + j + 1]), a, b));
+                    gs += x + y;
+                    p[8 * u + j / 2] = pack_f16(x, y);
+                }
+                l = fmaf(gs, meta[2 * TILE + 2 * c + u], l);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+                const int i = 32 * c + j;
+                const float x = ex2(fmaf(__uint_as_float(r[j]), fmaxf(meta[i] * rq, 1.2e-38f), meta[TILE + i] + sub));
+                const float y = ex2(fmaf(__uint_as_float(r[j + 1]), fmaxf(meta[i + 1] * rq, 1.2e-38f), meta[TILE + i + 1] + sub));
+                l = fmaf(x, meta[2 * TILE + i], l);
+                l = fmaf(y, meta[2 * TILE + i + 1], l);
+                p[j / 2] = pack_f16(x, y);
+            }
+        }
+        tc_st16(s_col + 16 * c, p);      // columns that have been read
+    }
+    return l;
+}
+
+// What a CTA leaves of an item that it does not hold whole.
+template <int D>
+__device__ __forceinline__ float* partial_of(const Att& P, int cta, int slot) {
+    return P.partial + ((int64_t)cta * 2 + slot) * (min(P.R, 256) * (int64_t)(D + 2));
+}
+
+__device__ __forceinline__ int rows_of(const Att& P) { return min(P.R, 256); }
+
+// Row r of the partial results of a cut item, put together by a warp and written out.
+template <int D>
+__device__ void merge_row(const Att& P, int r, int rows, int c0, int slot0, int parts, int lane, char* out, float* lse) {
+    float M = NEG_INF;
+    for (int i = lane; i < parts; i += 32)
+        M = fmaxf(M, __ldcg(partial_of<D>(P, c0 + i, i == 0 ? slot0 : 0) + (int64_t)rows * D + r));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+    const float base = M == NEG_INF ? 0.f : M;
+    constexpr int E = D / 32;
+    float acc[E] = {}, l = 0.f;
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+        float w = 0.f, wl = 0.f;
+        if (i0 + lane < parts) {
+            const float* p = partial_of<D>(P, c0 + i0 + lane, i0 + lane == 0 ? slot0 : 0) + (int64_t)rows * D;
+            w = ex2(__ldcg(p + r) - base);
+            wl = w * __ldcg(p + rows + r);
+        }
+        l += wl;
+        const int n = min(32, parts - i0);
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float wi = __shfl_sync(FULL, w, i);
+            const float* p = partial_of<D>(P, c0 + i0 + i, i0 + i == 0 ? slot0 : 0) + (int64_t)r * D + lane * E;
+            if constexpr (E == 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
+                acc[0] = fmaf(wi, x.x, acc[0]); acc[1] = fmaf(wi, x.y, acc[1]);
+                acc[2] = fmaf(wi, x.z, acc[2]); acc[3] = fmaf(wi, x.w, acc[3]);
+            } else {
+                const float2 x = __ldcg(reinterpret_cast<const float2*>(p));
+                acc[0] = fmaf(wi, x.x, acc[0]); acc[1] = fmaf(wi, x.y, acc[1]);
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(FULL, l, o);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if constexpr (E == 4)
+        reinterpret_cast<uint2*>(out)[lane] = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+    else
+        reinterpret_cast<uint32_t*>(out)[lane] = pack_bf16(acc[0] * inv, acc[1] * inv);
+    if (lse && lane == 0) *lse = l == 0.f ? NEG_INF : (base + log2f(l)) * LN2;
+}
+
+template <int D>
+__global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P) {
+    extern __shared__ unsigned char raw_smem[];
+    const uint32_t base = (smem_u32(raw_smem) + 1023u) & ~1023u;
+    TcShared& sh = *reinterpret_cast<TcShared*>(raw_smem + (base - smem_u32(raw_smem)) + Tc<D>::END);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Stretch st = find_stretch<TC_BT>(P);
+    if (st.lo >= st.hi) return;
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&sh.kf[i], TC_LOAD / 32);
+            bar_init(&sh.vf[i], TC_LOAD / 32);
+            bar_init(&sh.ke[i], 1);
+            bar_init(&sh.ve[i], 1);
+            bar_init(&sh.sf[i], 1);
+            bar_init(&sh.pf[i], 128);
+            bar_init(&sh.pv[i], 1);
+            sh.last[i] = 0;
+        }
+        for (int i = 0; i < 4; ++i) sh.bad_seg[i] = 0;
+        bar_init(&sh.qf, TC_LOAD / 32);
+        bar_init(&sh.qe, 1);
+        bar_init(&sh.drain, 1);
+        sh.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == TC_BT / 32 - 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(smem_u32(&sh.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tc_before();
+    }
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
+
+    if (warp >= TC_SOFTMAX / 32 && warp < TC_BT / 32 - 1) {
+        // ---- loads: the next tile's bytes are on their way while this one is converted
+        TcLoader<D> ld(P, sh, base, tid - TC_SOFTMAX);
+        constexpr int NP = TcLoader<D>::NP;
+        uint4 k0[NP], v0[NP], k1[NP], v1[NP];
+        float ks0, vs0, ks1, vs1;
+        bool bad0, bad1;
+        ld.begin(st);
+        ld.seg = -1;
+        LoadTile x0 = ld.next(), x1;
+        ld.fetch(x0, k0, v0, ks0, vs0, bad0);
+        for (int gt = 0; x0.kind; gt += 2) {
+            x1 = ld.next();
+            ld.fetch(x1, k1, v1, ks1, vs1, bad1);
+            if (x0.first) ++ld.seg;
+            ld.give(x0, gt, k0, v0, ks0, vs0, bad0);
+            if (!x1.kind) break;
+            x0 = ld.next();
+            ld.fetch(x0, k0, v0, ks0, vs0, bad0);
+            if (x1.first) ++ld.seg;
+            ld.give(x1, gt + 1, k1, v1, ks1, vs1, bad1);
+        }
+    } else if (warp == TC_BT / 32 - 1) {
+        // ---- matrix instructions
+        if (lane == 0) {
+            SegIter it;
+            Seg g;
+            it.begin(P, st);
+            uint32_t cnt[2] = {0, 0};
+            int g0 = 0;
+            constexpr uint32_t ID_QK = tc_idesc(TILE, false), ID_PV = tc_idesc(D, true);
+            for (int seg = 0; it.next(P, g); ++seg) {
+                const bool dual = P.R - g.mt * 256 > 128;
+                const int nt = g.t1 - g.t0;
+                int left = dual ? 2 * nt : nt;            // score products still to issue
+                bar_wait(&sh.qf, seg & 1, sh);
+                tc_after();
+                auto scores = [&](int i, int tl) {
+                    const int gt = g0 + tl, s = gt & 1;
+                    bar_wait(&sh.kf[s], (gt >> 1) & 1, sh);
+                    tc_after();
+                    const uint32_t q = base + Tc<D>::Q + (dual ? i : 0) * Tc<D>::TILE_B, k = base + Tc<D>::K + s * Tc<D>::TILE_B;
+#pragma unroll
+                    for (int u = 0; u < D / 16; ++u) {
+                        const uint32_t off = (u / 4) * Tc<D>::HALF + (u % 4) * 32;
+                        tc_mma_ss(tmem + i * TILE, tc_desc(q + off, 16), tc_desc(k + off, 16), ID_QK, u > 0);
+                    }
+                    tc_commit(&sh.sf[i]);
+                    if (!dual || i == 1) tc_commit(&sh.ke[s]);
+                    if (--left == 0) tc_commit(&sh.qe);
+                };
+                auto tile = [&](int i, int step) { return dual ? step : 2 * step + i; };
+                for (int i = 0; i < 2; ++i)
+                    if (tile(i, 0) < nt) scores(i, tile(i, 0));
+                for (int step = 0; tile(0, step) < nt; ++step) {
+                    for (int i = 0; i < 2; ++i) {
+                        const int tl = tile(i, step);
+                        if (tl >= nt) continue;
+                        const int gt = g0 + tl, s = gt & 1;
+                        bar_wait(&sh.vf[s], (gt >> 1) & 1, sh);
+                        bar_wait(&sh.pf[i], cnt[i] & 1, sh);
+                        tc_after();
+                        const uint32_t v = base + Tc<D>::V + s * Tc<D>::TILE_B;
+#pragma unroll
+                        for (int u = 0; u < TILE / 16; ++u)
+                            tc_mma_ts(tmem + Tc<D>::O_COL + i * D, tmem + i * TILE + u * 8, tc_desc(v + u * 2048, Tc<D>::HALF),
+                                      ID_PV, step > 0 || u > 0);
+                        ++cnt[i];
+                        if (!dual || i == 1) tc_commit(&sh.ve[s]);
+                        if (tile(i, step + 1) < nt) scores(i, tile(i, step + 1));
+                        else tc_commit(&sh.pv[i]);
+                    }
+                }
+                g0 += nt;
+            }
+            tc_commit(&sh.drain);
+            // also after a wait that gave up: nothing runs on when the tensor memory is freed
+            if (!bar_try(&sh.drain, 0)) bar_wait_slow(&sh.drain, 0, nullptr);
+        }
+        __syncwarp();
+    } else {
+        // ---- softmax of stream i; thread = row
+        const int i = warp / 4, r = tid & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;               // 32 lanes per warp, lane index in bits 16-31
+        const uint32_t s_col = tmem + lanes + i * TILE, o_col = tmem + lanes + Tc<D>::O_COL;
+        SegIter it;
+        Seg g;
+        it.begin(P, st);
+        uint32_t cnt = 0, pvc = 0;
+        int g0 = 0;
+        for (int seg = 0; it.next(P, g); ++seg) {
+            const int rows = min(256, P.R - g.mt * 256);
+            const bool dual = rows > 128;
+            const int nt = g.t1 - g.t0;
+            const int ri = dual ? i * 128 + r : r;                        // row of the item
+            const int row = g.mt * 256 + min(ri, rows - 1), n = row / P.G, head = g.h * P.G + row % P.G;
+            float m = NEG_INF, l = 0.f, rq = 0.f;
+            bool any = false;
+            for (int tl = dual ? 0 : i; tl < nt; tl += dual ? 1 : 2) {
+                const int gt = g0 + tl, t = g.t0 + tl;
+                const float* meta = sh.meta[gt & (TC_META - 1)][0];
+                bar_wait(&sh.sf[i], cnt & 1, sh);
+                tc_after();
+                if (!any) rq = sh.rq[seg & 3][ri];
+                const int mode = t >= g.q.nct ? 2 : (t + 1) * TILE > g.q.full ? 1 : 0;
+                uint32_t mk[4] = {};
+                float mx;
+                if (mode == 0) {
+                    mx = tile_max<0>(s_col, meta, rq, mk);
+                } else {
+                    tile_mask(P, g, t, n, mk);
+                    mx = mode == 1 ? tile_max<1>(s_col, meta, rq, mk) : tile_max<2>(s_col, meta, rq, mk);
+                }
+                if (!any) {
+                    m = mx;
+                } else if (__any_sync(FULL, mx > m + M_SLACK)) {
+                    // the product before this tile's scores has ended: O can be rescaled
+                    const float m2 = fmaxf(m, mx);
+                    const float f = m2 == NEG_INF ? 1.f : ex2(m - m2);
+                    l *= f;
+                    m = m2;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tc_ld32(o_col + i * D + c, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                        tc_st32(o_col + i * D + c, o);
+                    }
+                }
+                any = true;
+                const float sub = P_BIAS - (m == NEG_INF ? 0.f : m);
+                l += mode == 0 ? tile_probs<0>(s_col, meta, rq, mk, sub)
+                     : mode == 1 ? tile_probs<1>(s_col, meta, rq, mk, sub) : tile_probs<2>(s_col, meta, rq, mk, sub);
+                tc_wait_st();
+                tc_before();
+                bar_arrive(&sh.pf[i]);
+                ++cnt;
+            }
+            if (any) {
+                bar_wait(&sh.pv[i], pvc & 1, sh);
+                ++pvc;
+                tc_after();
+            }
+            // ---- the segment's rows: whole items are written out, parts go to the workspace
+            float f[2] = {1.f, 0.f};                                      // factors of the streams' sums
+            int c_lo = 0, c_hi = D;
+            if (!dual) {
+                sh.xm[i][r] = m;
+                sh.xl[i][r] = l;
+                tc_before();
+                asm volatile("bar.sync 1, %0;" :: "n"(TC_SOFTMAX) : "memory");
+                tc_after();
+                const float m0 = sh.xm[0][r], m1 = sh.xm[1][r], mm = fmaxf(m0, m1);
+                f[0] = m0 == NEG_INF ? (mm == NEG_INF ? 1.f : 0.f) : ex2(m0 - mm);
+                f[1] = nt < 2 ? 0.f : m1 == NEG_INF ? (mm == NEG_INF ? 1.f : 0.f) : ex2(m1 - mm);
+                l = sh.xl[0][r] * f[0] + (nt < 2 ? 0.f : sh.xl[1][r] * f[1]);
+                m = mm;
+                c_lo = i * (D / 2);
+                c_hi = c_lo + D / 2;
+            }
+            const bool whole = g.t0 == 0 && g.t1 == g.q.ntiles;
+            const bool nan = g.q.bad || *reinterpret_cast<volatile int*>(&sh.bad_seg[seg & 3]) == seg + 1;
+            if (nan && r == 0) atomicOr(P.status, 1u << SPEC_ERR_DEVICE_INPUT);
+            uint32_t bad_v = 0;
+            if (g.t1 > g.q.nct) {
+#pragma unroll
+                for (int w = 0; w < 12; ++w) bad_v |= sh.bad_v[seg & 3][w];
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const int64_t orow = ((int64_t)g.b * P.N + n) * P.Hq + head;
+            const int slot = g.item_lo + g.t0 == st.lo ? 0 : 1;
+            float* part = partial_of<D>(P, blockIdx.x, slot);
+            const float quiet = __int_as_float(0x7fffffff);
+#pragma unroll 1
+            for (int c = c_lo; c < c_hi; c += 32) {
+                uint32_t o[32];
+                tc_ld32(o_col + (dual ? i * D : 0) + c, o);
+                tc_wait_ld();
+                if (!dual) {
+                    if (nt > 1) {
+                        uint32_t o2[32];
+                        tc_ld32(o_col + D + c, o2);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            o[j] = __float_as_uint(__uint_as_float(o[j]) * f[0] + __uint_as_float(o2[j]) * f[1]);
+                    }
+                }
+                if (bad_v) {                                              // values that could not enter the product
+                    for (int w = 0; w < 12; ++w) {
+                        uint32_t hit = sh.bad_v[seg & 3][w];
+                        if (hit) hit &= tail_bits(P, g.b, n, g.q.open, 32 * w);
+                        for (; hit; hit &= hit - 1) {
+                            const int e = 32 * w + __ffs(hit) - 1;
+                            const char* src = e < g.q.open
+                                ? static_cast<const char*>(P.c.v_open) +
+                                      (((int64_t)g.q.slot * P.Hkv + g.h) * 2 * P.page + (g.q.full + e) % (2 * P.page)) * D * 2
+                                : P.v.p + g.b * P.v.b + (e - g.q.open) * P.v.n + g.h * P.v.h;
+                            const __nv_bfloat16* vv = reinterpret_cast<const __nv_bfloat16*>(src) + c;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                const float x = __bfloat162float(vv[j]);
+                                if (!(fabsf(x) <= 3.402823466e38f)) o[j] = __float_as_uint(__uint_as_float(o[j]) + x);
+                            }
+                        }
+                    }
+                }
+                if (ri < rows) {
+                    if (whole) {
+                        uint4* dst = reinterpret_cast<uint4*>(P.out + (orow * D + c) * 2);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) {
+                            float x[8];
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) x[u] = nan ? quiet : __uint_as_float(o[j + u]) * inv;
+                            dst[j / 8] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                                                    pack_bf16(x[6], x[7]));
+                        }
+                    } else {
+                        float4* dst = reinterpret_cast<float4*>(part + (int64_t)ri * D + c);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            dst[j / 4] = nan ? make_float4(quiet, quiet, quiet, quiet)
+                                             : make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]),
+                                                           __uint_as_float(o[j + 2]), __uint_as_float(o[j + 3]));
+                    }
+                }
+            }
+            const bool speaks = ri < rows && (dual || i == 0);
+            if (whole) {
+                if (speaks && P.lse) P.lse[orow] = nan ? quiet : l == 0.f ? NEG_INF : (m - P_BIAS + log2f(l)) * LN2;
+            } else {
+                if (speaks) {
+                    part[(int64_t)rows_of(P) * D + ri] = m == NEG_INF ? NEG_INF : m - P_BIAS;
+                    part[(int64_t)rows_of(P) * D + rows_of(P) + ri] = nan ? quiet : l;
+                }
+                const int c0 = cta_of(g.item_lo, st.total, st.ctas);
+                const int c1 = cta_of(g.item_lo + g.q.ntiles - 1, st.total, st.ctas);
+                const int slot0 = stretch_at(st.total, c0, st.ctas) == g.item_lo ? 0 : 1;
+                // the last of the item's CTAs (for two streams: the last of each) puts it together
+                __threadfence();
+                if (dual) asm volatile("bar.sync %0, 128;" :: "r"(3 + i) : "memory");
+                else asm volatile("bar.sync 1, %0;" :: "n"(TC_SOFTMAX) : "memory");
+                if (r == 0 && (dual || i == 0)) {
+                    const unsigned got = atomicAdd(P.item_cnt + 2 * c0 + (dual ? i : 0), 1u);
+                    const int is_last = got == (unsigned)(c1 - c0);
+                    if (is_last) P.item_cnt[2 * c0 + (dual ? i : 0)] = 0;
+                    __threadfence();
+                    sh.last[dual ? i : 0] = is_last;
+                }
+                if (dual) asm volatile("bar.sync %0, 128;" :: "r"(3 + i) : "memory");
+                else asm volatile("bar.sync 1, %0;" :: "n"(TC_SOFTMAX) : "memory");
+                if (*reinterpret_cast<volatile int*>(&sh.last[dual ? i : 0])) {
+                    __threadfence();
+                    const int first = dual ? i * 128 + (warp & 3) : warp, upto = dual ? min(rows, i * 128 + 128) : rows;
+                    for (int q = first; q < upto; q += dual ? 4 : 8) {
+                        const int row2 = g.mt * 256 + q;
+                        const int64_t o2 = ((int64_t)g.b * P.N + row2 / P.G) * P.Hq + g.h * P.G + row2 % P.G;
+                        merge_row<D>(P, q, rows_of(P), c0, slot0, c1 - c0 + 1, lane, P.out + o2 * D * 2,
+                                     P.lse ? P.lse + o2 : nullptr);
+                    }
+                }
+            }
+            // the next segment's products may write O again once every reader is through
+            tc_before();
+            if (!dual) asm volatile("bar.sync 1, %0;" :: "n"(TC_SOFTMAX) : "memory");
+            g0 += nt;
+        }
+    }
+    __syncthreads();
+    if (warp == TC_BT / 32 - 1) {
+        tc_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tmem));
+        if (lane == 0 && sh.abort) atomicOr(P.status, 1u << SPEC_ERR_TIMEOUT);
+    }
+}
 
 __device__ __forceinline__ float e4m3_f32(uint8_t v) {
     uint32_t h;
@@ -124,13 +1143,29 @@ __global__ void __launch_bounds__(128) k_attention_rows(const Att P) {
 
 using sv_host::fail;
 
+namespace {
+
+constexpr int ATT_CTAS = 148;             // CTAs at most: one per SM
+
+template <int D>
+spec_status launch_tc(const Att& P, cudaStream_t st) {
+    const cudaError_t e = cudaFuncSetAttribute(k_attention_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tc_smem<D>());
+    if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "k_attention_tc: %s", cudaGetErrorString(e));
+    const int ctas = sv_host::num_sms() < ATT_CTAS ? sv_host::num_sms() : ATT_CTAS;
+    k_attention_tc<D><<<ctas, TC_BT, tc_smem<D>(), st>>>(P);
+    return sv_host::launched("k_attention_tc");
+}
+
+}  // namespace
+
 extern "C" {
 
 size_t spec_cache_workspace_bytes(int B, int N, int q_heads, int head_dim) {
     if (B < 0 || B > sv_host::CACHE_MAX_B || N < 1 || N > SPEC_MAX_NODES || q_heads < 1 || q_heads > SPEC_MAX_HEADS ||
         (head_dim != 64 && head_dim != 128))
         return 0;
-    return sv_host::CACHE_WS_PARTIAL;
+    const size_t rows = (size_t)N * q_heads < 256 ? (size_t)N * q_heads : 256;
+    return sv_host::CACHE_WS_PARTIAL + sv_host::align256(sizeof(float) * 2 * ATT_CTAS * rows * (head_dim + 2));
 }
 
 spec_status spec_tree_attention(int B, int N, int q_heads, const spec_kv_cache* cache,
@@ -158,16 +1193,22 @@ spec_status spec_tree_attention(int B, int N, int q_heads, const spec_kv_cache* 
     if (((uintptr_t)out & 15u) != 0) return fail(SPEC_ERR_INVALID_ARG, "out not 16-byte aligned");
     if (spec_status s = sv_host::check_cache_ws(workspace, workspace_bytes, spec_cache_workspace_bytes(B, N, q_heads, D)))
         return s;
-    P.B = B; P.N = N; P.Hq = q_heads; P.Hkv = cache->kv_heads; P.G = q_heads / cache->kv_heads; P.D = D;
+    P.B = B; P.N = N; P.Hq = q_heads; P.Hkv = cache->kv_heads; P.G = q_heads / cache->kv_heads;
+    P.R = N * P.G;
+    P.mtiles = (P.R + 255) / 256;
     P.page = cache->page_size;
     P.c = *cache;
     P.anc = reinterpret_cast<const uint32_t*>(ancestors);
     P.scale = (float)((double)scale * 1.4426950408889634073599);
     P.out = static_cast<char*>(out);
     P.lse = lse;
-    P.status = static_cast<unsigned*>(workspace);
+    char* ws = static_cast<char*>(workspace);
+    P.status = reinterpret_cast<unsigned*>(ws + sv_host::CACHE_WS_STATUS);
+    P.item_cnt = reinterpret_cast<unsigned*>(ws + sv_host::CACHE_WS_ITEM);
+    P.partial = reinterpret_cast<float*>(ws + sv_host::CACHE_WS_PARTIAL);
     const int64_t rows = (int64_t)B * N * q_heads;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (P.R > 16) return D == 64 ? launch_tc<64>(P, st) : launch_tc<128>(P, st);
     if (D == 64) k_attention_rows<64><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(P);
     else k_attention_rows<128><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(P);
     return sv_host::launched("k_attention_rows");

@@ -117,9 +117,17 @@ class Cache:
         return self.rows[which][b][n:]
 
 
-def attention(q, k, v, keys, values, mask, scale):
-    """One sequence: q [N, Hq, D], nodes k/v [N, Hkv, D], cached keys/values [L, Hkv, D], mask [N, N].
-    All f64.  Returns out, lse, sum p |v|, max over keys of scale * sum |q| |k|."""
+def row_scale(x):
+    """[.., D] -> [..]: the power of two at or below the row's largest finite magnitude (1 for zeros)."""
+    a = torch.where(torch.isfinite(x), x, torch.zeros_like(x)).abs().amax(-1)
+    m, e = torch.frexp(a)
+    return torch.where(a > 0, torch.ldexp(torch.ones_like(a), e - 1), torch.ones_like(a))
+
+
+def attention(q, k, v, keys, values, mask, scale, vscale):
+    """One sequence: q [N, Hq, D], nodes k/v [N, Hkv, D], cached keys/values [L, Hkv, D], mask [N, N],
+    vscale [L, Hkv] the scales of the cached values.  All f64.  Returns out, lse, sum p |v|, max over
+    keys of scale * sum |q| |k|, and max p s * sum |v| / s over the keys' value scales s."""
     N, Hq, D = q.shape
     G = Hq // k.shape[1]
     K = torch.cat((keys, k)).repeat_interleave(G, 1)          # [T, Hq, D]
@@ -136,7 +144,11 @@ def attention(q, k, v, keys, values, mask, scale):
     w = torch.where(total > 0, p / total, torch.zeros_like(p))
     # a masked key's value takes no part, whatever it holds
     out = torch.einsum("nht,thd->nhd", w, torch.nan_to_num(V, 0, 0, 0))
-    return out, (torch.log(total) + top)[..., 0], torch.einsum("nht,thd->nhd", w, torch.nan_to_num(V, 0, 0, 0).abs()), mag
+    vabs = torch.nan_to_num(V, 0, 0, 0).abs()
+    S = torch.cat((vscale, row_scale(v))).repeat_interleave(G, 1)     # [T, Hq]
+    lead = (w * S.T).amax(-1)                                         # [N, Hq]
+    small = lead[..., None] * torch.einsum("nht,thd->nhd", see.double(), vabs / S[..., None])
+    return out, (torch.log(total) + top)[..., 0], torch.einsum("nht,thd->nhd", w, vabs), mag, small
 
 
 def inv_freq(rot, base=1e6):

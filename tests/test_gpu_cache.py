@@ -8,7 +8,11 @@ the rotation's sum bring the total below 2^-19 of |a| + |b|.  Attention: a score
 a sum of D + 8 f32 products or less, so it is off by at most
 (D + 8) 2^-23 scale sum|q||k| (twice the half step, for truncating sums); the probabilities are rounded to f16
 (2^-11) before the second product; the output's error is at most that relative
-error of each probability times sum p|v|, plus the final rounding.
+error of each probability times sum p|v|, plus the final rounding.  f16 has no
+steps below 2^-24: with the keys' value scales s_j, the kernel rounds
+P_j = 2^11 p_j s_j / max(p s) (or more), so below f16's normal numbers p_j s_j is
+off by up to 2^-25 / 2^11 of max(p s); the sum over keys of that times
+|v_j| / s_j is 2^-36 max(p s) sum |v| / s.
 """
 import math
 
@@ -348,17 +352,18 @@ def check_attention(r, lengths, q, k, v, mask, out, lse, scale):
         if lengths[b] < 0:
             assert (out[b] == 0).all() and (lse[b] == -math.inf).all()
             continue
-        side = []
+        side, vscale = [], None
         for which in range(2):
             e, s = r.blocks(b, which)
+            vscale = torch.cat((s.repeat_interleave(r.page, 0), ref.row_scale(r.open_rows(b, which).double())))
             full = (e.view(F8).double() * s[..., None, None]).transpose(1, 2).reshape(-1, r.H, r.D)
             side.append(torch.cat((full, r.open_rows(b, which).double())))
-        e, el, pv, mag = ref.attention(q[b].double(), k[b].double(), v[b].double(), *side, mask[b], scale)
+        e, el, pv, mag, small = ref.attention(q[b].double(), k[b].double(), v[b].double(), *side, mask[b], scale, vscale)
         ds = (r.D + 8) * 2.0 ** -23 * mag
         # the probabilities' own rounding, the scores' (in numerator and sum), the exponentials' (2^-21)
         rel = 2.0 ** -11 + 2 * ds + 2.0 ** -20
-        assert ((out[b] - e).abs() <= e.abs() * 2.0 ** -8 + pv * rel[..., None] + 1e-38).all(), \
-            float(((out[b] - e).abs() / (e.abs() * 2.0 ** -8 + pv * rel[..., None] + 1e-38)).max())
+        tol = e.abs() * 2.0 ** -8 + pv * rel[..., None] + small * 2.0 ** -36 + 1e-38
+        assert ((out[b] - e).abs() <= tol).all(), float(((out[b] - e).abs() / tol).max())
         empty = el == -math.inf
         assert torch.equal(lse[b] == -math.inf, empty)
         assert ((lse[b] - el)[~empty].abs() <= (ds + 2.0 ** -20 * (1 + el.abs()))[~empty]).all()
@@ -372,6 +377,9 @@ ATT = [  # B, N, Hq, Hkv, D, page, lengths
     (2, 32, 8, 2, 64, 128, [1023, 1]), (1, 64, 5, 1, 64, 16, [100]), (1, 256, 2, 1, 128, 64, [130]),
     (1, 129, 2, 2, 128, 128, [127]), (1, 31, 64, 2, 128, 64, [333]), (3, 43, 3, 1, 128, 16, [0, 47, 1]),
     (1, 2, 64, 1, 128, 16, [2050]), (1, 1, 129, 1, 64, 16, [40]), (2, 256, 8, 4, 64, 32, [65, 31]),
+    (40, 6, 64, 8, 128, 16, [(i * 397) % 1501 for i in range(40)]),      # many tiles and items per CTA
+    (24, 33, 64, 8, 128, 32, [(i * 211) % 900 for i in range(24)]), (20, 32, 32, 8, 64, 128, [(i * 533) % 2000 for i in range(20)]),
+    (48, 2, 40, 8, 64, 64, [(i * 97) % 700 - 20 for i in range(48)]), (60, 1, 32, 8, 128, 16, [(i * 397) % 3001 for i in range(60)]),
     (9, 5, 12, 4, 128, 16, [5, 4000, 17, 1, 90, 2222, 0, 64, 800])]
 
 
