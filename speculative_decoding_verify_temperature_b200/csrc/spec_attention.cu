@@ -1,6 +1,9 @@
 // spec_attention.cu -- attention of the nodes of draft trees over the paged
 // 8-bit cache and each other.
+#include <cuda.h>
 #include <math.h>
+
+#include <atomic>
 
 #include "cache_device.cuh"
 #include "internal.h"
@@ -14,7 +17,7 @@ constexpr float NEG_INF = -INFINITY;
 constexpr float LN2 = 0.69314718055994530942f;
 
 struct Att {
-    int B, N, Hq, Hkv, G, page, R;        // R = N * G rows of a kv head
+    int B, N, Hq, Hkv, G, page, pshift, R;   // page = 1 << pshift; R = N * G rows of a kv head
     int mtiles;                           // items per (sequence, kv head)
     sv_host::Rows q, k, v;
     spec_kv_cache c;
@@ -23,8 +26,14 @@ struct Att {
     char* out;
     float* lse;
     unsigned* status;
-    unsigned* item_cnt;                   // [gridDim.x] arrivals at an item that several CTAs share
+    struct Cut* cut;                      // [gridDim.x] the item that a CTA begins and does not end
     float* partial;                       // [gridDim.x][2][rows of an item][D + 2]
+};
+
+// An item whose tiles several CTAs share: they leave partial results, CTA c its
+// first tiles in slot `slot0` of its workspace and the CTAs after it theirs in slot 0.
+struct Cut {
+    int b, h, mt, parts, slot0;           // parts = 0: none
 };
 
 // ----------------------------------------------------------------------------- the work and its split
@@ -44,7 +53,7 @@ __device__ __forceinline__ Seq seq_of(const Att& P, int b) {
     const int64_t most = (int64_t)P.c.max_pages * P.page + P.page - 1;
     s.bad = s.len >= 0 && (s.len > most || s.len >= SPEC_MAX_CACHE_LEN || s.slot < 0 || s.slot >= P.c.num_slots);
     const bool live = s.len >= 0 && !s.bad;
-    s.full = live ? s.len / P.page * P.page : 0;
+    s.full = live ? s.len >> P.pshift << P.pshift : 0;
     s.open = live ? s.len - s.full : 0;
     s.nct = (s.full + TILE - 1) / TILE;
     s.ntiles = s.nct + (s.open + P.N + TILE - 1) / TILE;
@@ -54,7 +63,7 @@ __device__ __forceinline__ Seq seq_of(const Att& P, int b) {
 
 // The tiles of all items (sequence, kv head, rows), in that order, are one line;
 // every CTA takes an equal stretch of it, whatever the lengths are.  An item
-// that a stretch border cuts is put together by the last of its CTAs.
+// that a stretch border cuts leaves partial results, which a second kernel puts together.
 struct Stretch {
     long long lo, hi, total;              // tiles
     int ctas;                             // CTAs that share the line: each has at least one tile
@@ -197,38 +206,50 @@ __device__ __forceinline__ uint32_t tail_bits(const Att& P, int b, int n, int op
 
 // ----------------------------------------------------------------------------- tensor-core kernel (tcgen05)
 
-// Roles of the CTA's warps: 0-3 and 4-7 the softmax of one stream each, 8-15 the
-// loads, 16 the matrix instructions (one thread).
+// Roles of the CTA's warps: 0-3 and 4-7 the softmax of one stream each, 8-11 make
+// operands (f16 values from e4m3 bytes, queries, the tail), 12 issues the matrix
+// instructions (one thread), 13 copies pages to shared memory, 14 gathers the
+// pages' scales, 15 nothing.
 //
 // An item holds up to 256 rows.  With more than 128 the two streams are its two
 // halves and both take every tile; with 128 or fewer both streams hold the same
 // rows and take the tiles in turn, and their sums are joined at the end.  While
 // one stream's softmax works on its scores, the tensor cores work for the other.
 //
-//   S_i = Q_i K^T    f16 operands from shared memory, f32 in tensor memory
+//   S_i = Q_i K^T    e4m3 operands, f32 in tensor memory
 //   P_i              f16, over S_i's columns
-//   O_i += P_i V     P from tensor memory, V from shared memory
+//   O_i += P_i V     f16, P from tensor memory, V from shared memory
 //
-// The f16 operands are exact: an e4m3 value is an f16 value, and a bf16 row of q
-// or of the tail's k and v is divided by a power of two that brings its largest
-// magnitude to [1, 2) (what f16 then cannot hold is below 2^-25 of it).  The
-// scales come back in f32: with a_j the key's scale times the row's and s_v,j
-// the value's, x_j = S_j a_j is the score in base 2 and
+// Keys go to the tensor cores as the cache holds them: a swizzled tensor copy
+// brings a page's bytes to where the matrix instruction reads them.  The other
+// side is split: a bf16 row of q, divided by a power of two that brings its
+// largest magnitude to [128, 256), is the sum of two e4m3 rows (four bits of
+// its eight each; an element below 2^-9 of the largest is rounded at 2^-18 of it), so a score is
+// two products.  The tail's keys are split the same way, four products.
+// Values are turned into f16 (an e4m3 value times 2^-8 is an f16 value; the
+// tail's rows are divided by a power of two that brings them to [1, 2)).
+//
+// The scales come back in f32: with a_j the key's scale times the row's and
+// s_v,j the value's, x_j = S_j a_j is the score in base 2 and
 //   w_j = x_j + log2 s_v,j,  M = max w_j,  P_j = 2^(w_j - M),
 //   O = sum P_j v_j,  l = sum P_j / s_v,j,  out = O / l.
 // M follows the weight with which a value enters O, so that f16 holds the
 // leading P whatever the blocks' scales are.  O is rescaled only when M grows by
 // more than 2^4; P_BIAS lifts P to at most 2^15, so that f16's smallest step is
 // 2^-35 of the leading one.
-constexpr int TC_SOFTMAX = 256, TC_LOAD = 256, TC_BT = TC_SOFTMAX + TC_LOAD + 32;
+constexpr int TC_SOFTMAX = 256, TC_CONV = 128, TC_BT = 512;
+constexpr int TC_W_CONV = 8, TC_W_MMA = 12, TC_W_COPY = 13, TC_W_SCALE = 14;
 constexpr int TC_META = 4;                // tiles whose scales are kept
 constexpr float P_BIAS = 11.f, M_SLACK = 4.f;
 
 template <int D> struct Tc {
     static constexpr int HALVES = D / 64;                 // 128-byte rows of 64 f16
     static constexpr uint32_t HALF = 128 * 128;           // 128 such rows
-    static constexpr uint32_t TILE_B = HALVES * HALF;     // an operand tile
-    static constexpr uint32_t Q = 0, K = 2 * TILE_B, V = 4 * TILE_B, END = 6 * TILE_B;
+    static constexpr uint32_t V_B = HALVES * HALF;        // f16 values of a tile
+    static constexpr uint32_t RAW_B = TILE * D;           // e4m3 rows of a tile
+    static constexpr uint32_t Q_B = TILE * 2 * D;         // both e4m3 rows of 128 queries
+    static constexpr int KR = D == 128 ? 3 : 6, VR = D == 128 ? 2 : 4;   // units of keys, of value bytes
+    static constexpr uint32_t Q = 0, K = Q + 2 * Q_B, RAW = K + KR * RAW_B, V = RAW + VR * RAW_B, END = V + 2 * V_B;
     static constexpr int O_COL = 256;                     // tensor memory columns: S0 S1 (128 each), O0 O1 (D each)
 };
 struct TcShared {
@@ -236,11 +257,10 @@ struct TcShared {
     float rq[4][256];                                     // per row: its power of two * scale * log2(e)
     float xm[2][TILE], xl[2][TILE];                       // M and l of the streams that are joined
     uint32_t bad_v[4][12];                                // tail keys whose value is not finite
-    int bad_seg[4];                                       // 1 + segment that met a bad page
-    uint64_t kf[2], ke[2], vf[2], ve[2], sf[2], pf[2], pv[2], qf, qe, drain;
+    int bad_seg[8];                                       // 1 + segment that met a bad page
+    uint64_t kf[6], ke[6], rf[4], re[4], vf[2], ve[2], mf[TC_META], me[TC_META], sf[2], pf[2], pv[2], qf, qe, drain;
     uint32_t tmem;
     int abort;
-    int last[2];
 };
 // 1 KB of alignment slack; at least what keeps a second CTA, and its tensor memory, off the SM
 template <int D> constexpr size_t tc_smem() {
@@ -259,12 +279,45 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// Four e4m3 bytes to two pairs of f16 (exact).
-__device__ __forceinline__ uint2 e4m3_f16(uint32_t w) {
+// Four e4m3 bytes to f16 times 2^-8, the bytes in the order (0, 2), (1, 3): the exponent and mantissa bits move as
+// they are, subnormals included.  (The conversion instruction was measured at 6000 cycles a tile, this at 0000.)  A
+// NaN byte would read as 480: bit 7 of a byte of `nan` tells.
+__device__ __forceinline__ uint2 e4m3_f16(uint32_t w, uint32_t& nan) {
+    nan |= (w & 0x7f7f7f7fu) + 0x01010101u;
     uint2 r;
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}" : "=r"(r.x), "=r"(r.y) : "r"(w));
+    r.x = ((w << 7) & 0x3f803f80u) | ((w << 8) & 0x80008000u);
+    r.y = ((w >> 1) & 0x3f803f80u) | (w & 0x80008000u);
     return r;
+}
+// Place of dim j of a row within the operands (and, both ways, of O's columns).
+__host__ __device__ constexpr int place(int j) { return (j & ~3) | ((j & 1) << 1) | ((j >> 1) & 1); }
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ void sts64(uint32_t a, uint2 v) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" :: "r"(a), "r"(v.x), "r"(v.y) : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Two f32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -277,6 +330,18 @@ constexpr unsigned WAIT_TRIES = 1u << 24;
 constexpr unsigned long long WAIT_NS = 1000000000ull;
 __device__ __forceinline__ void bar_init(uint64_t* b, unsigned n) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(smem_u32(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(smem_u32(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* b) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 :: "r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(b)) : "memory");
+}
+// Rows [row, row + box) of the tensor map's 8-bit matrix, all columns, swizzled.
+__device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap* map, int row, uint64_t* b) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                 :: "r"(dst), "l"(map), "r"(0), "r"(row), "r"(smem_u32(b)) : "memory");
 }
 __device__ __forceinline__ void bar_arrive(uint64_t* b) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(b)) : "memory");
@@ -312,9 +377,9 @@ __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.
 __device__ __forceinline__ void tc_commit(uint64_t* b) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(smem_u32(b)) : "memory");
 }
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void tc_mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
                  :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
 }
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
@@ -350,14 +415,16 @@ __device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t (&r)[16]) {
                  : "memory");
 }
 
-// Shared-memory operand descriptor: 128-byte swizzle, 8-row groups 1024 bytes
-// apart; `lead` is the step between 64-element column groups (only looked at
-// where the contiguous axis is not the one summed over).
+// Shared-memory operand descriptor: rows of ROW bytes swizzled over ROW bytes (128
+// or 64), 8-row groups together; `lead` is the step between 64-element column
+// groups (only looked at where the contiguous axis is not the one summed over).
+template <int ROW>
 __device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lead) {
-    return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 |
-           2ull << 61;
+    return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(8 * ROW >> 4) << 32 | 1ull << 46 |
+           (ROW == 128 ? 2ull : 4ull) << 61;
 }
-// f16 x f16 -> f32, M = 128; bit 16: the second operand's contiguous axis is N
+// f32 result, M = 128, operand types 0 (f16, or e4m3 of the 8-bit kind); bit 16: the second
+// operand's contiguous axis is N
 __host__ __device__ constexpr uint32_t tc_idesc(int n, bool b_n_major) {
     return 1u << 4 | (b_n_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
 }
@@ -378,212 +445,341 @@ __device__ __forceinline__ float finite_abs(float x) {
     return a <= 3.402823466e38f ? a : 0.f;
 }
 
-// One tile as the loading warps see it.
-struct LoadTile {
-    int b, h, mt, t, kind;                // kind: 0 none left, 1 cached, 2 tail, 3 no keys at all
-    bool first;                           // of its segment
+__device__ __forceinline__ bool is_dual(const Att& P, int mt) { return P.R - mt * 256 > 128; }
+
+// The tiles of a CTA's segments, one after the other.
+struct TileIter {
+    SegIter it;
+    Seg g;
+    int seg, gt, t;                       // segment, tile of the CTA, tile of the item
+    __device__ __forceinline__ void begin(const Att& P, const Stretch& st) {
+        it.begin(P, st);
+        seg = gt = -1;
+        t = 0;
+        g.t1 = 0;
+    }
+    __device__ __forceinline__ bool next(const Att& P) {
+        ++gt;
+        if (++t < g.t1) return true;
+        if (!it.next(P, g)) return false;
+        ++seg;
+        t = g.t0;
+        return true;
+    }
+    __device__ __forceinline__ bool cached() const { return t < g.q.nct; }
+    __device__ __forceinline__ bool first() const { return t == g.t0; }
 };
 
+// This lane's page of a cached tile (lanes 0 to TILE / page - 1); -2: none.
+__device__ __forceinline__ int page_entry(const Att& P, const Seg& g, int t, int lane) {
+    const int ppt = TILE >> P.pshift, p = t * ppt + lane;
+    return lane < ppt && p < g.q.full >> P.pshift ? __ldg(P.c.page_table + g.b * P.c.page_table_stride + p) : -2;
+}
+
+// The copying warp: the pages of a tile's keys, swizzled, then of its values, as they are.
 template <int D>
-struct TcLoader {
+__device__ void tc_copy_pages(const Att& P, const CUtensorMap* kmap, TcShared& sh, uint32_t base, const Stretch& st, int lane) {
+    constexpr int KR = Tc<D>::KR, VR = Tc<D>::VR;
+    TileIter u;
+    u.begin(P, st);
+    const uint32_t bytes = (uint32_t)D << P.pshift;
+    int nk = 0, nv = 0, ahead = -2, ahead_t = -1, ahead_b = -1;
+    while (u.next(P)) {
+        // The tail does not lie in pages; it takes two units of keys, which this warp sees pass: a barrier's parity
+        // says nothing to a waiter that is two phases behind or ahead.
+        if (!u.cached()) {
+            for (int i = 0; i < 2; ++i, ++nk) bar_wait(&sh.ke[nk % KR], ((nk / KR) & 1) ^ 1, sh);
+            continue;
+        }
+        const int page = ahead_b == u.g.b && ahead_t == u.t ? ahead : page_entry(P, u.g, u.t, lane);
+        ahead = page_entry(P, u.g, u.t + 1, lane);        // on its way for the tile after
+        ahead_b = u.g.b;
+        ahead_t = u.t + 1;
+        const bool ok = page >= 0 && page < P.c.num_pages;
+        if (page != -2 && !ok) sh.bad_seg[u.seg & 7] = u.seg + 1;
+        const uint32_t all = __popc(__ballot_sync(FULL, ok)) * bytes;
+        const int ks = nk % KR, vs = nv % VR;
+        const int64_t ph = (int64_t)page * P.Hkv + u.g.h;
+        bar_wait(&sh.ke[ks], ((nk / KR) & 1) ^ 1, sh);
+        if (lane == 0) bar_expect(&sh.kf[ks], all);
+        __syncwarp();
+        if (ok) tensor_copy(base + Tc<D>::K + ks * Tc<D>::RAW_B + lane * bytes, kmap, (int)(ph << P.pshift), &sh.kf[ks]);
+        bar_wait(&sh.re[vs], ((nv / VR) & 1) ^ 1, sh);
+        if (lane == 0) bar_expect(&sh.rf[vs], all);
+        __syncwarp();
+        if (ok) bulk_copy(base + Tc<D>::RAW + vs * Tc<D>::RAW_B + lane * bytes, static_cast<const char*>(P.c.v_pages) + ph * bytes,
+                          bytes, &sh.rf[vs]);
+        ++nk;
+        ++nv;
+    }
+    // also after a wait that gave up: no copy is in flight when the CTA ends.  (A key unit that the tail filled is
+    // waited for too: its writers arrive as well.)
+    for (int i = max(0, nk - KR); i < nk; ++i)
+        if (!bar_try(&sh.kf[i % KR], (i / KR) & 1)) bar_wait_slow(&sh.kf[i % KR], (i / KR) & 1, nullptr);
+    for (int i = max(0, nv - VR); i < nv; ++i)
+        if (!bar_try(&sh.rf[i % VR], (i / VR) & 1)) bar_wait_slow(&sh.rf[i % VR], (i / VR) & 1, nullptr);
+}
+
+// The warp that gathers the scales of the cached tiles' groups of 16 keys, a tile ahead.
+__device__ __forceinline__ void tc_scales(const Att& P, TcShared& sh, const Stretch& st, int lane) {
+    TileIter u;
+    u.begin(P, st);
+    auto fetch = [&](const Seg& g, int t, float& ks, float& vs) {
+        ks = vs = 1.f;
+        const int tok = t * TILE + lane * 16;
+        if (lane < 8 && t < g.q.nct && tok < g.q.full) {
+            const int id = __ldg(P.c.page_table + g.b * P.c.page_table_stride + (tok >> P.pshift));
+            if (id >= 0 && id < P.c.num_pages) {
+                ks = __ldg(P.c.k_scale + (int64_t)id * P.Hkv + g.h);
+                vs = __ldg(P.c.v_scale + (int64_t)id * P.Hkv + g.h);
+            }
+        }
+    };
+    float ks = 1.f, vs = 1.f;
+    bool more = u.next(P);
+    if (more) fetch(u.g, u.t, ks, vs);
+    while (more) {
+        const int m = u.gt & (TC_META - 1);
+        const uint32_t par = ((u.gt / TC_META) & 1) ^ 1;
+        const bool cached = u.cached();
+        const float k0 = ks, v0 = vs * 256.f;             // the f16 values are 2^-8 of the bytes
+        more = u.next(P);
+        if (more) fetch(u.g, u.t, ks, vs);
+        bar_wait(&sh.me[m], par, sh);
+        if (!cached) continue;                            // the operand warps write the tail's
+        if (lane < 8) {
+            sh.meta[m][0][lane] = k0;
+            sh.meta[m][1][lane] = log2f(v0);
+            sh.meta[m][2][lane] = 1.f / v0;
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(&sh.mf[m]);
+    }
+}
+
+// The warps that make operands.
+template <int D>
+struct TcConv {
     static constexpr int CPR = D / 16;                    // 16-byte chunks of a cached row
-    static constexpr int RPP = TC_LOAD / CPR;             // rows per pass
+    static constexpr int RPP = TC_CONV / CPR;             // rows per pass
     static constexpr int NP = TILE / RPP;                 // passes
+    static constexpr int LPR = D / 8, RP = TC_CONV / LPR; // bf16 rows: lanes per row, rows per pass
+    static constexpr int NB = TILE / RP;                  // passes
     const Att& P;
     TcShared& sh;
     const uint32_t base;
-    const int tid, lane, c, r0;
-    SegIter it;
-    Seg g;
-    int t, seg;                                           // next tile of g; segments begun
-    bool have;
-    int ids[NP], ids_b, ids_t;                            // page ids fetched ahead
+    const int tid, lane;
 
-    __device__ __forceinline__ TcLoader(const Att& P_, TcShared& s, uint32_t b, int tid_)
-        : P(P_), sh(s), base(b), tid(tid_), lane(tid_ & 31), c(tid_ % CPR), r0(tid_ / CPR) {}
+    __device__ __forceinline__ TcConv(const Att& P_, TcShared& s, uint32_t b, int tid_)
+        : P(P_), sh(s), base(b), tid(tid_), lane(tid_ & 31) {}
 
-    __device__ __forceinline__ void begin(const Stretch& st) {
-        it.begin(P, st);
-        have = it.next(P, g);
-        t = have ? g.t0 : 0;
-        ids_b = -1;
-        ids_t = -1;
-    }
-    __device__ __forceinline__ LoadTile next() {
-        LoadTile x{};
-        if (have && t == g.t1) {
-            have = it.next(P, g);
-            if (have) t = g.t0;
-        }
-        if (!have) return x;
-        x.b = g.b; x.h = g.h; x.mt = g.mt; x.t = t;
-        x.kind = t < g.q.nct ? 1 : g.q.len >= 0 && !g.q.bad ? 2 : 3;
-        x.first = t == g.t0;
-        ++t;
-        return x;
-    }
-    __device__ __forceinline__ int page_id(int b, int t, int i) {
-        const int tok = t * TILE + r0 + i * RPP;
-        return tok < g.q.full ? __ldg(P.c.page_table + b * P.c.page_table_stride + tok / P.page) : -2;
-    }
-    // Bytes of a cached tile, and the scales of its groups of 16 keys (threads 0-7), on their way to registers.
-    // Called right after next(): g is the tile's item.
-    __device__ __forceinline__ void fetch(const LoadTile& x, uint4 (&k)[NP], uint4 (&v)[NP], float& ks, float& vs, bool& bad) {
-        bad = false;
-        if (x.kind != 1) return;
-        if (ids_b != x.b || ids_t != x.t) {
-#pragma unroll
-            for (int i = 0; i < NP; ++i) ids[i] = page_id(x.b, x.t, i);
-        }
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const int tok = x.t * TILE + r0 + i * RPP;
-            const bool ok = ids[i] >= 0 && ids[i] < P.c.num_pages;
-            bad |= ids[i] != -2 && !ok;
-            k[i] = v[i] = make_uint4(0, 0, 0, 0);
-            if (ok) {
-                const int64_t at = (((int64_t)ids[i] * P.Hkv + x.h) * P.page + tok % P.page) * D + c * 16;
-                k[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(P.c.k_pages) + at));
-                v[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(P.c.v_pages) + at));
-            }
-        }
-        ks = vs = 1.f;
-        if (tid < 8) {
-            const int tok = x.t * TILE + tid * 16;
-            const int id = tok < g.q.full ? __ldg(P.c.page_table + x.b * P.c.page_table_stride + tok / P.page) : -2;
-            if (id >= 0 && id < P.c.num_pages) {
-                ks = __ldg(P.c.k_scale + (int64_t)id * P.Hkv + x.h);
-                vs = __ldg(P.c.v_scale + (int64_t)id * P.Hkv + x.h);
-            }
-        }
-        ids_b = x.b;
-        ids_t = x.t + 1;
-#pragma unroll
-        for (int i = 0; i < NP; ++i) ids[i] = page_id(x.b, ids_t, i);
-    }
     __device__ __forceinline__ void arrive(uint64_t* bar) {
         proxy_fence();
         __syncwarp();
         if (lane == 0) bar_arrive(bar);
     }
-    // A cached tile's bytes as f16 rows.  The upper half of the lanes that share rows stores its two
-    // chunks in the other order, so that eight lanes meet all 32 banks.
-    __device__ __forceinline__ void put(uint32_t dst, const uint4 (&x)[NP]) {
+    // A unit's bytes as f16 rows, rows from `valid` on as zeros.  The upper half of the lanes that share a row
+    // stores its two chunks in the other order, so that eight lanes meet all 32 banks.
+    __device__ __forceinline__ void put(uint32_t dst, uint32_t src, int valid) {
+        const int c = tid % CPR, r0 = tid / CPR;
         const uint32_t half = dst + (c / 4) * Tc<D>::HALF;
         const int q = (c % 4) * 2, flip = c / 4;
-#pragma unroll
+        uint32_t nan = 0;
+#pragma unroll 4
         for (int i = 0; i < NP; ++i) {
-            const uint2 a = e4m3_f16(x[i].x), b = e4m3_f16(x[i].y), d = e4m3_f16(x[i].z), e = e4m3_f16(x[i].w);
-            const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, e.x, e.y);
             const int r = r0 + i * RPP;
+            uint4 x = lds128(src + r * D + c * 16);
+            if (r >= valid) x = make_uint4(0, 0, 0, 0);
+            const uint2 a = e4m3_f16(x.x, nan), b = e4m3_f16(x.y, nan), d = e4m3_f16(x.z, nan), e = e4m3_f16(x.w, nan);
+            const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, e.x, e.y);
             sts128(swz(half, r, q + flip), flip ? hi : lo);
             sts128(swz(half, r, q + 1 - flip), flip ? lo : hi);
         }
+        if (nan & 0x80808080u) put_nans(half, src, valid);
     }
-    // Rows of eight bf16 elements per lane, D / 8 lanes per row; returns the row's power of two.
-    __device__ __forceinline__ int put_row(uint32_t dst, int r, int l, uint4 raw, bool& nonfinite, bool zero_nonfinite) {
-        Vec8<SPEC_BF16> w;
-        w.a = raw;
-        float x[8], amax = 0.f;
-        w.get(x);
-        nonfinite = false;
+    // This thread's NaN bytes, one by one.
+    __device__ __noinline__ void put_nans(uint32_t half, uint32_t src, int valid) {
+        const int c = tid % CPR, r0 = tid / CPR;
+        for (int i = 0; i < 16 * NP; ++i) {
+            const int r = r0 + i / 16 * RPP, j = i & 15;
+            uint32_t v;
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(src + r * D + c * 16 + j));
+            const int p = place(j);
+            if (r < valid && (v & 0x7f) == 0x7f)
+                asm volatile("st.shared.b16 [%0], %1;" :: "r"(swz(half, r, (c % 4) * 2 + p / 8) + (p & 7) * 2), "h"((uint16_t)0x7e00) : "memory");
+        }
+    }
+    // Eight bf16 elements of a row in each of D / 8 lanes: the row's power of two, with its non-finite elements
+    // reported and (zero_bad) zeroed.
+    __device__ __forceinline__ int scale_row(float (&x)[8], bool& bad, bool zero_bad) {
+        float amax = 0.f;
+        bad = false;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float a = finite_abs(x[i]);
+            amax = fmaxf(amax, finite_abs(x[i]));
             if (!(fabsf(x[i]) <= 3.402823466e38f)) {
-                nonfinite = true;
-                if (zero_nonfinite) x[i] = 0.f;
+                bad = true;
+                if (zero_bad) x[i] = 0.f;
             }
-            amax = fmaxf(amax, a);
         }
 #pragma unroll
         for (int o = D / 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, o));
-        const int e = pow2_of(amax);
+        return pow2_of(amax);
+    }
+    // f16 value row r.
+    __device__ __forceinline__ void put_value_row(uint32_t dst, int r, int l, const float (&x)[8], int e) {
         const float s = exp2i(-e);
         sts128(swz(dst + (l / 8) * Tc<D>::HALF, r, l % 8),
-               make_uint4(pack_f16(x[0] * s, x[1] * s), pack_f16(x[2] * s, x[3] * s), pack_f16(x[4] * s, x[5] * s),
-                          pack_f16(x[6] * s, x[7] * s)));
-        return e;
+               make_uint4(pack_f16(x[0] * s, x[2] * s), pack_f16(x[1] * s, x[3] * s), pack_f16(x[4] * s, x[6] * s),
+                          pack_f16(x[5] * s, x[7] * s)));
     }
-    __device__ __forceinline__ void put_q(const LoadTile& x) {
-        constexpr int LPR = D / 8, RP = TC_LOAD / LPR;
-        const int l = tid % LPR;
-        const int rows = min(256, P.R - x.mt * 256);
-        const int upto = rows > 128 ? 256 : 128;
-        for (int r = tid / LPR; r < upto; r += RP) {
-            const int row = x.mt * 256 + r, n = row / P.G, h = x.h * P.G + row % P.G;
-            uint4 raw = make_uint4(0, 0, 0, 0);
-            if (r < rows)
-                raw = __ldg(reinterpret_cast<const uint4*>(P.q.p + x.b * P.q.b + n * P.q.n + h * P.q.h) + l);
-            bool nf;
-            const int e = put_row(base + Tc<D>::Q + (r / 128) * Tc<D>::TILE_B, r % 128, l, raw, nf, false);
-            if (l == 0) sh.rq[seg & 3][r] = exp2i(e) * P.scale;
+    // The two e4m3 rows of a bf16 row divided by 2^(e - 7); infinities become NaN.
+    __device__ __forceinline__ void split_row(const float (&x)[8], int e, uint2& hi, uint2& lo) {
+        const float s = exp2i(-e) * 128.f;
+        uint32_t h[4], w[4];
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            float a = x[i] * s, b = x[i + 1] * s;
+            if (!(fabsf(x[i]) <= 3.402823466e38f)) a = __int_as_float(0x7fffffff);
+            if (!(fabsf(x[i + 1]) <= 3.402823466e38f)) b = __int_as_float(0x7fffffff);
+            h[i / 2] = pack_e4m3(a, b);
+            uint32_t f;
+            asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(f) : "r"(h[i / 2]));
+            float fa, fb;
+            asm("{\n\t.reg .b16 p, q;\n\tmov.b32 {p, q}, %2;\n\tcvt.f32.f16 %0, p;\n\tcvt.f32.f16 %1, q;\n\t}" : "=f"(fa), "=f"(fb) : "r"(f));
+            w[i / 2] = pack_e4m3(a - fa, b - fb);
         }
+        hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+        lo = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
     }
-    // One of k and v of a tail tile: open tokens from the ring, then the nodes.
-    __device__ __forceinline__ void put_tail(const LoadTile& x, uint32_t dst, int which, float* a, float* b, float* c2) {
-        constexpr int LPR = D / 8, RP = TC_LOAD / LPR;
+    __device__ __forceinline__ void put_q(const Seg& g, int seg) {
         const int l = tid % LPR;
-        const Seq q = seq_of(P, x.b);
-        const char* ring = static_cast<const char*>(which ? P.c.v_open : P.c.k_open) +
-                           ((int64_t)q.slot * P.Hkv + x.h) * 2 * P.page * D * 2;
-        const sv_host::Rows& src = which ? P.v : P.k;
-        const int e0 = (x.t - q.nct) * TILE, keys = q.open + P.N;
-        for (int r = tid / LPR; r < TILE; r += RP) {
-            const int e = e0 + r;
-            uint4 raw = make_uint4(0, 0, 0, 0);
-            if (x.kind == 2 && e < q.open)
-                raw = *reinterpret_cast<const uint4*>(ring + ((int64_t)((q.full + e) % (2 * P.page)) * D + 8 * l) * 2);
-            else if (x.kind == 2 && e < keys)
-                raw = __ldg(reinterpret_cast<const uint4*>(src.p + x.b * src.b + (e - q.open) * src.n + x.h * src.h) + l);
-            bool nf;
-            const int p = put_row(dst, r, l, raw, nf, which == 1);
-            if (which == 1) {
-                if (nf) atomicOr(&sh.bad_v[seg & 3][e >> 5], 1u << (e & 31));
-                if (l == 0) {
-                    b[r] = (float)p;
-                    c2[r] = exp2i(-p);
+        const int rows = min(256, P.R - g.mt * 256);
+#pragma unroll 1
+        for (int p0 = 0; p0 < (rows > 128 ? 2 * NB : NB); p0 += 8) {
+            Vec8<SPEC_BF16> w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = tid / LPR + (p0 + i) * RP, row = g.mt * 256 + r, n = row / P.G, h = g.h * P.G + row - n * P.G;
+                w[i].zero();
+                if (r < rows) w[i].load(P.q.p + g.b * P.q.b + n * P.q.n + h * P.q.h + 16 * l);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = tid / LPR + (p0 + i) * RP;
+                float x[8];
+                w[i].get(x);
+                bool bad;
+                const int e = scale_row(x, bad, false);
+                uint2 hi, lo;
+                split_row(x, e, hi, lo);
+                const uint32_t dst = base + Tc<D>::Q + (r / 128) * Tc<D>::Q_B;
+                if (D == 128) {                           // two tiles of 128-byte rows
+                    sts64(swz(dst, r % 128, l / 2) + (l & 1) * 8, hi);
+                    sts64(swz(dst + Tc<D>::RAW_B, r % 128, l / 2) + (l & 1) * 8, lo);
+                } else {                                  // side by side
+                    sts64(swz(dst, r % 128, l / 2) + (l & 1) * 8, hi);
+                    sts64(swz(dst, r % 128, 4 + l / 2) + (l & 1) * 8, lo);
                 }
-            } else if (l == 0) {
-                a[r] = exp2i(p);
+                if (l == 0) sh.rq[seg & 3][r] = exp2i(e) * (P.scale * 0.0078125f);
             }
         }
     }
-    // Hands tile number `gt` of the CTA to the tensor cores.
-    __device__ __forceinline__ void give(const LoadTile& x, int gt, const uint4 (&k)[NP], const uint4 (&v)[NP], float ks, float vs,
-                                         bool bad) {
-        const int st = gt & 1;
-        const uint32_t par = ((gt >> 1) & 1) ^ 1;
-        if (x.first) {
-            bar_wait(&sh.qe, (seg & 1) ^ 1, sh);
-            if (tid < 12) sh.bad_v[seg & 3][tid] = 0;
-            asm volatile("bar.sync 2, %0;" :: "n"(TC_LOAD) : "memory");
-            put_q(x);
-            arrive(&sh.qf);
+    // Eight passes of the tail's rows, from pass p0 on: open tokens from the ring, then the nodes.
+    __device__ __forceinline__ void load_tail(const TileIter& u, int which, int p0, Vec8<SPEC_BF16> (&w)[8]) {
+        const int l = tid % LPR;
+        const Seq& q = u.g.q;
+        const bool live = q.len >= 0 && !q.bad;
+        const char* ring = static_cast<const char*>(which ? P.c.v_open : P.c.k_open) +
+                           ((int64_t)q.slot * P.Hkv + u.g.h) * 2 * P.page * D * 2;
+        const sv_host::Rows& src = which ? P.v : P.k;
+        const int e0 = (u.t - q.nct) * TILE, keys = q.open + P.N;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = e0 + tid / LPR + (p0 + i) * RP;
+            w[i].zero();
+            if (live && e < q.open) w[i].load_plain(ring + ((int64_t)((q.full + e) & (2 * P.page - 1)) * D + 8 * l) * 2);
+            else if (live && e < keys) w[i].load(src.p + u.g.b * src.b + (e - q.open) * src.n + u.g.h * src.h + 16 * l);
         }
-        if (bad) sh.bad_seg[seg & 3] = seg + 1;
-        float* m = sh.meta[gt & (TC_META - 1)][0];
-        bar_wait(&sh.ke[st], par, sh);
-        const uint32_t kd = base + Tc<D>::K + st * Tc<D>::TILE_B, vd = base + Tc<D>::V + st * Tc<D>::TILE_B;
-        if (x.kind == 1) {
-            if (tid < 8) {
-                m[tid] = ks;
-                m[TILE + tid] = log2f(vs);
-                m[2 * TILE + tid] = 1.f / vs;
+    }
+    // A tile of the tail: its two units of keys, its values and all of its scales.
+    __device__ __forceinline__ void tail(const TileIter& u, int nk) {
+        constexpr int KR = Tc<D>::KR;
+        const int l = tid % LPR, e0 = (u.t - u.g.q.nct) * TILE, m = u.gt & (TC_META - 1);
+        const int k0 = nk % KR, k1 = (nk + 1) % KR;
+        bar_wait(&sh.me[m], ((u.gt / TC_META) & 1) ^ 1, sh);
+        bar_wait(&sh.ke[k0], ((nk / KR) & 1) ^ 1, sh);
+        bar_wait(&sh.ke[k1], (((nk + 1) / KR) & 1) ^ 1, sh);
+        bar_wait(&sh.ve[u.gt & 1], ((u.gt >> 1) & 1) ^ 1, sh);
+#pragma unroll 1
+        for (int p0 = 0; p0 < NB; p0 += 8) {
+            Vec8<SPEC_BF16> k[8], v[8];
+            load_tail(u, 0, p0, k);
+            load_tail(u, 1, p0, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = tid / LPR + (p0 + i) * RP;
+                float x[8];
+                bool bad;
+                v[i].get(x);
+                const int ve = scale_row(x, bad, true);   // what is not finite reaches its rows at the end
+                if (bad) atomicOr(&sh.bad_v[u.seg & 3][(e0 + r) >> 5], 1u << ((e0 + r) & 31));
+                put_value_row(base + Tc<D>::V + (u.gt & 1) * Tc<D>::V_B, r, l, x, ve);
+                k[i].get(x);
+                const int ke = scale_row(x, bad, false);
+                uint2 hi, lo;
+                split_row(x, ke, hi, lo);
+                sts64(key_at(base + Tc<D>::K + k0 * Tc<D>::RAW_B, r, l), hi);
+                sts64(key_at(base + Tc<D>::K + k1 * Tc<D>::RAW_B, r, l), lo);
+                if (l == 0) {
+                    sh.meta[m][0][r] = exp2i(ke) * 0.0078125f;
+                    sh.meta[m][1][r] = (float)ve;
+                    sh.meta[m][2][r] = exp2i(-ve);
+                }
             }
-            put(kd, k);
-        } else {
-            // the value rows' scales belong to the same record: they are known before the keys are handed over
-            bar_wait(&sh.ve[st], par, sh);
-            put_tail(x, vd, 1, m, m + TILE, m + 2 * TILE);
-            put_tail(x, kd, 0, m, m + TILE, m + 2 * TILE);
         }
-        arrive(&sh.kf[st]);
-        if (x.kind == 1) {
-            bar_wait(&sh.ve[st], par, sh);
-            put(vd, v);
+        proxy_fence();
+        asm volatile("bar.sync 2, %0;" :: "n"(TC_CONV) : "memory");
+        if (tid == 0) {
+            bar_arrive(&sh.mf[m]);
+            bar_arrive(&sh.kf[k0]);
+            bar_arrive(&sh.kf[k1]);
         }
-        arrive(&sh.vf[st]);
+        if (lane == 0) bar_arrive(&sh.vf[u.gt & 1]);
+    }
+    // Eight e4m3 of row r, as the tensor copy lays them: rows of D bytes, swizzled over D bytes.
+    __device__ __forceinline__ uint32_t key_at(uint32_t dst, int r, int l) {
+        const int q = D == 128 ? (l / 2) ^ (r & 7) : (l / 2) ^ ((r >> 1) & 3);
+        return dst + r * D + q * 16 + (l & 1) * 8;
+    }
+    __device__ __forceinline__ void run(const Stretch& st) {
+        constexpr int VR = Tc<D>::VR;
+        TileIter u;
+        u.begin(P, st);
+        int nk = 0, nv = 0;
+        while (u.next(P)) {
+            if (u.first()) {
+                bar_wait(&sh.qe, (u.seg & 1) ^ 1, sh);
+                if (tid < 12) sh.bad_v[u.seg & 3][tid] = 0;
+                asm volatile("bar.sync 2, %0;" :: "n"(TC_CONV) : "memory");
+                put_q(u.g, u.seg);
+                arrive(&sh.qf);
+            }
+            if (!u.cached()) {
+                tail(u, nk);
+                nk += 2;
+                continue;
+            }
+            ++nk;
+            const int s = nv % VR;
+            bar_wait(&sh.rf[s], (nv / VR) & 1, sh);
+            bar_wait(&sh.ve[u.gt & 1], ((u.gt >> 1) & 1) ^ 1, sh);
+            put(base + Tc<D>::V + (u.gt & 1) * Tc<D>::V_B, base + Tc<D>::RAW + s * Tc<D>::RAW_B, u.g.q.full - u.t * TILE);
+            __syncwarp();
+            if (lane == 0) bar_arrive(&sh.re[s]);
+            ++nv;
+            arrive(&sh.vf[u.gt & 1]);
+        }
     }
 };
 
@@ -601,26 +797,32 @@ __device__ __forceinline__ void tile_mask(const Att& P, const Seg& g, int t, int
 }
 
 // MODE 0: cached tile, all keys; 1: cached tile, masked; 2: tail (masked, scales per key).
+// The largest w of the row's keys.
 template <int MODE>
 __device__ __forceinline__ float tile_max(uint32_t s_col, const float* meta, float rq, const uint32_t (&mk)[4]) {
     float mx = NEG_INF;
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < 4; ++c) {
         uint32_t r[32];
         tc_ld32(s_col + 32 * c, r);
         tc_wait_ld();
         if (MODE > 0) {
+            const uint32_t bits = mk[c];
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                if (!((mk[c] >> j) & 1)) r[j] = 0xff800000u;
+                if (!((bits >> j) & 1)) r[j] = 0xff800000u;
         }
         if (MODE < 2) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                float gm = __uint_as_float(r[16 * u]);
+                float a = __uint_as_float(r[16 * u]), b = __uint_as_float(r[16 * u + 1]);
 #pragma unroll
-                for (int j = 1; j < 16; ++j) gm = fmaxf(gm, __uint_as_float(r[16 * u + j]));
-                mx = fmaxf(mx, fmaf(gm, fmaxf(meta[2 * c + u] * rq, 1.2e-38f), meta[TILE + 2 * c + u]));
+                for (int j = 2; j < 14; j += 4) {
+                    a = max3(a, __uint_as_float(r[16 * u + j]), __uint_as_float(r[16 * u + j + 1]));
+                    b = max3(b, __uint_as_float(r[16 * u + j + 2]), __uint_as_float(r[16 * u + j + 3]));
+                }
+                a = max3(a, __uint_as_float(r[16 * u + 14]), __uint_as_float(r[16 * u + 15]));
+                mx = fmaxf(mx, fmaf(fmaxf(a, b), fmaxf(meta[2 * c + u] * rq, 1.2e-38f), meta[TILE + 2 * c + u]));
             }
         } else {
 #pragma unroll
@@ -630,32 +832,36 @@ __device__ __forceinline__ float tile_max(uint32_t s_col, const float* meta, flo
     }
     return mx;
 }
+// P = 2^(w + sub) in f16 over the scores; returns the row's sum of P / s_v.
 template <int MODE>
 __device__ __forceinline__ float tile_probs(uint32_t s_col, const float* meta, float rq, const uint32_t (&mk)[4], float sub) {
     float l = 0.f;
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < 4; ++c) {
         uint32_t r[32], p[16];
         tc_ld32(s_col + 32 * c, r);
         tc_wait_ld();
         if (MODE > 0) {
+            const uint32_t bits = mk[c];
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                if (!((mk[c] >> j) & 1)) r[j] = 0xff800000u;
+                if (!((bits >> j) & 1)) r[j] = 0xff800000u;
         }
         if (MODE < 2) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const float a = fmaxf(meta[2 * c + u] * rq, 1.2e-38f), b = meta[TILE + 2 * c + u] + sub;
-                float gs = 0.f;
+                float2 gs = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int j = 0; j < 16; j += 2) {
-                    const float x = ex2(fmaf(__uint_as_float(r[16 * u + j]), a, b));
-                    const float y = ex2(fmaf(__uint_as_float(r[16 * u + j + 1]), a, b));
-                    gs += x + y;
-                    p[8 * u + j / 2] = pack_f16(x, y);
+                    float2 x = fma2(make_float2(__uint_as_float(r[16 * u + j]), __uint_as_float(r[16 * u + j + 1])),
+                                    make_float2(a, a), make_float2(b, b));
+                    x.x = ex2(x.x);
+                    x.y = ex2(x.y);
+                    gs = add2(gs, x);
+                    p[8 * u + j / 2] = pack_f16(x.x, x.y);
                 }
-                l = fmaf(gs, meta[2 * TILE + 2 * c + u], l);
+                l = fmaf(gs.x + gs.y, meta[2 * TILE + 2 * c + u], l);
             }
         } else {
 #pragma unroll
@@ -681,77 +887,43 @@ __device__ __forceinline__ float* partial_of(const Att& P, int cta, int slot) {
 
 __device__ __forceinline__ int rows_of(const Att& P) { return min(P.R, 256); }
 
-// Row r of the partial results of a cut item, put together by a warp and written out.
 template <int D>
-__device__ void merge_row(const Att& P, int r, int rows, int c0, int slot0, int parts, int lane, char* out, float* lse) {
-    float M = NEG_INF;
-    for (int i = lane; i < parts; i += 32)
-        M = fmaxf(M, __ldcg(partial_of<D>(P, c0 + i, i == 0 ? slot0 : 0) + (int64_t)rows * D + r));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
-    const float base = M == NEG_INF ? 0.f : M;
-    constexpr int E = D / 32;
-    float acc[E] = {}, l = 0.f;
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-        float w = 0.f, wl = 0.f;
-        if (i0 + lane < parts) {
-            const float* p = partial_of<D>(P, c0 + i0 + lane, i0 + lane == 0 ? slot0 : 0) + (int64_t)rows * D;
-            w = ex2(__ldcg(p + r) - base);
-            wl = w * __ldcg(p + rows + r);
-        }
-        l += wl;
-        const int n = min(32, parts - i0);
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float wi = __shfl_sync(FULL, w, i);
-            const float* p = partial_of<D>(P, c0 + i0 + i, i0 + i == 0 ? slot0 : 0) + (int64_t)r * D + lane * E;
-            if constexpr (E == 4) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
-                acc[0] = fmaf(wi, x.x, acc[0]); acc[1] = fmaf(wi, x.y, acc[1]);
-                acc[2] = fmaf(wi, x.z, acc[2]); acc[3] = fmaf(wi, x.w, acc[3]);
-            } else {
-                const float2 x = __ldcg(reinterpret_cast<const float2*>(p));
-                acc[0] = fmaf(wi, x.x, acc[0]); acc[1] = fmaf(wi, x.y, acc[1]);
-            }
-        }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(FULL, l, o);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    if constexpr (E == 4)
-        reinterpret_cast<uint2*>(out)[lane] = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
-    else
-        reinterpret_cast<uint32_t*>(out)[lane] = pack_bf16(acc[0] * inv, acc[1] * inv);
-    if (lse && lane == 0) *lse = l == 0.f ? NEG_INF : (base + log2f(l)) * LN2;
-}
-
-template <int D>
-__global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P) {
+__global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __grid_constant__ CUtensorMap kmap) {
     extern __shared__ unsigned char raw_smem[];
     const uint32_t base = (smem_u32(raw_smem) + 1023u) & ~1023u;
     TcShared& sh = *reinterpret_cast<TcShared*>(raw_smem + (base - smem_u32(raw_smem)) + Tc<D>::END);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Stretch st = find_stretch<TC_BT>(P);
+    if (tid == 0) P.cut[blockIdx.x].parts = 0;
     if (st.lo >= st.hi) return;
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            bar_init(&sh.kf[i], TC_LOAD / 32);
-            bar_init(&sh.vf[i], TC_LOAD / 32);
+        for (int i = 0; i < 6; ++i) {
+            bar_init(&sh.kf[i], 1);
             bar_init(&sh.ke[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            bar_init(&sh.rf[i], 1);
+            bar_init(&sh.re[i], TC_CONV / 32);
+            bar_init(&sh.mf[i], 1);
+            bar_init(&sh.me[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&sh.vf[i], TC_CONV / 32);
             bar_init(&sh.ve[i], 1);
             bar_init(&sh.sf[i], 1);
             bar_init(&sh.pf[i], 128);
             bar_init(&sh.pv[i], 1);
-            sh.last[i] = 0;
         }
-        for (int i = 0; i < 4; ++i) sh.bad_seg[i] = 0;
-        bar_init(&sh.qf, TC_LOAD / 32);
+        for (int i = 0; i < 8; ++i) sh.bad_seg[i] = 0;
+        bar_init(&sh.qf, TC_CONV / 32);
         bar_init(&sh.qe, 1);
         bar_init(&sh.drain, 1);
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        proxy_fence();
     }
-    if (warp == TC_BT / 32 - 1) {
+    if (warp == TC_W_MMA) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(smem_u32(&sh.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         tc_before();
@@ -760,55 +932,48 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P) {
     tc_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
 
-    if (warp >= TC_SOFTMAX / 32 && warp < TC_BT / 32 - 1) {
-        // ---- loads: the next tile's bytes are on their way while this one is converted
-        TcLoader<D> ld(P, sh, base, tid - TC_SOFTMAX);
-        constexpr int NP = TcLoader<D>::NP;
-        uint4 k0[NP], v0[NP], k1[NP], v1[NP];
-        float ks0, vs0, ks1, vs1;
-        bool bad0, bad1;
-        ld.begin(st);
-        ld.seg = -1;
-        LoadTile x0 = ld.next(), x1;
-        ld.fetch(x0, k0, v0, ks0, vs0, bad0);
-        for (int gt = 0; x0.kind; gt += 2) {
-            x1 = ld.next();
-            ld.fetch(x1, k1, v1, ks1, vs1, bad1);
-            if (x0.first) ++ld.seg;
-            ld.give(x0, gt, k0, v0, ks0, vs0, bad0);
-            if (!x1.kind) break;
-            x0 = ld.next();
-            ld.fetch(x0, k0, v0, ks0, vs0, bad0);
-            if (x1.first) ++ld.seg;
-            ld.give(x1, gt + 1, k1, v1, ks1, vs1, bad1);
-        }
-    } else if (warp == TC_BT / 32 - 1) {
+    if (warp >= TC_W_CONV && warp < TC_W_MMA) {
+        TcConv<D>(P, sh, base, tid - TC_SOFTMAX).run(st);
+    } else if (warp == TC_W_COPY) {
+        tc_copy_pages<D>(P, &kmap, sh, base, st, lane);
+    } else if (warp == TC_W_SCALE) {
+        tc_scales(P, sh, st, lane);
+    } else if (warp == TC_W_MMA) {
         // ---- matrix instructions
         if (lane == 0) {
             SegIter it;
             Seg g;
             it.begin(P, st);
             uint32_t cnt[2] = {0, 0};
-            int g0 = 0;
+            int g0 = 0, nk0 = 0;
             constexpr uint32_t ID_QK = tc_idesc(TILE, false), ID_PV = tc_idesc(D, true);
+            constexpr int KR = Tc<D>::KR;
             for (int seg = 0; it.next(P, g); ++seg) {
-                const bool dual = P.R - g.mt * 256 > 128;
-                const int nt = g.t1 - g.t0;
+                const bool dual = is_dual(P, g.mt);
+                const int nt = g.t1 - g.t0, nc = max(0, min(nt, g.q.nct - g.t0));    // tiles, cached ones
                 int left = dual ? 2 * nt : nt;            // score products still to issue
                 bar_wait(&sh.qf, seg & 1, sh);
                 tc_after();
+                // Products of the two kinds are not ordered among themselves: a stream's probabilities have to be through
+                // before its next scores are written over them.
                 auto scores = [&](int i, int tl) {
-                    const int gt = g0 + tl, s = gt & 1;
-                    bar_wait(&sh.kf[s], (gt >> 1) & 1, sh);
-                    tc_after();
-                    const uint32_t q = base + Tc<D>::Q + (dual ? i : 0) * Tc<D>::TILE_B, k = base + Tc<D>::K + s * Tc<D>::TILE_B;
+                    if (cnt[i]) bar_wait(&sh.pv[i], (cnt[i] - 1) & 1, sh);
+                    const uint32_t q = base + Tc<D>::Q + (dual ? i : 0) * Tc<D>::Q_B;
+                    const int parts = tl < nc ? 1 : 2, nk = nk0 + tl + max(0, tl - nc);
+                    for (int part = 0; part < parts; ++part) {
+                        const int s = (nk + part) % KR;
+                        bar_wait(&sh.kf[s], ((nk + part) / KR) & 1, sh);
+                        tc_after();
+                        const uint32_t k = base + Tc<D>::K + s * Tc<D>::RAW_B;
 #pragma unroll
-                    for (int u = 0; u < D / 16; ++u) {
-                        const uint32_t off = (u / 4) * Tc<D>::HALF + (u % 4) * 32;
-                        tc_mma_ss(tmem + i * TILE, tc_desc(q + off, 16), tc_desc(k + off, 16), ID_QK, u > 0);
+                        for (int u = 0; u < 2 * D / 32; ++u) {     // q's first rows, then its second
+                            const uint32_t off = D == 128 ? (u / 4) * Tc<D>::RAW_B + (u % 4) * 32 : u * 32;
+                            tc_mma_e4m3(tmem + i * TILE, tc_desc<128>(q + off, 16), tc_desc<D>(k + (u % (D / 32)) * 32, 16),
+                                        ID_QK, part > 0 || u > 0);
+                        }
+                        if (!dual || i == 1) tc_commit(&sh.ke[s]);
                     }
                     tc_commit(&sh.sf[i]);
-                    if (!dual || i == 1) tc_commit(&sh.ke[s]);
                     if (--left == 0) tc_commit(&sh.qe);
                 };
                 auto tile = [&](int i, int step) { return dual ? step : 2 * step + i; };
@@ -822,25 +987,29 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P) {
                         bar_wait(&sh.vf[s], (gt >> 1) & 1, sh);
                         bar_wait(&sh.pf[i], cnt[i] & 1, sh);
                         tc_after();
-                        const uint32_t v = base + Tc<D>::V + s * Tc<D>::TILE_B;
+                        const uint32_t v = base + Tc<D>::V + s * Tc<D>::V_B;
 #pragma unroll
                         for (int u = 0; u < TILE / 16; ++u)
-                            tc_mma_ts(tmem + Tc<D>::O_COL + i * D, tmem + i * TILE + u * 8, tc_desc(v + u * 2048, Tc<D>::HALF),
+                            tc_mma_ts(tmem + Tc<D>::O_COL + i * D, tmem + i * TILE + u * 8, tc_desc<128>(v + u * 2048, Tc<D>::HALF),
                                       ID_PV, step > 0 || u > 0);
                         ++cnt[i];
-                        if (!dual || i == 1) tc_commit(&sh.ve[s]);
+                        if (!dual || i == 1) {
+                            tc_commit(&sh.ve[s]);
+                            tc_commit(&sh.me[gt & (TC_META - 1)]);
+                        }
+                        tc_commit(&sh.pv[i]);
                         if (tile(i, step + 1) < nt) scores(i, tile(i, step + 1));
-                        else tc_commit(&sh.pv[i]);
                     }
                 }
                 g0 += nt;
+                nk0 += nt + (nt - nc);
             }
             tc_commit(&sh.drain);
             // also after a wait that gave up: nothing runs on when the tensor memory is freed
             if (!bar_try(&sh.drain, 0)) bar_wait_slow(&sh.drain, 0, nullptr);
         }
         __syncwarp();
-    } else {
+    } else if (warp < TC_SOFTMAX / 32) {
         // ---- softmax of stream i; thread = row
         const int i = warp / 4, r = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;               // 32 lanes per warp, lane index in bits 16-31
@@ -848,7 +1017,7 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P) {
         SegIter it;
         Seg g;
         it.begin(P, st);
-        uint32_t cnt = 0, pvc = 0;
+        uint32_t cnt = 0;
         int g0 = 0;
         for (int seg = 0; it.next(P, g); ++seg) {
             const int rows = min(256, P.R - g.mt * 256);
@@ -858,12 +1027,22 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P) {
             const int row = g.mt * 256 + min(ri, rows - 1), n = row / P.G, head = g.h * P.G + row % P.G;
             float m = NEG_INF, l = 0.f, rq = 0.f;
             bool any = false;
+            const bool idle = ri - lane >= rows;
             for (int tl = dual ? 0 : i; tl < nt; tl += dual ? 1 : 2) {
                 const int gt = g0 + tl, t = g.t0 + tl;
                 const float* meta = sh.meta[gt & (TC_META - 1)][0];
-                bar_wait(&sh.sf[i], cnt & 1, sh);
+                bar_wait(&sh.sf[i], cnt & 1, sh);          // first: with it, the scales' barrier is in this phase or the next
+                bar_wait(&sh.mf[gt & (TC_META - 1)], (gt / TC_META) & 1, sh);
                 tc_after();
-                if (!any) rq = sh.rq[seg & 3][ri];
+                const bool begins = !any;
+                if (begins) rq = sh.rq[seg & 3][ri];
+                any = true;
+                ++cnt;
+                if (idle) {                                               // no row in this warp: whatever P holds stays in its rows
+                    tc_before();
+                    bar_arrive(&sh.pf[i]);
+                    continue;
+                }
                 const int mode = t >= g.q.nct ? 2 : (t + 1) * TILE > g.q.full ? 1 : 0;
                 uint32_t mk[4] = {};
                 float mx;
@@ -873,7 +1052,7 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P) {
                     tile_mask(P, g, t, n, mk);
                     mx = mode == 1 ? tile_max<1>(s_col, meta, rq, mk) : tile_max<2>(s_col, meta, rq, mk);
                 }
-                if (!any) {
+                if (begins) {
                     m = mx;
                 } else if (__any_sync(FULL, mx > m + M_SLACK)) {
                     // the product before this tile's scores has ended: O can be rescaled
@@ -891,18 +1070,15 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P) {
                         tc_st32(o_col + i * D + c, o);
                     }
                 }
-                any = true;
                 const float sub = P_BIAS - (m == NEG_INF ? 0.f : m);
                 l += mode == 0 ? tile_probs<0>(s_col, meta, rq, mk, sub)
                      : mode == 1 ? tile_probs<1>(s_col, meta, rq, mk, sub) : tile_probs<2>(s_col, meta, rq, mk, sub);
                 tc_wait_st();
                 tc_before();
                 bar_arrive(&sh.pf[i]);
-                ++cnt;
             }
             if (any) {
-                bar_wait(&sh.pv[i], pvc & 1, sh);
-                ++pvc;
+                bar_wait(&sh.pv[i], (cnt - 1) & 1, sh);
                 tc_after();
             }
             // ---- the segment's rows: whole items are written out, parts go to the workspace
@@ -923,7 +1099,7 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P) {
                 c_hi = c_lo + D / 2;
             }
             const bool whole = g.t0 == 0 && g.t1 == g.q.ntiles;
-            const bool nan = g.q.bad || *reinterpret_cast<volatile int*>(&sh.bad_seg[seg & 3]) == seg + 1;
+            const bool nan = g.q.bad || *reinterpret_cast<volatile int*>(&sh.bad_seg[seg & 7]) == seg + 1;
             if (nan && r == 0) atomicOr(P.status, 1u << SPEC_ERR_DEVICE_INPUT);
             uint32_t bad_v = 0;
             if (g.t1 > g.q.nct) {
@@ -936,7 +1112,7 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P) {
             float* part = partial_of<D>(P, blockIdx.x, slot);
             const float quiet = __int_as_float(0x7fffffff);
 #pragma unroll 1
-            for (int c = c_lo; c < c_hi; c += 32) {
+            for (int c = c_lo; c < (idle ? c_lo : c_hi); c += 32) {
                 uint32_t o[32];
                 tc_ld32(o_col + (dual ? i * D : 0) + c, o);
                 tc_wait_ld();
@@ -964,7 +1140,7 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P) {
 #pragma unroll
                             for (int j = 0; j < 32; ++j) {
                                 const float x = __bfloat162float(vv[j]);
-                                if (!(fabsf(x) <= 3.402823466e38f)) o[j] = __float_as_uint(__uint_as_float(o[j]) + x);
+                                if (!(fabsf(x) <= 3.402823466e38f)) o[place(j)] = __float_as_uint(__uint_as_float(o[place(j)]) + x);
                             }
                         }
                     }
@@ -976,7 +1152,7 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P) {
                         for (int j = 0; j < 32; j += 8) {
                             float x[8];
 #pragma unroll
-                            for (int u = 0; u < 8; ++u) x[u] = nan ? quiet : __uint_as_float(o[j + u]) * inv;
+                            for (int u = 0; u < 8; ++u) x[u] = nan ? quiet : __uint_as_float(o[place(j + u)]) * inv;
                             dst[j / 8] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
                                                     pack_bf16(x[6], x[7]));
                         }
@@ -985,8 +1161,8 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P) {
 #pragma unroll
                         for (int j = 0; j < 32; j += 4)
                             dst[j / 4] = nan ? make_float4(quiet, quiet, quiet, quiet)
-                                             : make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]),
-                                                           __uint_as_float(o[j + 2]), __uint_as_float(o[j + 3]));
+                                             : make_float4(__uint_as_float(o[place(j)]), __uint_as_float(o[place(j + 1)]),
+                                                           __uint_as_float(o[place(j + 2)]), __uint_as_float(o[place(j + 3)]));
                     }
                 }
             }
@@ -998,31 +1174,9 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P) {
                     part[(int64_t)rows_of(P) * D + ri] = m == NEG_INF ? NEG_INF : m - P_BIAS;
                     part[(int64_t)rows_of(P) * D + rows_of(P) + ri] = nan ? quiet : l;
                 }
-                const int c0 = cta_of(g.item_lo, st.total, st.ctas);
-                const int c1 = cta_of(g.item_lo + g.q.ntiles - 1, st.total, st.ctas);
-                const int slot0 = stretch_at(st.total, c0, st.ctas) == g.item_lo ? 0 : 1;
-                // the last of the item's CTAs (for two streams: the last of each) puts it together
-                __threadfence();
-                if (dual) asm volatile("bar.sync %0, 128;" :: "r"(3 + i) : "memory");
-                else asm volatile("bar.sync 1, %0;" :: "n"(TC_SOFTMAX) : "memory");
-                if (r == 0 && (dual || i == 0)) {
-                    const unsigned got = atomicAdd(P.item_cnt + 2 * c0 + (dual ? i : 0), 1u);
-                    const int is_last = got == (unsigned)(c1 - c0);
-                    if (is_last) P.item_cnt[2 * c0 + (dual ? i : 0)] = 0;
-                    __threadfence();
-                    sh.last[dual ? i : 0] = is_last;
-                }
-                if (dual) asm volatile("bar.sync %0, 128;" :: "r"(3 + i) : "memory");
-                else asm volatile("bar.sync 1, %0;" :: "n"(TC_SOFTMAX) : "memory");
-                if (*reinterpret_cast<volatile int*>(&sh.last[dual ? i : 0])) {
-                    __threadfence();
-                    const int first = dual ? i * 128 + (warp & 3) : warp, upto = dual ? min(rows, i * 128 + 128) : rows;
-                    for (int q = first; q < upto; q += dual ? 4 : 8) {
-                        const int row2 = g.mt * 256 + q;
-                        const int64_t o2 = ((int64_t)g.b * P.N + row2 / P.G) * P.Hq + g.h * P.G + row2 % P.G;
-                        merge_row<D>(P, q, rows_of(P), c0, slot0, c1 - c0 + 1, lane, P.out + o2 * D * 2,
-                                     P.lse ? P.lse + o2 : nullptr);
-                    }
+                if (g.t0 == 0 && tid == 0) {
+                    const int c1 = cta_of(g.item_lo + g.q.ntiles - 1, st.total, st.ctas);
+                    P.cut[blockIdx.x] = Cut{g.b, g.h, g.mt, c1 - (int)blockIdx.x + 1, slot};
                 }
             }
             // the next segment's products may write O again once every reader is through
@@ -1032,10 +1186,75 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P) {
         }
     }
     __syncthreads();
-    if (warp == TC_BT / 32 - 1) {
+    if (warp == TC_W_MMA) {
         tc_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tmem));
         if (lane == 0 && sh.abort) atomicOr(P.status, 1u << SPEC_ERR_TIMEOUT);
+    }
+}
+
+// Puts the cut items together: block x the item that CTA x began, one warp per
+// row, lane p the maximum and sum of part p.  Bound by latency: the parts lie in L2.
+constexpr int MERGE_BT = 256, MERGE_ROWS = 32;
+
+template <int D>
+__global__ void __launch_bounds__(MERGE_BT) k_attention_merge(const Att P) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Cut cut = P.cut[blockIdx.x];
+    const int lane = threadIdx.x & 31, rows = rows_of(P);
+    const int upto = min(min(rows, P.R - cut.mt * 256), (int)(blockIdx.y + 1) * MERGE_ROWS);
+    if (cut.parts == 0) return;
+    constexpr int E = D / 32;
+    for (int r = blockIdx.y * MERGE_ROWS + (threadIdx.x >> 5); r < upto; r += MERGE_BT / 32) {
+        auto part = [&](int i) { return partial_of<D>(P, blockIdx.x + i, i == 0 ? cut.slot0 : 0); };
+        float M = NEG_INF, m0 = NEG_INF, l0 = 0.f;
+        for (int i = lane; i < cut.parts; i += 32) {
+            const float* p = part(i) + (int64_t)rows * D;
+            const float m = __ldcg(p + r), s = __ldcg(p + rows + r);
+            if (i == lane) m0 = m, l0 = s;
+            M = fmaxf(M, m);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+        const float base = M == NEG_INF ? 0.f : M;
+        float acc[E] = {}, l = 0.f;
+        for (int i0 = 0; i0 < cut.parts; i0 += 32) {
+            if (i0) {
+                m0 = NEG_INF, l0 = 0.f;
+                if (i0 + lane < cut.parts) {
+                    const float* p = part(i0 + lane) + (int64_t)rows * D;
+                    m0 = __ldcg(p + r);
+                    l0 = __ldcg(p + rows + r);
+                }
+            }
+            const float w = ex2(m0 - base);
+            l = fmaf(w, l0, l);
+            const int n = min(32, cut.parts - i0);
+#pragma unroll 8
+            for (int i = 0; i < n; ++i) {
+                const float wi = __shfl_sync(FULL, w, i);
+                const float* p = part(i0 + i) + (int64_t)r * D + lane * E;
+                if constexpr (E == 4) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
+                    acc[0] = fmaf(wi, x.x, acc[0]); acc[1] = fmaf(wi, x.y, acc[1]);
+                    acc[2] = fmaf(wi, x.z, acc[2]); acc[3] = fmaf(wi, x.w, acc[3]);
+                } else {
+                    const float2 x = __ldcg(reinterpret_cast<const float2*>(p));
+                    acc[0] = fmaf(wi, x.x, acc[0]); acc[1] = fmaf(wi, x.y, acc[1]);
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(FULL, l, o);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int row = cut.mt * 256 + r, n = row / P.G;
+        const int64_t at = ((int64_t)cut.b * P.N + n) * P.Hq + cut.h * P.G + row - n * P.G;
+        char* out = P.out + at * D * 2;
+        if constexpr (E == 4)
+            reinterpret_cast<uint2*>(out)[lane] = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+        else
+            reinterpret_cast<uint32_t*>(out)[lane] = pack_bf16(acc[0] * inv, acc[1] * inv);
+        if (P.lse && lane == 0) P.lse[at] = l == 0.f ? NEG_INF : (base + log2f(l)) * LN2;
     }
 }
 
@@ -1148,12 +1367,57 @@ namespace {
 constexpr int ATT_CTAS = 148;             // CTAs at most: one per SM
 
 template <int D>
+spec_status launch_merge(const Att& P, int ctas, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, (unsigned)((P.R < 256 ? P.R : 256) + MERGE_ROWS - 1) / MERGE_ROWS);
+    cfg.blockDim = dim3(MERGE_BT);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_attention_merge<D>, P);
+    if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "k_attention_merge launch: %s", cudaGetErrorString(e));
+    return sv_host::launched("k_attention_merge");
+}
+
+// The cache's keys as a matrix of 8-bit rows: a box is one page of one head.
+template <int D>
+spec_status key_map(const Att& P, CUtensorMap* map) {
+    static std::atomic<void*> entry{nullptr};
+    void* f = entry.load(std::memory_order_acquire);
+    if (!f) {
+        cudaDriverEntryPointQueryResult found;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+        if (e != cudaSuccess || found != cudaDriverEntryPointSuccess || !f)
+            return fail(SPEC_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+        entry.store(f, std::memory_order_release);
+    }
+    const bool empty = P.c.num_pages == 0;                // nothing is copied then: any address serves
+    const cuuint64_t dims[2] = {(cuuint64_t)D, empty ? (cuuint64_t)P.page : (cuuint64_t)P.c.num_pages * P.Hkv * P.page};
+    const cuuint64_t strides[1] = {(cuuint64_t)D};
+    const cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)P.page}, step[2] = {1, 1};
+    const CUresult r = reinterpret_cast<CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                                     const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                                     CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill)>(f)(
+        map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, empty ? static_cast<void*>(P.out) : P.c.k_pages, dims, strides, box, step,
+        CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(SPEC_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", (int)r);
+    return SPEC_OK;
+}
+
+template <int D>
 spec_status launch_tc(const Att& P, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(k_attention_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tc_smem<D>());
     if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "k_attention_tc: %s", cudaGetErrorString(e));
     const int ctas = sv_host::num_sms() < ATT_CTAS ? sv_host::num_sms() : ATT_CTAS;
-    k_attention_tc<D><<<ctas, TC_BT, tc_smem<D>(), st>>>(P);
-    return sv_host::launched("k_attention_tc");
+    CUtensorMap kmap;
+    if (const spec_status s = key_map<D>(P, &kmap)) return s;
+    k_attention_tc<D><<<ctas, TC_BT, tc_smem<D>(), st>>>(P, kmap);
+    const spec_status s = sv_host::launched("k_attention_tc");
+    return s == SPEC_OK ? launch_merge<D>(P, ctas, st) : s;
 }
 
 }  // namespace
@@ -1197,6 +1461,7 @@ spec_status spec_tree_attention(int B, int N, int q_heads, const spec_kv_cache* 
     P.R = N * P.G;
     P.mtiles = (P.R + 255) / 256;
     P.page = cache->page_size;
+    P.pshift = __builtin_ctz(P.page);
     P.c = *cache;
     P.anc = reinterpret_cast<const uint32_t*>(ancestors);
     P.scale = (float)((double)scale * 1.4426950408889634073599);
@@ -1204,7 +1469,7 @@ spec_status spec_tree_attention(int B, int N, int q_heads, const spec_kv_cache* 
     P.lse = lse;
     char* ws = static_cast<char*>(workspace);
     P.status = reinterpret_cast<unsigned*>(ws + sv_host::CACHE_WS_STATUS);
-    P.item_cnt = reinterpret_cast<unsigned*>(ws + sv_host::CACHE_WS_ITEM);
+    P.cut = reinterpret_cast<Cut*>(ws + sv_host::CACHE_WS_CUT);
     P.partial = reinterpret_cast<float*>(ws + sv_host::CACHE_WS_PARTIAL);
     const int64_t rows = (int64_t)B * N * q_heads;
     cudaStream_t st = static_cast<cudaStream_t>(stream);

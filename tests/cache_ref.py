@@ -124,14 +124,25 @@ def row_scale(x):
     return torch.where(a > 0, torch.ldexp(torch.ones_like(a), e - 1), torch.ones_like(a))
 
 
-def attention(q, k, v, keys, values, mask, scale, vscale):
+def small_part(x):
+    """Per element, what a row loses when it is held as two e4m3 rows after its largest magnitude was brought to
+    [2^7, 2^8): 2^-10 of that scale, for elements below 2^-2 of it only (the others have their eight bits)."""
+    unit = row_scale(x) * 2.0 ** -7
+    a = torch.nan_to_num(x, 0, 0, 0).abs()
+    return torch.where(a < unit[..., None] * 0.25, torch.minimum(a, unit[..., None] * 2.0 ** -10), torch.zeros_like(a))
+
+
+def attention(q, k, v, keys, values, mask, scale, vscale, full):
     """One sequence: q [N, Hq, D], nodes k/v [N, Hkv, D], cached keys/values [L, Hkv, D], mask [N, N],
-    vscale [L, Hkv] the scales of the cached values.  All f64.  Returns out, lse, sum p |v|, max over
-    keys of scale * sum |q| |k|, and max p s * sum |v| / s over the keys' value scales s."""
+    vscale [L, Hkv] the scales of the cached values, full: the tokens in 8-bit blocks.  All f64.  Returns
+    out, lse, sum p |v|, max over keys of scale * sum |q| |k|, max p s * sum |v| / s over the keys' value
+    scales s, and max over keys of scale * (what the rows' small elements can lose)."""
     N, Hq, D = q.shape
     G = Hq // k.shape[1]
     K = torch.cat((keys, k)).repeat_interleave(G, 1)          # [T, Hq, D]
     V = torch.cat((values, v)).repeat_interleave(G, 1)
+    loss = torch.cat((torch.zeros_like(K[:full]), small_part(K[full:])))
+    lost = (torch.einsum("nhd,thd->nht", small_part(q), K.abs()) + torch.einsum("nhd,thd->nht", q.abs(), loss)) * scale
     see = torch.cat((torch.ones(N, keys.shape[0], dtype=torch.bool), mask), 1)[:, None].expand(N, Hq, -1)
     s = torch.einsum("nhd,thd->nht", q, K) * scale
     mag = torch.einsum("nhd,thd->nht", q.abs(), K.abs()) * scale
@@ -148,7 +159,8 @@ def attention(q, k, v, keys, values, mask, scale, vscale):
     S = torch.cat((vscale, row_scale(v))).repeat_interleave(G, 1)     # [T, Hq]
     lead = (w * S.T).amax(-1)                                         # [N, Hq]
     small = lead[..., None] * torch.einsum("nht,thd->nhd", see.double(), vabs / S[..., None])
-    return out, (torch.log(total) + top)[..., 0], torch.einsum("nht,thd->nhd", w, vabs), mag, small
+    lost = torch.where(see, lost, torch.zeros_like(lost)).amax(-1)
+    return out, (torch.log(total) + top)[..., 0], torch.einsum("nht,thd->nhd", w, vabs), mag, small, lost
 
 
 def inv_freq(rot, base=1e6):

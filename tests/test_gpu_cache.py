@@ -12,7 +12,10 @@ error of each probability times sum p|v|, plus the final rounding.  f16 has no
 steps below 2^-24: with the keys' value scales s_j, the kernel rounds
 P_j = 2^11 p_j s_j / max(p s) (or more), so below f16's normal numbers p_j s_j is
 off by up to 2^-25 / 2^11 of max(p s); the sum over keys of that times
-|v_j| / s_j is 2^-36 max(p s) sum |v| / s.
+|v_j| / s_j is 2^-36 max(p s) sum |v| / s.  And a query (and a key that is not yet
+in 8 bits) may be held as two e4m3 rows: exact but for its elements below 2^-9 of its
+largest, which are rounded at 2^-10 of e4m3's scale; the products of that with
+the other side are added to a score's error.
 """
 import math
 
@@ -358,8 +361,9 @@ def check_attention(r, lengths, q, k, v, mask, out, lse, scale):
             vscale = torch.cat((s.repeat_interleave(r.page, 0), ref.row_scale(r.open_rows(b, which).double())))
             full = (e.view(F8).double() * s[..., None, None]).transpose(1, 2).reshape(-1, r.H, r.D)
             side.append(torch.cat((full, r.open_rows(b, which).double())))
-        e, el, pv, mag, small = ref.attention(q[b].double(), k[b].double(), v[b].double(), *side, mask[b], scale, vscale)
-        ds = (r.D + 8) * 2.0 ** -23 * mag
+        full = max(lengths[b], 0) // r.page * r.page
+        e, el, pv, mag, small, lost = ref.attention(q[b].double(), k[b].double(), v[b].double(), *side, mask[b], scale, vscale, full)
+        ds = (r.D + 8) * 2.0 ** -23 * mag + lost
         # the probabilities' own rounding, the scores' (in numerator and sum), the exponentials' (2^-21)
         rel = 2.0 ** -11 + 2 * ds + 2.0 ** -20
         tol = e.abs() * 2.0 ** -8 + pv * rel[..., None] + small * 2.0 ** -36 + 1e-38
