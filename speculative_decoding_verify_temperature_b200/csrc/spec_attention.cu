@@ -206,10 +206,10 @@ __device__ __forceinline__ uint32_t tail_bits(const Att& P, int b, int n, int op
 
 // ----------------------------------------------------------------------------- tensor-core kernel (tcgen05)
 
-// Roles of the CTA's warps: 0-3 and 4-7 the softmax of one stream each, 8-11 make
-// operands (f16 values from e4m3 bytes, queries, the tail), 12 issues the matrix
-// instructions (one thread), 13 copies pages to shared memory, 14 gathers the
-// pages' scales, 15 nothing.
+// Roles of the CTA's warps: 0-3 and 4-7 the softmax of one stream each, 8-15 make
+// operands (f16 values from e4m3 bytes, queries, the tail), 16 issues the matrix
+// instructions (one thread), 17 copies pages to shared memory, 18 gathers the
+// pages' scales, 19 nothing.
 //
 // An item holds up to 256 rows.  With more than 128 the two streams are its two
 // halves and both take every tile; with 128 or fewer both streams hold the same
@@ -237,8 +237,8 @@ __device__ __forceinline__ uint32_t tail_bits(const Att& P, int b, int n, int op
 // leading P whatever the blocks' scales are.  O is rescaled only when M grows by
 // more than 2^4; P_BIAS lifts P to at most 2^15, so that f16's smallest step is
 // 2^-35 of the leading one.
-constexpr int TC_SOFTMAX = 256, TC_CONV = 128, TC_BT = 512;
-constexpr int TC_W_CONV = 8, TC_W_MMA = 12, TC_W_COPY = 13, TC_W_SCALE = 14;
+constexpr int TC_SOFTMAX = 256, TC_CONV = 256, TC_BT = 640;
+constexpr int TC_W_CONV = 8, TC_W_MMA = 16, TC_W_COPY = 17, TC_W_SCALE = 18;
 constexpr int TC_META = 4;                // tiles whose scales are kept
 constexpr float P_BIAS = 11.f, M_SLACK = 4.f;
 
@@ -520,7 +520,33 @@ __device__ void tc_copy_pages(const Att& P, const CUtensorMap* kmap, TcShared& s
         if (!bar_try(&sh.rf[i % VR], (i / VR) & 1)) bar_wait_slow(&sh.rf[i % VR], (i / VR) & 1, nullptr);
 }
 
+__device__ __forceinline__ void prefetch_row(const char* p, int bytes) {
+    for (int i = 0; i < bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" :: "l"(p + i));
+}
+// Rows that a segment's loads will ask for one after the other, on their way to L2 long before: its tail, and the
+// queries of the segment after it.
+template <int D>
+__device__ void prefetch_segment(const Att& P, const TileIter& u, int lane) {
+    const Seg& g = u.g;
+    if (g.t1 > g.q.nct && g.q.len >= 0 && !g.q.bad) {
+        const int64_t ring = ((int64_t)g.q.slot * P.Hkv + g.h) * 2 * P.page;
+        for (int e = lane; e < g.q.open + P.N; e += 32) {
+            const int64_t at = (ring + ((g.q.full + e) & (2 * P.page - 1))) * D * 2, n = e - g.q.open;
+            prefetch_row(e < g.q.open ? static_cast<const char*>(P.c.k_open) + at : P.k.p + g.b * P.k.b + n * P.k.n + g.h * P.k.h, D * 2);
+            prefetch_row(e < g.q.open ? static_cast<const char*>(P.c.v_open) + at : P.v.p + g.b * P.v.b + n * P.v.n + g.h * P.v.h, D * 2);
+        }
+    }
+    SegIter it = u.it;
+    Seg s;
+    if (!it.next(P, s)) return;
+    for (int r = s.mt * 256 + lane; r < min(P.R, s.mt * 256 + 256); r += 32) {
+        const int n = r / P.G;
+        prefetch_row(P.q.p + s.b * P.q.b + n * P.q.n + (s.h * P.G + r - n * P.G) * P.q.h, D * 2);
+    }
+}
+
 // The warp that gathers the scales of the cached tiles' groups of 16 keys, a tile ahead.
+template <int D>
 __device__ __forceinline__ void tc_scales(const Att& P, TcShared& sh, const Stretch& st, int lane) {
     TileIter u;
     u.begin(P, st);
@@ -537,7 +563,10 @@ __device__ __forceinline__ void tc_scales(const Att& P, TcShared& sh, const Stre
     };
     float ks = 1.f, vs = 1.f;
     bool more = u.next(P);
-    if (more) fetch(u.g, u.t, ks, vs);
+    if (more) {
+        fetch(u.g, u.t, ks, vs);
+        prefetch_segment<D>(P, u, lane);
+    }
     while (more) {
         const int m = u.gt & (TC_META - 1);
         const uint32_t par = ((u.gt / TC_META) & 1) ^ 1;
@@ -545,6 +574,7 @@ __device__ __forceinline__ void tc_scales(const Att& P, TcShared& sh, const Stre
         const float k0 = ks, v0 = vs * 256.f;             // the f16 values are 2^-8 of the bytes
         more = u.next(P);
         if (more) fetch(u.g, u.t, ks, vs);
+        if (more && u.first()) prefetch_segment<D>(P, u, lane);
         bar_wait(&sh.me[m], par, sh);
         if (!cached) continue;                            // the operand warps write the tail's
         if (lane < 8) {
@@ -609,134 +639,160 @@ struct TcConv {
                 asm volatile("st.shared.b16 [%0], %1;" :: "r"(swz(half, r, (c % 4) * 2 + p / 8) + (p & 7) * 2), "h"((uint16_t)0x7e00) : "memory");
         }
     }
-    // Eight bf16 elements of a row in each of D / 8 lanes: the row's power of two, with its non-finite elements
-    // reported and (zero_bad) zeroed.
-    __device__ __forceinline__ int scale_row(float (&x)[8], bool& bad, bool zero_bad) {
-        float amax = 0.f;
-        bad = false;
+    // Eight bf16 elements of a row in each of D / 8 lanes: the row's power of two, from the bits of its finite
+    // magnitudes.  An element that is not finite is made 0 (a NaN with keep_nan) and reported.
+    __device__ __forceinline__ int scale_row(uint4& w, bool& bad, bool keep_nan) {
+        uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+        bad = (m & 0xffffu) >= 0x7f80u || m >= 0x7f800000u;
+        if (bad) m = strip(w, keep_nan);
+        m = max(m & 0xffffu, m >> 16);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            amax = fmaxf(amax, finite_abs(x[i]));
-            if (!(fabsf(x[i]) <= 3.402823466e38f)) {
-                bad = true;
-                if (zero_bad) x[i] = 0.f;
+        for (int o = D / 16; o; o >>= 1) m = max(m, __shfl_xor_sync(FULL, m, o));
+        return m ? max((int)(m >> 7), 7) - 127 : 0;       // -120 to 127
+    }
+    static __device__ __noinline__ uint32_t strip(uint4& w, bool keep_nan) {
+        uint32_t x[4] = {w.x, w.y, w.z, w.w}, m = 0;
+        for (int i = 0; i < 4; ++i)
+            for (int s = 0; s < 32; s += 16) {
+                const uint32_t a = (x[i] >> s) & 0x7fffu;
+                if (a >= 0x7f80u) x[i] = (x[i] & ~(0xffffu << s)) | (keep_nan ? 0x7fffu << s : 0u);
+                else m = max(m, a);
             }
-        }
-#pragma unroll
-        for (int o = D / 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, o));
-        return pow2_of(amax);
+        w = make_uint4(x[0], x[1], x[2], x[3]);
+        return m;
+    }
+    // The row times 2^e in f16: exact but for what lies below f16's smallest step.
+    __device__ __forceinline__ void to_f16(const uint4& w, int e, uint32_t (&h)[4]) {
+        const float s = exp2i(e);
+        h[0] = pack_f16(bf_lo(w.x) * s, bf_hi(w.x) * s);
+        h[1] = pack_f16(bf_lo(w.y) * s, bf_hi(w.y) * s);
+        h[2] = pack_f16(bf_lo(w.z) * s, bf_hi(w.z) * s);
+        h[3] = pack_f16(bf_lo(w.w) * s, bf_hi(w.w) * s);
     }
     // f16 value row r.
-    __device__ __forceinline__ void put_value_row(uint32_t dst, int r, int l, const float (&x)[8], int e) {
-        const float s = exp2i(-e);
+    __device__ __forceinline__ void put_value_row(uint32_t dst, int r, int l, const uint4& w, int e) {
+        uint32_t h[4];
+        to_f16(w, -e, h);
         sts128(swz(dst + (l / 8) * Tc<D>::HALF, r, l % 8),
-               make_uint4(pack_f16(x[0] * s, x[2] * s), pack_f16(x[1] * s, x[3] * s), pack_f16(x[4] * s, x[6] * s),
-                          pack_f16(x[5] * s, x[7] * s)));
+               make_uint4(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[0], h[1], 0x7632), __byte_perm(h[2], h[3], 0x5410),
+                          __byte_perm(h[2], h[3], 0x7632)));
     }
-    // The two e4m3 rows of a bf16 row divided by 2^(e - 7); infinities become NaN.
-    __device__ __forceinline__ void split_row(const float (&x)[8], int e, uint2& hi, uint2& lo) {
-        const float s = exp2i(-e) * 128.f;
-        uint32_t h[4], w[4];
+    // The two e4m3 rows of a bf16 row divided by 2^(e - 7); the second's elements are exact differences.
+    __device__ __forceinline__ void split_row(const uint4& w, int e, uint2& hi, uint2& lo) {
+        uint32_t h[4], a[4], b[4];
+        to_f16(w, 7 - e, h);
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            float a = x[i] * s, b = x[i + 1] * s;
-            if (!(fabsf(x[i]) <= 3.402823466e38f)) a = __int_as_float(0x7fffffff);
-            if (!(fabsf(x[i + 1]) <= 3.402823466e38f)) b = __int_as_float(0x7fffffff);
-            h[i / 2] = pack_e4m3(a, b);
-            uint32_t f;
-            asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(f) : "r"(h[i / 2]));
-            float fa, fb;
-            asm("{\n\t.reg .b16 p, q;\n\tmov.b32 {p, q}, %2;\n\tcvt.f32.f16 %0, p;\n\tcvt.f32.f16 %1, q;\n\t}" : "=f"(fa), "=f"(fb) : "r"(f));
-            w[i / 2] = pack_e4m3(a - fa, b - fb);
+        for (int i = 0; i < 4; ++i) {
+            asm("{\n\t.reg .b16 p, q;\n\t.reg .b32 f, d;\n\tcvt.rn.satfinite.e4m3x2.f16x2 p, %2;\n\tcvt.rn.f16x2.e4m3x2 f, p;\n\t"
+                "sub.f16x2 d, %2, f;\n\tcvt.rn.satfinite.e4m3x2.f16x2 q, d;\n\tcvt.u32.u16 %0, p;\n\tcvt.u32.u16 %1, q;\n\t}"
+                : "=r"(a[i]), "=r"(b[i]) : "r"(h[i]));
         }
-        hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-        lo = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+        hi = make_uint2(a[0] | a[1] << 16, a[2] | a[3] << 16);
+        lo = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+    }
+    // Rows are loaded two passes ahead of their use, in a loop that stays small: this code runs once per item, and
+    // unrolled it cost more in instruction fetches (30000 cycles a tail tile) than all it computes.
+    __device__ __forceinline__ void load_q(const Seg& g, int rows, int p, Vec8<SPEC_BF16>& w) {
+        const int r = min(tid / LPR + p * RP, rows - 1);  // rows behind the last repeat it
+        const int row = g.mt * 256 + r, n = row / P.G, h = g.h * P.G + row - n * P.G;
+        w.load_plain(P.q.p + g.b * P.q.b + n * P.q.n + h * P.q.h + 16 * (tid % LPR));
+    }
+    __device__ __forceinline__ void put_q_row(Vec8<SPEC_BF16> w, int p, float* rq) {
+        const int l = tid % LPR, r = tid / LPR + p * RP;
+        bool bad;
+        const int e = scale_row(w.a, bad, true);
+        uint2 hi, lo;
+        split_row(w.a, e, hi, lo);
+        const uint32_t dst = base + Tc<D>::Q + (r / 128) * Tc<D>::Q_B;
+        // D = 128: two tiles of 128-byte rows; 64: side by side
+        sts64(swz(dst, r % 128, l / 2) + (l & 1) * 8, hi);
+        sts64((D == 128 ? swz(dst + Tc<D>::RAW_B, r % 128, l / 2) : swz(dst, r % 128, 4 + l / 2)) + (l & 1) * 8, lo);
+        if (l == 0) rq[r] = exp2i(e) * (P.scale * 0.0078125f);
     }
     __device__ __forceinline__ void put_q(const Seg& g, int seg) {
-        const int l = tid % LPR;
-        const int rows = min(256, P.R - g.mt * 256);
+        // the rows behind the last are whatever they are: their results are not looked at
+        const int rows = min(256, P.R - g.mt * 256), np = (rows + 2 * RP - 1) / (2 * RP) * 2;
+        float* rq = sh.rq[seg & 3];
+        Vec8<SPEC_BF16> a, b;
+        load_q(g, rows, 0, a);
+        load_q(g, rows, 1, b);
 #pragma unroll 1
-        for (int p0 = 0; p0 < (rows > 128 ? 2 * NB : NB); p0 += 8) {
-            Vec8<SPEC_BF16> w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = tid / LPR + (p0 + i) * RP, row = g.mt * 256 + r, n = row / P.G, h = g.h * P.G + row - n * P.G;
-                w[i].zero();
-                if (r < rows) w[i].load(P.q.p + g.b * P.q.b + n * P.q.n + h * P.q.h + 16 * l);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = tid / LPR + (p0 + i) * RP;
-                float x[8];
-                w[i].get(x);
-                bool bad;
-                const int e = scale_row(x, bad, false);
-                uint2 hi, lo;
-                split_row(x, e, hi, lo);
-                const uint32_t dst = base + Tc<D>::Q + (r / 128) * Tc<D>::Q_B;
-                if (D == 128) {                           // two tiles of 128-byte rows
-                    sts64(swz(dst, r % 128, l / 2) + (l & 1) * 8, hi);
-                    sts64(swz(dst + Tc<D>::RAW_B, r % 128, l / 2) + (l & 1) * 8, lo);
-                } else {                                  // side by side
-                    sts64(swz(dst, r % 128, l / 2) + (l & 1) * 8, hi);
-                    sts64(swz(dst, r % 128, 4 + l / 2) + (l & 1) * 8, lo);
-                }
-                if (l == 0) sh.rq[seg & 3][r] = exp2i(e) * (P.scale * 0.0078125f);
-            }
+        for (int p = 0; p < np; p += 2) {
+            const Vec8<SPEC_BF16> a0 = a, b0 = b;
+            load_q(g, rows, p + 2, a);                    // behind the last pass: the last row again
+            load_q(g, rows, p + 3, b);
+            put_q_row(a0, p, rq);
+            put_q_row(b0, p + 1, rq);
         }
     }
-    // Eight passes of the tail's rows, from pass p0 on: open tokens from the ring, then the nodes.
-    __device__ __forceinline__ void load_tail(const TileIter& u, int which, int p0, Vec8<SPEC_BF16> (&w)[8]) {
+    // Row e of the tail: open tokens from the ring, then the nodes.  One load for every row, from a place that is
+    // there (a query where there is no key): a branch per row would wait for each load in turn.
+    __device__ __forceinline__ void load_tail(const TileIter& u, int p, Vec8<SPEC_BF16>& k, Vec8<SPEC_BF16>& v) {
         const int l = tid % LPR;
         const Seq& q = u.g.q;
-        const bool live = q.len >= 0 && !q.bad;
-        const char* ring = static_cast<const char*>(which ? P.c.v_open : P.c.k_open) +
-                           ((int64_t)q.slot * P.Hkv + u.g.h) * 2 * P.page * D * 2;
-        const sv_host::Rows& src = which ? P.v : P.k;
-        const int e0 = (u.t - q.nct) * TILE, keys = q.open + P.N;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int e = e0 + tid / LPR + (p0 + i) * RP;
-            w[i].zero();
-            if (live && e < q.open) w[i].load_plain(ring + ((int64_t)((q.full + e) & (2 * P.page - 1)) * D + 8 * l) * 2);
-            else if (live && e < keys) w[i].load(src.p + u.g.b * src.b + (e - q.open) * src.n + u.g.h * src.h + 16 * l);
+        const int e = (u.t - q.nct) * TILE + tid / LPR + p * RP;
+        const bool in = q.len >= 0 && !q.bad && e < q.open + P.N;
+        const bool open = e < q.open;
+        const int64_t at = ((((int64_t)q.slot * P.Hkv + u.g.h) * 2 * P.page + ((q.full + e) & (2 * P.page - 1))) * D) * 2;
+        const int64_t n = e - q.open;
+        const char* kp = open ? static_cast<const char*>(P.c.k_open) + at : P.k.p + u.g.b * P.k.b + n * P.k.n + u.g.h * P.k.h;
+        const char* vp = open ? static_cast<const char*>(P.c.v_open) + at : P.v.p + u.g.b * P.v.b + n * P.v.n + u.g.h * P.v.h;
+        k.load_plain((in ? kp : P.q.p) + 16 * l);
+        v.load_plain((in ? vp : P.q.p) + 16 * l);
+        if (!in) {
+            k.zero();
+            v.zero();
+        }
+    }
+    __device__ __forceinline__ void put_tail_row(const TileIter& u, Vec8<SPEC_BF16> k, Vec8<SPEC_BF16> v, int p, uint32_t khi,
+                                                 uint32_t klo, uint32_t vd, float* meta) {
+        const int l = tid % LPR, r = tid / LPR + p * RP;
+        bool bad;
+        const int ve = min(scale_row(v.a, bad, false), 126);   // what is not finite reaches its rows at the end
+        if (bad) {
+            const int e = (u.t - u.g.q.nct) * TILE + r;
+            atomicOr(&sh.bad_v[u.seg & 3][e >> 5], 1u << (e & 31));
+        }
+        put_value_row(vd, r, l, v.a, ve);
+        const int ke = scale_row(k.a, bad, true);
+        uint2 hi, lo;
+        split_row(k.a, ke, hi, lo);
+        sts64(key_at(khi, r, l), hi);
+        sts64(key_at(klo, r, l), lo);
+        if (l == 0) {
+            meta[r] = exp2i(ke) * 0.0078125f;
+            meta[TILE + r] = (float)ve;
+            meta[2 * TILE + r] = exp2i(-ve);
         }
     }
     // A tile of the tail: its two units of keys, its values and all of its scales.
     __device__ __forceinline__ void tail(const TileIter& u, int nk) {
         constexpr int KR = Tc<D>::KR;
-        const int l = tid % LPR, e0 = (u.t - u.g.q.nct) * TILE, m = u.gt & (TC_META - 1);
+        const int m = u.gt & (TC_META - 1);
         const int k0 = nk % KR, k1 = (nk + 1) % KR;
+        Vec8<SPEC_BF16> ka, va, kb, vb;
+        load_tail(u, 0, ka, va);
+        load_tail(u, 1, kb, vb);
         bar_wait(&sh.me[m], ((u.gt / TC_META) & 1) ^ 1, sh);
         bar_wait(&sh.ke[k0], ((nk / KR) & 1) ^ 1, sh);
         bar_wait(&sh.ke[k1], (((nk + 1) / KR) & 1) ^ 1, sh);
         bar_wait(&sh.ve[u.gt & 1], ((u.gt >> 1) & 1) ^ 1, sh);
+        const uint32_t khi = base + Tc<D>::K + k0 * Tc<D>::RAW_B, klo = base + Tc<D>::K + k1 * Tc<D>::RAW_B;
+        const uint32_t vd = base + Tc<D>::V + (u.gt & 1) * Tc<D>::V_B;
+        float* meta = sh.meta[m][0];
+        // rows behind the last key: their scores are masked, their values have to be finite
+        const int keys = u.g.q.len >= 0 && !u.g.q.bad ? min(TILE, u.g.q.open + P.N - (u.t - u.g.q.nct) * TILE) : 0;
+        const int np = (keys + 2 * RP - 1) / (2 * RP) * 2;
+        for (int i = np * RP * (D / 8) + tid; i < TILE * (D / 8); i += TC_CONV)
+            sts128(swz(vd + (i % (D / 8) / 8) * Tc<D>::HALF, i / (D / 8), i % 8), make_uint4(0, 0, 0, 0));
+        for (int r = np * RP + tid; r < TILE; r += TC_CONV) meta[r] = meta[TILE + r] = meta[2 * TILE + r] = 1.f;
 #pragma unroll 1
-        for (int p0 = 0; p0 < NB; p0 += 8) {
-            Vec8<SPEC_BF16> k[8], v[8];
-            load_tail(u, 0, p0, k);
-            load_tail(u, 1, p0, v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = tid / LPR + (p0 + i) * RP;
-                float x[8];
-                bool bad;
-                v[i].get(x);
-                const int ve = scale_row(x, bad, true);   // what is not finite reaches its rows at the end
-                if (bad) atomicOr(&sh.bad_v[u.seg & 3][(e0 + r) >> 5], 1u << ((e0 + r) & 31));
-                put_value_row(base + Tc<D>::V + (u.gt & 1) * Tc<D>::V_B, r, l, x, ve);
-                k[i].get(x);
-                const int ke = scale_row(x, bad, false);
-                uint2 hi, lo;
-                split_row(x, ke, hi, lo);
-                sts64(key_at(base + Tc<D>::K + k0 * Tc<D>::RAW_B, r, l), hi);
-                sts64(key_at(base + Tc<D>::K + k1 * Tc<D>::RAW_B, r, l), lo);
-                if (l == 0) {
-                    sh.meta[m][0][r] = exp2i(ke) * 0.0078125f;
-                    sh.meta[m][1][r] = (float)ve;
-                    sh.meta[m][2][r] = exp2i(-ve);
-                }
-            }
+        for (int p = 0; p < np; p += 2) {
+            const Vec8<SPEC_BF16> k2 = ka, v2 = va, k3 = kb, v3 = vb;
+            load_tail(u, p + 2, ka, va);
+            load_tail(u, p + 3, kb, vb);
+            put_tail_row(u, k2, v2, p, khi, klo, vd, meta);
+            put_tail_row(u, k3, v3, p + 1, khi, klo, vd, meta);
         }
         proxy_fence();
         asm volatile("bar.sync 2, %0;" :: "n"(TC_CONV) : "memory");
@@ -937,7 +993,7 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
     } else if (warp == TC_W_COPY) {
         tc_copy_pages<D>(P, &kmap, sh, base, st, lane);
     } else if (warp == TC_W_SCALE) {
-        tc_scales(P, sh, st, lane);
+        tc_scales<D>(P, sh, st, lane);
     } else if (warp == TC_W_MMA) {
         // ---- matrix instructions
         if (lane == 0) {
