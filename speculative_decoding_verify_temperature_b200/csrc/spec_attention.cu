@@ -432,18 +432,7 @@ __host__ __device__ constexpr uint32_t tc_idesc(int n, bool b_n_major) {
 // Address of 16-byte chunk q (0-7) of row r within a 64-column half.
 __device__ __forceinline__ uint32_t swz(uint32_t half, int r, int q) { return half + r * 128 + ((q ^ (r & 7)) << 4); }
 
-// Power of two that brings the finite magnitude amax to [1, 2) (to [2, 4) at the
-// very top of f32's range); 1 for zero.
-__device__ __forceinline__ int pow2_of(float amax) {
-    const int e = (int)(__float_as_uint(amax) >> 23) - 127;
-    return amax > 0.f ? min(max(e, -126), 126) : 0;
-}
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126..127
-
-__device__ __forceinline__ float finite_abs(float x) {
-    const float a = fabsf(x);
-    return a <= 3.402823466e38f ? a : 0.f;
-}
 
 __device__ __forceinline__ bool is_dual(const Att& P, int mt) { return P.R - mt * 256 > 128; }
 
@@ -594,7 +583,6 @@ struct TcConv {
     static constexpr int RPP = TC_CONV / CPR;             // rows per pass
     static constexpr int NP = TILE / RPP;                 // passes
     static constexpr int LPR = D / 8, RP = TC_CONV / LPR; // bf16 rows: lanes per row, rows per pass
-    static constexpr int NB = TILE / RP;                  // passes
     const Att& P;
     TcShared& sh;
     const uint32_t base;
@@ -1314,104 +1302,523 @@ __global__ void __launch_bounds__(MERGE_BT) k_attention_merge(const Att P) {
     }
 }
 
-__device__ __forceinline__ float e4m3_f32(uint8_t v) {
-    uint32_t h;
-    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"((uint32_t)v));
-    float f;
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(f) : "r"(h));
-    return f;
-}
+// ----------------------------------------------------------------------------- few rows (mma.sync)
 
-// One warp per row (b, n, query head): each lane holds D / 32 elements of q and
-// of the sum, every key is one dot product over the warp, with the running
-// maximum and sum of the softmax.
+// At most 16 rows of a kv head (single tokens, short chains): bound by the bytes
+// of the cache.  A warp takes 16 keys at a time straight from global memory into
+// the fragments of m16n8k16 products, with no shared memory between: the
+// dimensions that are summed over, and the columns of the result, may stand in any
+// order as long as both sides agree, so each lane loads 16 bytes of a key where it
+// needs them.
+//   scores  B column n = key n: lane (g, c) holds, of keys g and g + 8, bytes
+//           [16 c, 16 c + 16) of each 64; four bytes feed one 16-wide step.
+//   values  B row k = key k, column g: lane (g, c) holds, of keys 2c, 2c + 1,
+//           2c + 8, 2c + 9, the dims [g D/8, (g + 1) D/8): byte j of two keys
+//           makes the pair that the step for column block j wants.
+// Each warp has its own running maximum, sum and output (in registers); the four
+// meet in shared memory at the end of an item.  The bytes of the next 16 keys are on their
+// way while these are computed, and the page ids of those after them.
+// e4m3 keys go through the conversion instruction and values through bit moves, which
+// run on different pipes.
+constexpr int MM_BT = 128, MM_WARPS = MM_BT / 32, MM_ROWS = 16;
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint2 cvt_e4m3_f16(uint32_t w) {     // bytes (0, 1), (2, 3)
+    uint2 r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}" : "=r"(r.x), "=r"(r.y) : "r"(w));
+    return r;
+}
+// Largest finite magnitude of bf16 words, as bits; elements that are not finite become 0 or (keep_nan) NaN.
+template <int N>
+__device__ __forceinline__ uint32_t bf16_amax(uint32_t (&w)[N], bool& bad, bool keep_nan) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+    m = max(m & 0xffffu, m >> 16);
+    bad = m >= 0x7f80u;
+    if (bad) {
+        m = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int s = 0; s < 32; s += 16) {
+                const uint32_t a = (w[i] >> s) & 0x7fffu;
+                if (a >= 0x7f80u) w[i] = (w[i] & ~(0xffffu << s)) | (keep_nan ? 0x7fffu << s : 0u);
+                else m = max(m, a);
+            }
+    }
+    return m;
+}
+__device__ __forceinline__ int bits_exp(uint32_t m) { return m ? max(min((int)(m >> 7), 253), 1) - 127 : 0; }
+__device__ __forceinline__ uint32_t bf16_f16(uint32_t w, float s) { return pack_f16(bf_lo(w) * s, bf_hi(w) * s); }
+
+// 16 keys as a warp sees them.
+struct Chunk {
+    int b, h, seg, tok, kind;             // kind: 0 none left, 1 cached, 2 tail (tok: its first key), 3 nothing to do
+};
+struct MmAhead {
+    SegIter it;
+    Seg s;
+    int more;
+};
+
 template <int D>
-__global__ void __launch_bounds__(128) k_attention_rows(const Att P) {
-    constexpr int E = D / 32;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= (int64_t)P.B * P.N * P.Hq) return;
-    const int h = row % P.Hq, n = row / P.Hq % P.N, b = row / P.Hq / P.N, hk = h / P.G;
-    const int page = P.page;
-    const int len = P.c.lengths[b];
-    const int slot = P.c.slots ? P.c.slots[b] : b;
-    const int64_t most = (int64_t)P.c.max_pages * page + page - 1;
-    bool bad = len >= 0 && (len > most || len >= SPEC_MAX_CACHE_LEN || slot < 0 || slot >= P.c.num_slots);
-    float q[E], acc[E] = {}, m = -INFINITY, l = 0.f;
-    const __nv_bfloat16* qp = reinterpret_cast<const __nv_bfloat16*>(P.q.p + b * P.q.b + n * P.q.n + h * P.q.h);
-#pragma unroll
-    for (int i = 0; i < E; ++i) q[i] = __bfloat162float(qp[lane * E + i]);
-    auto key = [&](const float (&k)[E], const float (&v)[E]) {
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) s = fmaf(q[i], k[i], s);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
-        s *= P.scale;
-        const float m2 = fmaxf(m, s);
-        const float old = m2 == -INFINITY ? 1.f : exp2f(m - m2), p = m2 == -INFINITY ? 0.f : exp2f(s - m2);
-        l = l * old + p;
-#pragma unroll
-        for (int i = 0; i < E; ++i) acc[i] = acc[i] * old + p * v[i];
-        m = s != s ? s : m2;
-    };
-    if (!bad && len >= 0) {
-        const int full = len / page;
-        for (int j = 0; j < full && !bad; ++j) {
-            const int id = P.c.page_table[b * P.c.page_table_stride + j];
-            if (id < 0 || id >= P.c.num_pages) {
-                bad = true;
-                break;
-            }
-            const int64_t ph = (int64_t)id * P.Hkv + hk;
-            const uint8_t* kp = static_cast<const uint8_t*>(P.c.k_pages) + ph * page * D;
-            const uint8_t* vp = static_cast<const uint8_t*>(P.c.v_pages) + ph * page * D;
-            const float ks = P.c.k_scale[ph], vs = P.c.v_scale[ph];
-            for (int t = 0; t < page; ++t) {
-                float k[E], v[E];
-#pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    k[i] = e4m3_f32(kp[t * D + lane * E + i]) * ks;
-                    v[i] = e4m3_f32(vp[t * D + lane * E + i]) * vs;
+struct MmWarp {
+    static constexpr int KH = D / 64;                     // 16-byte pieces of a key per lane
+    static constexpr int VW = D / 32;                     // 4-byte words of a value per lane
+    static constexpr int NT = D / 8;                      // column blocks of the output
+    const Att& P;
+    const int lane, warp, g, c;
+    MmAhead& a;                                           // the segment of the chunk after, kept by lane 0
+    int seg, t, t1, sub, b, h, nct, full, keys;           // and what of it every chunk needs
+    float o[NT][4], m[2], l[2];
+
+    __device__ __forceinline__ MmWarp(const Att& P_, int warp_, MmAhead& a_)
+        : P(P_), lane(threadIdx.x & 31), warp(warp_), g(lane >> 2), c(lane & 3), a(a_) {}
+
+    __device__ __forceinline__ void begin(const Stretch& st) {
+        if (lane == 0) a.it.begin(P, st);
+        seg = -1;
+        t1 = t = 0;
+        sub = TILE / 16;
+    }
+    __device__ __forceinline__ Chunk next() {
+        Chunk x{};
+        sub += MM_WARPS;
+        if (sub >= TILE / 16) {
+            sub = warp;
+            if (++t >= t1) {
+                __syncwarp();
+                if (lane == 0) a.more = a.it.next(P, a.s);
+                __syncwarp();
+                if (!a.more) {
+                    t1 = 0;
+                    return x;
                 }
-                key(k, v);
+                ++seg;
+                t = a.s.t0;
+                t1 = a.s.t1;
+                b = a.s.b;
+                h = a.s.h;
+                nct = a.s.q.nct;
+                full = a.s.q.full;
+                keys = a.s.q.len >= 0 && !a.s.q.bad ? a.s.q.open + P.N : 0;
             }
         }
-        for (int t = full * page; t < len; ++t) {
-            const int64_t at = (((int64_t)slot * P.Hkv + hk) * 2 * page + t % (2 * page)) * D;
-            const __nv_bfloat16* kp = static_cast<const __nv_bfloat16*>(P.c.k_open) + at;
-            const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(P.c.v_open) + at;
-            float k[E], v[E];
+        x.b = b; x.h = h; x.seg = seg;
+        x.tok = (t < nct ? t : t - nct) * TILE + sub * 16;
+        x.kind = t < nct ? (x.tok < full ? 1 : 3) : x.tok < keys ? 2 : 3;
+        return x;
+    }
+    __device__ __forceinline__ int page_id(const Chunk& x) const {
+        return x.kind == 1 ? __ldg(P.c.page_table + x.b * P.c.page_table_stride + (x.tok >> P.pshift)) : 0;
+    }
+    // A cached chunk's bytes and scales, on their way to registers.
+    __device__ __forceinline__ void fetch(const Chunk& x, int id, uint4 (&k)[2][KH], uint32_t (&v)[4][VW], float& ks, float& vs) const {
+        if (x.kind != 1 || id < 0 || id >= P.c.num_pages) return;
+        const int64_t ph = (int64_t)id * P.Hkv + x.h;
+        const int64_t row = (ph << P.pshift) + (x.tok & (P.page - 1));
+        const char* kp = static_cast<const char*>(P.c.k_pages) + (row + g) * D + 16 * c;
+        const char* vp = static_cast<const char*>(P.c.v_pages) + (row + 2 * c) * D + g * (D / 8);
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                k[i] = __bfloat162float(kp[lane * E + i]);
-                v[i] = __bfloat162float(vp[lane * E + i]);
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < KH; ++j) k[i][j] = ldg_stream(kp + 8 * i * D + 64 * j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const char* p = vp + ((i & 1) + (i >> 1) * 8) * D;
+            if constexpr (VW == 4) {
+                const uint4 w = ldg_stream(p);
+                v[i][0] = w.x; v[i][1] = w.y; v[i][2] = w.z; v[i][3] = w.w;
+            } else {
+                const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+                v[i][0] = w.x; v[i][1] = w.y;
             }
-            key(k, v);
         }
-        const int W = (P.N + 31) / 32;
-        for (int t = 0; t < P.N; ++t) {
-            const bool sees = P.anc ? (P.anc[((int64_t)b * P.N + n) * W + t / 32] >> (t & 31)) & 1 : t <= n;
-            if (!sees) continue;
-            const __nv_bfloat16* kp = reinterpret_cast<const __nv_bfloat16*>(P.k.p + b * P.k.b + t * P.k.n + hk * P.k.h);
-            const __nv_bfloat16* vp = reinterpret_cast<const __nv_bfloat16*>(P.v.p + b * P.v.b + t * P.v.n + hk * P.v.h);
-            float k[E], v[E];
+        ks = __ldg(P.c.k_scale + ph);
+        vs = __ldg(P.c.v_scale + ph);
+    }
+    static __device__ __forceinline__ uint4 ldg_stream(const void* p) {
+        uint4 v;
+        asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+        return v;
+    }
+    // Scores of two key blocks to probabilities (f16 fragments of the second product).  a: per column the key's scale
+    // (rows' factors rq come on top), b: log2 of its value's, inv: 1 / that.
+    __device__ __forceinline__ void softmax(const float (&s)[2][4], const float (&rq)[2], const float (&a)[4], const float (&b)[4],
+                                            const float (&inv)[4], const uint32_t (&mask)[2], uint32_t (&p)[4]) {
+        float w[2][4];                                    // [row g, g + 8][keys 2c, 2c + 1, 2c + 8, 2c + 9]
+        bool grow = false;
+        float top[2];
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                k[i] = __bfloat162float(kp[lane * E + i]);
-                v[i] = __bfloat162float(vp[lane * E + i]);
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float x = fmaf(s[j >> 1][2 * r + (j & 1)], fmaxf(a[j] * rq[r], 1.2e-38f), b[j]);
+                w[r][j] = (mask[r] >> (2 * c + (j & 1) + (j >> 1) * 8)) & 1 ? x : NEG_INF;
             }
-            key(k, v);
+            float mx = fmaxf(fmaxf(w[r][0], w[r][1]), fmaxf(w[r][2], w[r][3]));
+            mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
+            top[r] = fmaxf(m[r], mx);
+            grow |= mx > m[r] + M_SLACK;
+        }
+        if (__any_sync(FULL, grow)) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float f = top[r] == NEG_INF ? 1.f : ex2(m[r] - top[r]);
+                m[r] = top[r];
+                l[r] *= f;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    o[j][2 * r] *= f;
+                    o[j][2 * r + 1] *= f;
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float sub = P_BIAS - (m[r] == NEG_INF ? 0.f : m[r]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                w[r][j] = ex2(w[r][j] + sub);
+                l[r] = fmaf(w[r][j], inv[j], l[r]);
+            }
+            p[r] = pack_f16(w[r][0], w[r][1]);
+            p[2 + r] = pack_f16(w[r][2], w[r][3]);
         }
     }
-    const float nan = __int_as_float(0x7fffffff);
-    if (bad && lane == 0) atomicOr(P.status, 1u << SPEC_ERR_DEVICE_INPUT);
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-    __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(P.out) + row * D;
+    __device__ __forceinline__ void cached(const uint4 (&k)[2][KH], const uint32_t (&v)[4][VW], float ks, float vs, const uint4* qf,
+                                           const float (&rq)[2]) {
+        float s[2][4] = {};
 #pragma unroll
-    for (int i = 0; i < E; ++i) o[lane * E + i] = __float2bfloat16(bad ? nan : acc[i] * inv);
-    if (P.lse && lane == 0)
-        P.lse[row] = bad ? nan : l > 0.f || l != l ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+        for (int j = 0; j < KH; ++j)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const uint4 a = qf[(j * 4 + u) * 32 + lane];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t w = u == 0 ? k[i][j].x : u == 1 ? k[i][j].y : u == 2 ? k[i][j].z : k[i][j].w;
+                    const uint2 b = cvt_e4m3_f16(w);
+                    mma16816(s[i], a.x, a.y, a.z, a.w, b.x, b.y);
+                }
+            }
+        const float lv = log2f(vs) + 8.f, iv = 1.f / (vs * 256.f);       // the f16 values are 2^-8 of the bytes
+        const float aa[4] = {ks, ks, ks, ks}, bb[4] = {lv, lv, lv, lv}, ii[4] = {iv, iv, iv, iv};
+        const uint32_t all[2] = {0xffffu, 0xffffu};
+        uint32_t p[4], nan = 0;
+        softmax(s, rq, aa, bb, ii, all, p);
+#pragma unroll
+        for (int u = 0; u < VW; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {                 // bytes 2h, 2h + 1 of word u
+                const uint2 x = e4m3_f16(__byte_perm(v[0][u], v[1][u], h ? 0x7632 : 0x5410), nan);
+                const uint2 y = e4m3_f16(__byte_perm(v[2][u], v[3][u], h ? 0x7632 : 0x5410), nan);
+                mma16816(o[4 * u + 2 * h], p[0], p[1], p[2], p[3], x.x, y.x);
+                mma16816(o[4 * u + 2 * h + 1], p[0], p[1], p[2], p[3], x.y, y.y);
+            }
+        if (__any_sync(FULL, nan & 0x80808080u)) nan_values(v);
+    }
+    // A NaN byte read as 480: every row sees every cached key, so its column is NaN for all of them.
+    __device__ __forceinline__ void nan_values(const uint32_t (&v)[4][VW]) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            bool bad = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) bad |= ((v[i][j / 4] >> (8 * (j & 3))) & 0x7f) == 0x7f;
+            // this lane holds column g of the block, the output's lane columns 2c and 2c + 1
+            const uint32_t hit = __ballot_sync(FULL, bad);
+            const float q = __int_as_float(0x7fffffff);
+            if (hit >> (8 * c) & 0xfu) o[j][0] = o[j][2] = q;
+            if (hit >> (8 * c + 4) & 0xfu) o[j][1] = o[j][3] = q;
+        }
+    }
+    // 16 keys of the tail, from bf16 rows.  bad_v: the item's keys whose value is not finite.
+    __device__ __forceinline__ void tail(const Chunk& x, const Seq& q, const uint4* qf, const float (&rq)[2], uint32_t* bad_v) {
+        const int64_t ring = ((int64_t)q.slot * P.Hkv + x.h) * 2 * P.page;
+        auto row = [&](int e, int which) -> const char* {                // a place that is there for every row
+            const int64_t at = (ring + ((q.full + e) & (2 * P.page - 1))) * D * 2, n = e - q.open;
+            const sv_host::Rows& src = which ? P.v : P.k;
+            const char* p = e < q.open ? static_cast<const char*>(which ? P.c.v_open : P.c.k_open) + at
+                                       : src.p + x.b * src.b + n * src.n + x.h * src.h;
+            return e < q.open + P.N ? p : P.q.p;
+        };
+        const int keys = q.open + P.N;
+        float s[2][4] = {}, ka[2];
+        uint32_t kw[2][KH * 8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const char* p = row(x.tok + 8 * i + g, 0) + 32 * c;
+#pragma unroll
+            for (int j = 0; j < KH; ++j)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(p + 128 * j + 16 * u);
+                    kw[i][8 * j + 4 * u] = w.x; kw[i][8 * j + 4 * u + 1] = w.y;
+                    kw[i][8 * j + 4 * u + 2] = w.z; kw[i][8 * j + 4 * u + 3] = w.w;
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            bool bad;
+            uint32_t mx = bf16_amax(kw[i], bad, true);
+            mx = max(mx, __shfl_xor_sync(FULL, mx, 1));
+            mx = max(mx, __shfl_xor_sync(FULL, mx, 2));
+            const int e = bits_exp(mx);
+            ka[i] = exp2i(e);
+#pragma unroll
+            for (int u = 0; u < KH * 4; ++u) {
+                const uint4 a = qf[u * 32 + lane];
+                mma16816(s[i], a.x, a.y, a.z, a.w, bf16_f16(kw[i][2 * u], exp2i(-e)), bf16_f16(kw[i][2 * u + 1], exp2i(-e)));
+            }
+        }
+        float aa[4], bb[4], ii[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) aa[j] = __shfl_sync(FULL, ka[j >> 1], (2 * c + (j & 1)) * 4);
+        uint32_t vw[4][VW * 2];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int e = x.tok + 2 * c + (j & 1) + (j >> 1) * 8;
+            const char* p = row(e, 1) + g * (D / 4);
+#pragma unroll
+            for (int u = 0; u < VW / 2; ++u) {
+                const uint4 w = *reinterpret_cast<const uint4*>(p + 16 * u);
+                vw[j][4 * u] = w.x; vw[j][4 * u + 1] = w.y; vw[j][4 * u + 2] = w.z; vw[j][4 * u + 3] = w.w;
+            }
+            bool bad;
+            uint32_t mx = bf16_amax(vw[j], bad, false);
+            if (bad && e < keys) atomicOr(&bad_v[e >> 5], 1u << (e & 31));
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) mx = max(mx, __shfl_xor_sync(FULL, mx, d));
+            const int ex = bits_exp(mx);
+            bb[j] = (float)ex;
+            ii[j] = exp2i(-ex);
+#pragma unroll
+            for (int u = 0; u < VW * 2; ++u) vw[j][u] = bf16_f16(vw[j][u], exp2i(-ex));
+        }
+        uint32_t mask[2], p[4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int n = min(g + 8 * r, P.R - 1) / P.G;
+            mask[r] = tail_bits(P, x.b, n, q.open, x.tok) & 0xffffu;
+        }
+        softmax(s, rq, aa, bb, ii, mask, p);
+#pragma unroll
+        for (int u = 0; u < VW * 2; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                mma16816(o[2 * u + h], p[0], p[1], p[2], p[3], __byte_perm(vw[0][u], vw[1][u], h ? 0x7632 : 0x5410),
+                         __byte_perm(vw[2][u], vw[3][u], h ? 0x7632 : 0x5410));
+    }
+    // The item's queries as fragments of this warp, and the factors of rows g and g + 8.
+    __device__ __forceinline__ void load_q(const Chunk& x, uint4* qf, float (&rq)[2]) {
+        uint32_t w[2][KH * 8];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = min(g + 8 * r, P.R - 1), n = row / P.G;
+            const char* p = P.q.p + x.b * P.q.b + n * P.q.n + (x.h * P.G + row - n * P.G) * P.q.h + 32 * c;
+#pragma unroll
+            for (int j = 0; j < KH; ++j)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(p + 128 * j + 16 * u);
+                    w[r][8 * j + 4 * u] = v.x; w[r][8 * j + 4 * u + 1] = v.y;
+                    w[r][8 * j + 4 * u + 2] = v.z; w[r][8 * j + 4 * u + 3] = v.w;
+                }
+        }
+        float sc[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            bool bad;
+            uint32_t mx = bf16_amax(w[r], bad, true);
+            mx = max(mx, __shfl_xor_sync(FULL, mx, 1));
+            mx = max(mx, __shfl_xor_sync(FULL, mx, 2));
+            const int e = bits_exp(mx);
+            sc[r] = exp2i(-e);
+            rq[r] = exp2i(e) * P.scale;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < KH * 4; ++u)
+            qf[u * 32 + lane] = make_uint4(bf16_f16(w[0][2 * u], sc[0]), bf16_f16(w[1][2 * u], sc[1]), bf16_f16(w[0][2 * u + 1], sc[0]),
+                                           bf16_f16(w[1][2 * u + 1], sc[1]));
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+        m[0] = m[1] = NEG_INF;
+        l[0] = l[1] = 0.f;
+    }
+};
+
+template <int D> struct MmShared {
+    uint4 q[MM_WARPS][D / 16][32];                        // each warp's query fragments
+    float o[MM_WARPS][MM_ROWS][D + 4];
+    float m[MM_WARPS][MM_ROWS], l[MM_WARPS][MM_ROWS];
+    uint32_t bad_v[12];
+    int bad;
+    MmAhead now, ahead[MM_WARPS];                         // the segment being computed; of each warp's next chunk
+};
+
+// The end of a segment: the warps' results put together and written out, or left as a part.
+template <int D>
+__device__ __forceinline__ void mm_finish(const Att& P, MmWarp<D>& w, MmShared<D>& sh, bool bad) {
+    const int tid = threadIdx.x;
+    const Seg& g = sh.now.s;
+    const Stretch& st = sh.now.it.s;
+    constexpr int NT = D / 8;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        w.l[r] += __shfl_xor_sync(FULL, w.l[r], 1);
+        w.l[r] += __shfl_xor_sync(FULL, w.l[r], 2);
+        const int row = w.g + 8 * r;
+        if (w.c == 0) {
+            sh.m[w.warp][row] = w.m[r];
+            sh.l[w.warp][row] = w.l[r];
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int j = 0; j < NT; j += 4)
+                *reinterpret_cast<float4*>(&sh.o[w.warp][row][(2 * w.c + s) * NT + j]) =
+                    make_float4(w.o[j][2 * r + s], w.o[j + 1][2 * r + s], w.o[j + 2][2 * r + s], w.o[j + 3][2 * r + s]);
+    }
+    if (bad) sh.bad = 1;
+    __syncthreads();
+    const bool whole = g.t0 == 0 && g.t1 == g.q.ntiles;
+    const bool nan = g.q.bad || sh.bad;
+    const float quiet = __int_as_float(0x7fffffff);
+    const int slot = g.item_lo + g.t0 == st.lo ? 0 : 1;
+    float* part = partial_of<D>(P, blockIdx.x, slot);
+    uint32_t any_bad = 0;
+    if (g.t1 > g.q.nct)
+        for (int i = 0; i < 12; ++i) any_bad |= sh.bad_v[i];
+    constexpr int LPR = D / 4;                            // lanes of a row, four dims each
+    for (int r = tid / LPR; r < P.R; r += MM_BT / LPR) {
+        const int d = tid % LPR * 4;
+        float mm = NEG_INF;
+#pragma unroll
+        for (int i = 0; i < MM_WARPS; ++i) mm = fmaxf(mm, sh.m[i][r]);
+        const float base = mm == NEG_INF ? 0.f : mm;
+        float l = 0.f, x[4] = {};
+#pragma unroll
+        for (int i = 0; i < MM_WARPS; ++i) {
+            const float f = ex2(sh.m[i][r] - base);
+            l = fmaf(f, sh.l[i][r], l);
+            const float4 v = *reinterpret_cast<const float4*>(&sh.o[i][r][d]);
+            x[0] = fmaf(f, v.x, x[0]); x[1] = fmaf(f, v.y, x[1]); x[2] = fmaf(f, v.z, x[2]); x[3] = fmaf(f, v.w, x[3]);
+        }
+        const int n = r / P.G;
+        if (any_bad) {
+            for (int i = 0; i < 12; ++i) {
+                uint32_t hit = sh.bad_v[i];
+                if (hit) hit &= tail_bits(P, g.b, n, g.q.open, 32 * i);
+                for (; hit; hit &= hit - 1) {
+                    const int e = 32 * i + __ffs(hit) - 1;
+                    const char* src = e < g.q.open
+                        ? static_cast<const char*>(P.c.v_open) +
+                              (((int64_t)g.q.slot * P.Hkv + g.h) * 2 * P.page + (g.q.full + e) % (2 * P.page)) * D * 2
+                        : P.v.p + g.b * P.v.b + (e - g.q.open) * P.v.n + g.h * P.v.h;
+                    const __nv_bfloat16* vv = reinterpret_cast<const __nv_bfloat16*>(src) + d;
+                    for (int j = 0; j < 4; ++j) {
+                        const float y = __bfloat162float(vv[j]);
+                        if (!(fabsf(y) <= 3.402823466e38f)) x[j] += y;
+                    }
+                }
+            }
+        }
+        const int64_t at = ((int64_t)g.b * P.N + n) * P.Hq + g.h * P.G + r - n * P.G;
+        if (nan) x[0] = x[1] = x[2] = x[3] = l = quiet;
+        if (whole) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            *reinterpret_cast<uint2*>(P.out + (at * D + d) * 2) =
+                make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
+            if (d == 0 && P.lse) P.lse[at] = nan ? quiet : l == 0.f ? NEG_INF : (mm - P_BIAS + log2f(l)) * LN2;
+        } else {
+            *reinterpret_cast<float4*>(part + (int64_t)r * D + d) = make_float4(x[0], x[1], x[2], x[3]);
+            if (d == 0) {
+                part[(int64_t)P.R * D + r] = mm == NEG_INF ? NEG_INF : mm - P_BIAS;
+                part[(int64_t)P.R * D + P.R + r] = l;
+            }
+        }
+    }
+    if (tid == 0) {
+        if (nan) atomicOr(P.status, 1u << SPEC_ERR_DEVICE_INPUT);
+        if (!whole && g.t0 == 0) {
+            const int c1 = cta_of(g.item_lo + g.q.ntiles - 1, st.total, st.ctas);
+            P.cut[blockIdx.x] = Cut{g.b, g.h, g.mt, c1 - (int)blockIdx.x + 1, slot};
+        }
+    }
+    __syncthreads();
+    if (tid < 12) sh.bad_v[tid] = 0;
+    if (tid == 12) sh.bad = 0;
+    if (tid == 32) sh.now.more = sh.now.it.next(P, sh.now.s);
+    __syncthreads();
+}
+
+template <int D>
+__global__ void __launch_bounds__(MM_BT, 3) k_attention_mma(const Att P) {
+    extern __shared__ __align__(16) unsigned char mm_smem[];
+    MmShared<D>& sh = *reinterpret_cast<MmShared<D>*>(mm_smem);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Stretch st = find_stretch<MM_BT>(P);
+    if (threadIdx.x == 0) P.cut[blockIdx.x].parts = 0;
+    if (st.lo >= st.hi) return;
+    if (threadIdx.x < 12) sh.bad_v[threadIdx.x] = 0;
+    if (threadIdx.x == 12) sh.bad = 0;
+    if (threadIdx.x == 32) {
+        sh.now.it.begin(P, st);
+        sh.now.more = sh.now.it.next(P, sh.now.s);
+    }
+    __syncthreads();
+    using W = MmWarp<D>;
+    W w(P, threadIdx.x >> 5, sh.ahead[threadIdx.x >> 5]);
+    w.begin(st);
+    uint4 k0[2][W::KH], k1[2][W::KH];
+    uint32_t v0[4][W::VW], v1[4][W::VW];
+    float ks0 = 1.f, vs0 = 1.f, ks1 = 1.f, vs1 = 1.f, rq[2];
+    uint4* qf = &sh.q[w.warp][0][0];
+    Chunk x = w.next();
+    int id0 = w.page_id(x);
+    w.fetch(x, id0, k0, v0, ks0, vs0);
+    Chunk y = w.next();
+    int id1 = w.page_id(y);
+    bool bad = false;
+    int seg = -1;
+    // chunk x is computed, y's bytes are on their way, z's page id is
+#define MM_STEP(K, V, KS, VS, ID, K2, V2, KS2, VS2, ID2)                                                       \
+    {                                                                                                          \
+        w.fetch(y, ID2, K2, V2, KS2, VS2);                                                                     \
+        if (x.seg != seg) {                                                                                    \
+            seg = x.seg;                                                                                       \
+            w.load_q(x, qf, rq);                                                                               \
+        }                                                                                                      \
+        const Chunk z = y.kind ? w.next() : y;                                                                 \
+        const int id2 = w.page_id(z);                                                                          \
+        if (x.kind == 1) {                                                                                     \
+            if (ID < 0 || ID >= P.c.num_pages) bad = true;                                                     \
+            else w.cached(K, V, KS, VS, qf, rq);                                                               \
+        } else if (x.kind == 2) {                                                                              \
+            w.tail(x, sh.now.s.q, qf, rq, sh.bad_v);                                                           \
+        }                                                                                                      \
+        if (y.kind == 0 || y.seg != x.seg) {                                                                   \
+            mm_finish<D>(P, w, sh, bad);                                                                       \
+            bad = false;                                                                                       \
+        }                                                                                                      \
+        if (y.kind == 0) break;                                                                                \
+        x = y;                                                                                                 \
+        y = z;                                                                                                 \
+        ID = id2;                                                                                              \
+    }
+    while (true) {
+        MM_STEP(k0, v0, ks0, vs0, id0, k1, v1, ks1, vs1, id1)
+        MM_STEP(k1, v1, ks1, vs1, id1, k0, v0, ks0, vs0, id0)
+    }
+#undef MM_STEP
 }
 
 }  // namespace
@@ -1420,7 +1827,7 @@ using sv_host::fail;
 
 namespace {
 
-constexpr int ATT_CTAS = 148;             // CTAs at most: one per SM
+constexpr int TC_CTAS = 148, MM_CTAS = 3 * 148;      // CTAs at most
 
 template <int D>
 spec_status launch_merge(const Att& P, int ctas, cudaStream_t st) {
@@ -1468,11 +1875,22 @@ template <int D>
 spec_status launch_tc(const Att& P, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(k_attention_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tc_smem<D>());
     if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "k_attention_tc: %s", cudaGetErrorString(e));
-    const int ctas = sv_host::num_sms() < ATT_CTAS ? sv_host::num_sms() : ATT_CTAS;
+    const int ctas = sv_host::num_sms() < TC_CTAS ? sv_host::num_sms() : TC_CTAS;
     CUtensorMap kmap;
     if (const spec_status s = key_map<D>(P, &kmap)) return s;
     k_attention_tc<D><<<ctas, TC_BT, tc_smem<D>(), st>>>(P, kmap);
     const spec_status s = sv_host::launched("k_attention_tc");
+    return s == SPEC_OK ? launch_merge<D>(P, ctas, st) : s;
+}
+
+template <int D>
+spec_status launch_mma(const Att& P, cudaStream_t st) {
+    const size_t smem = sizeof(MmShared<D>);
+    const cudaError_t e = cudaFuncSetAttribute(k_attention_mma<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "k_attention_mma: %s", cudaGetErrorString(e));
+    const int ctas = 3 * sv_host::num_sms() < MM_CTAS ? 3 * sv_host::num_sms() : MM_CTAS;
+    k_attention_mma<D><<<ctas, MM_BT, smem, st>>>(P);
+    const spec_status s = sv_host::launched("k_attention_mma");
     return s == SPEC_OK ? launch_merge<D>(P, ctas, st) : s;
 }
 
@@ -1484,8 +1902,10 @@ size_t spec_cache_workspace_bytes(int B, int N, int q_heads, int head_dim) {
     if (B < 0 || B > sv_host::CACHE_MAX_B || N < 1 || N > SPEC_MAX_NODES || q_heads < 1 || q_heads > SPEC_MAX_HEADS ||
         (head_dim != 64 && head_dim != 128))
         return 0;
-    const size_t rows = (size_t)N * q_heads < 256 ? (size_t)N * q_heads : 256;
-    return sv_host::CACHE_WS_PARTIAL + sv_host::align256(sizeof(float) * 2 * ATT_CTAS * rows * (head_dim + 2));
+    // rows of an item: at most N * q_heads (one kv head), 16 of them in the kernel with more CTAs
+    const size_t rows = (size_t)N * q_heads < 256 ? (size_t)N * q_heads : 256, few = rows < MM_ROWS ? rows : MM_ROWS;
+    const size_t parts = TC_CTAS * rows > MM_CTAS * few ? TC_CTAS * rows : MM_CTAS * few;
+    return sv_host::CACHE_WS_PARTIAL + sv_host::align256(sizeof(float) * 2 * parts * (head_dim + 2));
 }
 
 spec_status spec_tree_attention(int B, int N, int q_heads, const spec_kv_cache* cache,
@@ -1527,12 +1947,9 @@ spec_status spec_tree_attention(int B, int N, int q_heads, const spec_kv_cache* 
     P.status = reinterpret_cast<unsigned*>(ws + sv_host::CACHE_WS_STATUS);
     P.cut = reinterpret_cast<Cut*>(ws + sv_host::CACHE_WS_CUT);
     P.partial = reinterpret_cast<float*>(ws + sv_host::CACHE_WS_PARTIAL);
-    const int64_t rows = (int64_t)B * N * q_heads;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (P.R > 16) return D == 64 ? launch_tc<64>(P, st) : launch_tc<128>(P, st);
-    if (D == 64) k_attention_rows<64><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(P);
-    else k_attention_rows<128><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(P);
-    return sv_host::launched("k_attention_rows");
+    if (P.R > MM_ROWS) return D == 64 ? launch_tc<64>(P, st) : launch_tc<128>(P, st);
+    return D == 64 ? launch_mma<64>(P, st) : launch_mma<128>(P, st);
 }
 
 }  // extern "C"
