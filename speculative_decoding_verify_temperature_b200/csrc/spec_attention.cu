@@ -226,8 +226,7 @@ __device__ __forceinline__ uint32_t tail_bits(const Att& P, int b, int n, int op
 // largest magnitude to [128, 256), is the sum of two e4m3 rows (four bits of
 // its eight each; an element below 2^-9 of the largest is rounded at 2^-18 of it), so a score is
 // two products.  The tail's keys are split the same way, four products.
-// Values are turned into f16 (an e4m3 value times 2^-8 is an f16 value; the
-// tail's rows are divided by a power of two that brings them to [1, 2)).
+// Values are turned into f16 (which holds every e4m3 value; the tail's rows are divided by a power of two that brings them to [1, 2)).
 //
 // The scales come back in f32: with a_j the key's scale times the row's and
 // s_v,j the value's, x_j = S_j a_j is the score in base 2 and
@@ -279,18 +278,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// Four e4m3 bytes to f16 times 2^-8, the bytes in the order (0, 2), (1, 3): the exponent and mantissa bits move as
-// they are, subnormals included.  (The conversion instruction was measured at 6000 cycles a tile, this at 0000.)  A
-// NaN byte would read as 480: bit 7 of a byte of `nan` tells.
-__device__ __forceinline__ uint2 e4m3_f16(uint32_t w, uint32_t& nan) {
-    nan |= (w & 0x7f7f7f7fu) + 0x01010101u;
+// Four e4m3 bytes to f16 (exact), bytes (0, 1) and (2, 3).
+__device__ __forceinline__ uint2 e4m3_f16(uint32_t w) {
     uint2 r;
-    r.x = ((w << 7) & 0x3f803f80u) | ((w << 8) & 0x80008000u);
-    r.y = ((w >> 1) & 0x3f803f80u) | (w & 0x80008000u);
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}" : "=r"(r.x), "=r"(r.y) : "r"(w));
     return r;
 }
-// Place of dim j of a row within the operands (and, both ways, of O's columns).
-__host__ __device__ constexpr int place(int j) { return (j & ~3) | ((j & 1) << 1) | ((j >> 1) & 1); }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
@@ -337,6 +331,13 @@ __device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* b) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                  :: "r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(b)) : "memory");
+}
+__device__ __forceinline__ void copy4(const float* dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// Arrives once this thread's copy4()s have landed.
+__device__ __forceinline__ void copy4_arrive(uint64_t* b) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(b)) : "memory");
 }
 // Rows [row, row + box) of the tensor map's 8-bit matrix, all columns, swizzled.
 __device__ __forceinline__ void tensor_copy(uint32_t dst, const CUtensorMap* map, int row, uint64_t* b) {
@@ -560,7 +561,7 @@ __device__ __forceinline__ void tc_scales(const Att& P, TcShared& sh, const Stre
         const int m = u.gt & (TC_META - 1);
         const uint32_t par = ((u.gt / TC_META) & 1) ^ 1;
         const bool cached = u.cached();
-        const float k0 = ks, v0 = vs * 256.f;             // the f16 values are 2^-8 of the bytes
+        const float k0 = ks, v0 = vs;
         more = u.next(P);
         if (more) fetch(u.g, u.t, ks, vs);
         if (more && u.first()) prefetch_segment<D>(P, u, lane);
@@ -602,29 +603,15 @@ struct TcConv {
         const int c = tid % CPR, r0 = tid / CPR;
         const uint32_t half = dst + (c / 4) * Tc<D>::HALF;
         const int q = (c % 4) * 2, flip = c / 4;
-        uint32_t nan = 0;
-#pragma unroll 4
+#pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int r = r0 + i * RPP;
             uint4 x = lds128(src + r * D + c * 16);
             if (r >= valid) x = make_uint4(0, 0, 0, 0);
-            const uint2 a = e4m3_f16(x.x, nan), b = e4m3_f16(x.y, nan), d = e4m3_f16(x.z, nan), e = e4m3_f16(x.w, nan);
+            const uint2 a = e4m3_f16(x.x), b = e4m3_f16(x.y), d = e4m3_f16(x.z), e = e4m3_f16(x.w);
             const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, e.x, e.y);
             sts128(swz(half, r, q + flip), flip ? hi : lo);
             sts128(swz(half, r, q + 1 - flip), flip ? lo : hi);
-        }
-        if (nan & 0x80808080u) put_nans(half, src, valid);
-    }
-    // This thread's NaN bytes, one by one.
-    __device__ __noinline__ void put_nans(uint32_t half, uint32_t src, int valid) {
-        const int c = tid % CPR, r0 = tid / CPR;
-        for (int i = 0; i < 16 * NP; ++i) {
-            const int r = r0 + i / 16 * RPP, j = i & 15;
-            uint32_t v;
-            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(src + r * D + c * 16 + j));
-            const int p = place(j);
-            if (r < valid && (v & 0x7f) == 0x7f)
-                asm volatile("st.shared.b16 [%0], %1;" :: "r"(swz(half, r, (c % 4) * 2 + p / 8) + (p & 7) * 2), "h"((uint16_t)0x7e00) : "memory");
         }
     }
     // Eight bf16 elements of a row in each of D / 8 lanes: the row's power of two, from the bits of its finite
@@ -662,8 +649,7 @@ struct TcConv {
         uint32_t h[4];
         to_f16(w, -e, h);
         sts128(swz(dst + (l / 8) * Tc<D>::HALF, r, l % 8),
-               make_uint4(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[0], h[1], 0x7632), __byte_perm(h[2], h[3], 0x5410),
-                          __byte_perm(h[2], h[3], 0x7632)));
+               make_uint4(h[0], h[1], h[2], h[3]));
     }
     // The two e4m3 rows of a bf16 row divided by 2^(e - 7); the second's elements are exact differences.
     __device__ __forceinline__ void split_row(const uint4& w, int e, uint2& hi, uint2& lo) {
@@ -1184,7 +1170,7 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
 #pragma unroll
                             for (int j = 0; j < 32; ++j) {
                                 const float x = __bfloat162float(vv[j]);
-                                if (!(fabsf(x) <= 3.402823466e38f)) o[place(j)] = __float_as_uint(__uint_as_float(o[place(j)]) + x);
+                                if (!(fabsf(x) <= 3.402823466e38f)) o[j] = __float_as_uint(__uint_as_float(o[j]) + x);
                             }
                         }
                     }
@@ -1196,7 +1182,7 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
                         for (int j = 0; j < 32; j += 8) {
                             float x[8];
 #pragma unroll
-                            for (int u = 0; u < 8; ++u) x[u] = nan ? quiet : __uint_as_float(o[place(j + u)]) * inv;
+                            for (int u = 0; u < 8; ++u) x[u] = nan ? quiet : __uint_as_float(o[j + u]) * inv;
                             dst[j / 8] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
                                                     pack_bf16(x[6], x[7]));
                         }
@@ -1205,8 +1191,8 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
 #pragma unroll
                         for (int j = 0; j < 32; j += 4)
                             dst[j / 4] = nan ? make_float4(quiet, quiet, quiet, quiet)
-                                             : make_float4(__uint_as_float(o[place(j)]), __uint_as_float(o[place(j + 1)]),
-                                                           __uint_as_float(o[place(j + 2)]), __uint_as_float(o[place(j + 3)]));
+                                             : make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]),
+                                                           __uint_as_float(o[j + 2]), __uint_as_float(o[j + 3]));
                     }
                 }
             }
@@ -1305,32 +1291,25 @@ __global__ void __launch_bounds__(MERGE_BT) k_attention_merge(const Att P) {
 // ----------------------------------------------------------------------------- few rows (mma.sync)
 
 // At most 16 rows of a kv head (single tokens, short chains): bound by the bytes
-// of the cache.  A warp takes 16 keys at a time straight from global memory into
-// the fragments of m16n8k16 products, with no shared memory between: the
-// dimensions that are summed over, and the columns of the result, may stand in any
-// order as long as both sides agree, so each lane loads 16 bytes of a key where it
-// needs them.
-//   scores  B column n = key n: lane (g, c) holds, of keys g and g + 8, bytes
-//           [16 c, 16 c + 16) of each 64; four bytes feed one 16-wide step.
+// of the cache.  A warp takes 16 keys at a time; tensor copies bring their 2 D
+// bytes to a ring of three in shared memory that is the warp's own, so that two of
+// them are on their way while one is computed (three warps per scheduler, 8 KB each at D = 128).
+// From there they go straight into the fragments of m16n8k16 products: the
+// dimensions that are summed over, and the columns of the result, may stand in
+// any order as long as both sides agree, so each lane reads 16 bytes where it needs them
+// (the swizzle keeps the lanes on different banks).
+//   scores  B column n = key n: lane (g, c) holds, of keys g and g + 8, the bytes
+//           [c D/4, (c + 1) D/4); four of them feed one 16-wide step.
 //   values  B row k = key k, column g: lane (g, c) holds, of keys 2c, 2c + 1,
 //           2c + 8, 2c + 9, the dims [g D/8, (g + 1) D/8): byte j of two keys
 //           makes the pair that the step for column block j wants.
 // Each warp has its own running maximum, sum and output (in registers); the four
-// meet in shared memory at the end of an item.  The bytes of the next 16 keys are on their
-// way while these are computed, and the page ids of those after them.
-// e4m3 keys go through the conversion instruction and values through bit moves, which
-// run on different pipes.
-constexpr int MM_BT = 128, MM_WARPS = MM_BT / 32, MM_ROWS = 16;
+// are joined through shared memory at the end of an item.
+constexpr int MM_BT = 128, MM_WARPS = MM_BT / 32, MM_ROWS = 16, MM_RING = 3, MM_CTAS_SM = 3;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint2 cvt_e4m3_f16(uint32_t w) {     // bytes (0, 1), (2, 3)
-    uint2 r;
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}" : "=r"(r.x), "=r"(r.y) : "r"(w));
-    return r;
 }
 // Largest finite magnitude of bf16 words, as bits; elements that are not finite become 0 or (keep_nan) NaN.
 template <int N>
@@ -1358,12 +1337,24 @@ __device__ __forceinline__ uint32_t bf16_f16(uint32_t w, float s) { return pack_
 
 // 16 keys as a warp sees them.
 struct Chunk {
-    int b, h, seg, tok, kind;             // kind: 0 none left, 1 cached, 2 tail (tok: its first key), 3 nothing to do
+    int tok, is;                          // first key; kind (0 none left, 1 cached, 2 tail, 3 nothing to do), kv head, segment's parity
+    __device__ __forceinline__ int kind() const { return is & 3; }
+    __device__ __forceinline__ int h() const { return is >> 2 & 0xfff; }
+    __device__ __forceinline__ int parity() const { return is >> 14; }
 };
 struct MmAhead {
     SegIter it;
     Seg s;
     int more;
+};
+
+// A warp's ring: its slots of 16 keys and values; their page's scales.
+template <int D> struct MmRing {
+    unsigned char k[MM_RING][16 * D], v[MM_RING][16 * D];
+};
+struct MmSlots {
+    float scale[MM_RING][2];
+    uint64_t full[MM_RING];
 };
 
 template <int D>
@@ -1374,79 +1365,67 @@ struct MmWarp {
     const Att& P;
     const int lane, warp, g, c;
     MmAhead& a;                                           // the segment of the chunk after, kept by lane 0
-    int seg, t, t1, sub, b, h, nct, full, keys;           // and what of it every chunk needs
+    int t, sub, parity;
     float o[NT][4], m[2], l[2];
 
     __device__ __forceinline__ MmWarp(const Att& P_, int warp_, MmAhead& a_)
         : P(P_), lane(threadIdx.x & 31), warp(warp_), g(lane >> 2), c(lane & 3), a(a_) {}
 
     __device__ __forceinline__ void begin(const Stretch& st) {
-        if (lane == 0) a.it.begin(P, st);
-        seg = -1;
-        t1 = t = 0;
+        if (lane == 0) {
+            a.it.begin(P, st);
+            a.s.t1 = 0;
+        }
+        __syncwarp();
+        parity = 1;
+        t = 0;
         sub = TILE / 16;
     }
-    __device__ __forceinline__ Chunk next() {
+    // The chunk after, and (cached) its page.
+    __device__ __forceinline__ Chunk next(int& page) {
         Chunk x{};
+        page = 0;
         sub += MM_WARPS;
         if (sub >= TILE / 16) {
             sub = warp;
-            if (++t >= t1) {
+            if (++t >= a.s.t1) {
                 __syncwarp();
                 if (lane == 0) a.more = a.it.next(P, a.s);
                 __syncwarp();
-                if (!a.more) {
-                    t1 = 0;
-                    return x;
-                }
-                ++seg;
+                if (!a.more) return x;
+                parity ^= 1;
                 t = a.s.t0;
-                t1 = a.s.t1;
-                b = a.s.b;
-                h = a.s.h;
-                nct = a.s.q.nct;
-                full = a.s.q.full;
-                keys = a.s.q.len >= 0 && !a.s.q.bad ? a.s.q.open + P.N : 0;
             }
         }
-        x.b = b; x.h = h; x.seg = seg;
-        x.tok = (t < nct ? t : t - nct) * TILE + sub * 16;
-        x.kind = t < nct ? (x.tok < full ? 1 : 3) : x.tok < keys ? 2 : 3;
+        const Seg& s = a.s;
+        x.tok = (t < s.q.nct ? t : t - s.q.nct) * TILE + sub * 16;
+        const int keys = s.q.len >= 0 && !s.q.bad ? s.q.open + P.N : 0;
+        const int kind = t < s.q.nct ? (x.tok < s.q.full ? 1 : 3) : x.tok < keys ? 2 : 3;
+        x.is = kind | s.h << 2 | parity << 14;
+        if (kind == 1) page = __ldg(P.c.page_table + s.b * P.c.page_table_stride + (x.tok >> P.pshift));
         return x;
     }
-    __device__ __forceinline__ int page_id(const Chunk& x) const {
-        return x.kind == 1 ? __ldg(P.c.page_table + x.b * P.c.page_table_stride + (x.tok >> P.pshift)) : 0;
-    }
-    // A cached chunk's bytes and scales, on their way to registers.
-    __device__ __forceinline__ void fetch(const Chunk& x, int id, uint4 (&k)[2][KH], uint32_t (&v)[4][VW], float& ks, float& vs) const {
-        if (x.kind != 1 || id < 0 || id >= P.c.num_pages) return;
-        const int64_t ph = (int64_t)id * P.Hkv + x.h;
-        const int64_t row = (ph << P.pshift) + (x.tok & (P.page - 1));
-        const char* kp = static_cast<const char*>(P.c.k_pages) + (row + g) * D + 16 * c;
-        const char* vp = static_cast<const char*>(P.c.v_pages) + (row + 2 * c) * D + g * (D / 8);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < KH; ++j) k[i][j] = ldg_stream(kp + 8 * i * D + 64 * j);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const char* p = vp + ((i & 1) + (i >> 1) * 8) * D;
-            if constexpr (VW == 4) {
-                const uint4 w = ldg_stream(p);
-                v[i][0] = w.x; v[i][1] = w.y; v[i][2] = w.z; v[i][3] = w.w;
-            } else {
-                const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
-                v[i][0] = w.x; v[i][1] = w.y;
+    // A cached chunk's bytes and scales on their way to slot s of the ring (every chunk passes through a slot).
+    __device__ __forceinline__ void fetch(const Chunk& x, int id, int s, MmRing<D>& ring, MmSlots& slots, const CUtensorMap* kmap,
+                                          const CUtensorMap* vmap) const {
+        if (x.kind() == 0) return;
+        const bool there = x.kind() == 1 && id >= 0 && id < P.c.num_pages;
+        const int64_t ph = (int64_t)id * P.Hkv + x.h();
+        __syncwarp();                                     // the slot has been read
+        if (lane < 2) {
+            if (there) {
+                copy4(&slots.scale[s][lane], (lane ? P.c.v_scale : P.c.k_scale) + ph);
+                if (lane == 0) {
+                    const int row = (int)((ph << P.pshift) + (x.tok & (P.page - 1)));
+                    bar_expect(&slots.full[s], 2 * 16 * D);
+                    tensor_copy(smem_u32(ring.k[s]), kmap, row, &slots.full[s]);
+                    tensor_copy(smem_u32(ring.v[s]), vmap, row, &slots.full[s]);
+                }
+            } else if (lane == 0) {
+                bar_arrive(&slots.full[s]);
             }
+            copy4_arrive(&slots.full[s]);
         }
-        ks = __ldg(P.c.k_scale + ph);
-        vs = __ldg(P.c.v_scale + ph);
-    }
-    static __device__ __forceinline__ uint4 ldg_stream(const void* p) {
-        uint4 v;
-        asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-        return v;
     }
     // Scores of two key blocks to probabilities (f16 fragments of the second product).  a: per column the key's scale
     // (rows' factors rq come on top), b: log2 of its value's, inv: 1 / that.
@@ -1493,59 +1472,64 @@ struct MmWarp {
             p[2 + r] = pack_f16(w[r][2], w[r][3]);
         }
     }
-    __device__ __forceinline__ void cached(const uint4 (&k)[2][KH], const uint32_t (&v)[4][VW], float ks, float vs, const uint4* qf,
-                                           const float (&rq)[2]) {
+    // 16-byte piece q of row r of a slot, as the tensor copy swizzles it.
+    static __device__ __forceinline__ uint32_t piece(uint32_t at, int r, int q) {
+        return at + r * D + ((D == 128 ? q ^ (r & 7) : q ^ (r >> 1 & 3)) << 4);
+    }
+    __device__ __forceinline__ void cached(const MmRing<D>& ring, const MmSlots& slots, int sl, const uint4* qf, const float (&rq)[2]) {
+        const uint32_t kp = smem_u32(ring.k[sl]), vp = smem_u32(ring.v[sl]);
         float s[2][4] = {};
 #pragma unroll
-        for (int j = 0; j < KH; ++j)
+        for (int j = 0; j < KH; ++j) {
+            uint4 k[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) k[i] = lds128(piece(kp, g + 8 * i, KH * c + j));
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const uint4 a = qf[(j * 4 + u) * 32 + lane];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint32_t w = u == 0 ? k[i][j].x : u == 1 ? k[i][j].y : u == 2 ? k[i][j].z : k[i][j].w;
-                    const uint2 b = cvt_e4m3_f16(w);
+                    const uint2 b = e4m3_f16(u == 0 ? k[i].x : u == 1 ? k[i].y : u == 2 ? k[i].z : k[i].w);
                     mma16816(s[i], a.x, a.y, a.z, a.w, b.x, b.y);
                 }
             }
-        const float lv = log2f(vs) + 8.f, iv = 1.f / (vs * 256.f);       // the f16 values are 2^-8 of the bytes
+        }
+        uint32_t v[4][VW];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 2 * c + (i & 1) + (i >> 1) * 8;
+            if constexpr (VW == 4) {
+                const uint4 w = lds128(piece(vp, r, g));
+                v[i][0] = w.x; v[i][1] = w.y; v[i][2] = w.z; v[i][3] = w.w;
+            } else {
+                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[i][0]), "=r"(v[i][1]) : "r"(piece(vp, r, g >> 1) + (g & 1) * 8));
+            }
+        }
+        const float ks = slots.scale[sl][0], vs = slots.scale[sl][1];
+        const float lv = __log2f(vs), iv = __frcp_rn(vs);
         const float aa[4] = {ks, ks, ks, ks}, bb[4] = {lv, lv, lv, lv}, ii[4] = {iv, iv, iv, iv};
         const uint32_t all[2] = {0xffffu, 0xffffu};
-        uint32_t p[4], nan = 0;
+        uint32_t p[4];
         softmax(s, rq, aa, bb, ii, all, p);
 #pragma unroll
         for (int u = 0; u < VW; ++u)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {                 // bytes 2h, 2h + 1 of word u
-                const uint2 x = e4m3_f16(__byte_perm(v[0][u], v[1][u], h ? 0x7632 : 0x5410), nan);
-                const uint2 y = e4m3_f16(__byte_perm(v[2][u], v[3][u], h ? 0x7632 : 0x5410), nan);
+            for (int h = 0; h < 2; ++h) {                 // bytes 2h, 2h + 1 of word u, of two keys side by side
+                const uint2 x = e4m3_f16(__byte_perm(v[0][u], v[1][u], h ? 0x7362 : 0x5140));
+                const uint2 y = e4m3_f16(__byte_perm(v[2][u], v[3][u], h ? 0x7362 : 0x5140));
                 mma16816(o[4 * u + 2 * h], p[0], p[1], p[2], p[3], x.x, y.x);
                 mma16816(o[4 * u + 2 * h + 1], p[0], p[1], p[2], p[3], x.y, y.y);
             }
-        if (__any_sync(FULL, nan & 0x80808080u)) nan_values(v);
-    }
-    // A NaN byte read as 480: every row sees every cached key, so its column is NaN for all of them.
-    __device__ __forceinline__ void nan_values(const uint32_t (&v)[4][VW]) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            bool bad = false;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) bad |= ((v[i][j / 4] >> (8 * (j & 3))) & 0x7f) == 0x7f;
-            // this lane holds column g of the block, the output's lane columns 2c and 2c + 1
-            const uint32_t hit = __ballot_sync(FULL, bad);
-            const float q = __int_as_float(0x7fffffff);
-            if (hit >> (8 * c) & 0xfu) o[j][0] = o[j][2] = q;
-            if (hit >> (8 * c + 4) & 0xfu) o[j][1] = o[j][3] = q;
-        }
     }
     // 16 keys of the tail, from bf16 rows.  bad_v: the item's keys whose value is not finite.
-    __device__ __forceinline__ void tail(const Chunk& x, const Seq& q, const uint4* qf, const float (&rq)[2], uint32_t* bad_v) {
-        const int64_t ring = ((int64_t)q.slot * P.Hkv + x.h) * 2 * P.page;
+    __device__ __forceinline__ void tail(int tok, const Seg& sg, const uint4* qf, const float (&rq)[2], uint32_t* bad_v) {
+        const Seq& q = sg.q;
+        const int64_t ring = ((int64_t)q.slot * P.Hkv + sg.h) * 2 * P.page;
         auto row = [&](int e, int which) -> const char* {                // a place that is there for every row
             const int64_t at = (ring + ((q.full + e) & (2 * P.page - 1))) * D * 2, n = e - q.open;
             const sv_host::Rows& src = which ? P.v : P.k;
             const char* p = e < q.open ? static_cast<const char*>(which ? P.c.v_open : P.c.k_open) + at
-                                       : src.p + x.b * src.b + n * src.n + x.h * src.h;
+                                       : src.p + sg.b * src.b + n * src.n + sg.h * src.h;
             return e < q.open + P.N ? p : P.q.p;
         };
         const int keys = q.open + P.N;
@@ -1553,12 +1537,12 @@ struct MmWarp {
         uint32_t kw[2][KH * 8];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const char* p = row(x.tok + 8 * i + g, 0) + 32 * c;
+            const char* p = row(tok + 8 * i + g, 0) + c * (D / 2);
 #pragma unroll
             for (int j = 0; j < KH; ++j)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(p + 128 * j + 16 * u);
+                    const uint4 w = *reinterpret_cast<const uint4*>(p + 32 * j + 16 * u);
                     kw[i][8 * j + 4 * u] = w.x; kw[i][8 * j + 4 * u + 1] = w.y;
                     kw[i][8 * j + 4 * u + 2] = w.z; kw[i][8 * j + 4 * u + 3] = w.w;
                 }
@@ -1583,7 +1567,7 @@ struct MmWarp {
         uint32_t vw[4][VW * 2];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int e = x.tok + 2 * c + (j & 1) + (j >> 1) * 8;
+            const int e = tok + 2 * c + (j & 1) + (j >> 1) * 8;
             const char* p = row(e, 1) + g * (D / 4);
 #pragma unroll
             for (int u = 0; u < VW / 2; ++u) {
@@ -1605,7 +1589,7 @@ struct MmWarp {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int n = min(g + 8 * r, P.R - 1) / P.G;
-            mask[r] = tail_bits(P, x.b, n, q.open, x.tok) & 0xffffu;
+            mask[r] = tail_bits(P, sg.b, n, q.open, tok) & 0xffffu;
         }
         softmax(s, rq, aa, bb, ii, mask, p);
 #pragma unroll
@@ -1615,18 +1599,18 @@ struct MmWarp {
                 mma16816(o[2 * u + h], p[0], p[1], p[2], p[3], __byte_perm(vw[0][u], vw[1][u], h ? 0x7632 : 0x5410),
                          __byte_perm(vw[2][u], vw[3][u], h ? 0x7632 : 0x5410));
     }
-    // The item's queries as fragments of this warp, and the factors of rows g and g + 8.
-    __device__ __forceinline__ void load_q(const Chunk& x, uint4* qf, float (&rq)[2]) {
+    // The item's queries as fragments, and the factors of rows g and g + 8.
+    __device__ __forceinline__ void load_q(const Seg& sg, uint4* qf, float (&rq)[2]) {
         uint32_t w[2][KH * 8];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int row = min(g + 8 * r, P.R - 1), n = row / P.G;
-            const char* p = P.q.p + x.b * P.q.b + n * P.q.n + (x.h * P.G + row - n * P.G) * P.q.h + 32 * c;
+            const char* p = P.q.p + sg.b * P.q.b + n * P.q.n + (sg.h * P.G + row - n * P.G) * P.q.h + c * (D / 2);
 #pragma unroll
             for (int j = 0; j < KH; ++j)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(p + 128 * j + 16 * u);
+                    const uint4 v = *reinterpret_cast<const uint4*>(p + 32 * j + 16 * u);
                     w[r][8 * j + 4 * u] = v.x; w[r][8 * j + 4 * u + 1] = v.y;
                     w[r][8 * j + 4 * u + 2] = v.z; w[r][8 * j + 4 * u + 3] = v.w;
                 }
@@ -1655,12 +1639,14 @@ struct MmWarp {
     }
 };
 
-template <int D> struct MmShared {
-    uint4 q[MM_WARPS][D / 16][32];                        // each warp's query fragments
-    float o[MM_WARPS][MM_ROWS][D + 4];
+template <int D> struct alignas(16) MmShared {
+    MmRing<D> ring[MM_WARPS];                             // 1024-byte aligned, as the swizzle wants
+    MmSlots slots[MM_WARPS];
+    uint4 q[D / 16][32];                                  // the query fragments: every warp writes the same
+    float4 o[MM_WARPS / 2][D / 8][32];                    // a warp's output fragments, for another one
     float m[MM_WARPS][MM_ROWS], l[MM_WARPS][MM_ROWS];
     uint32_t bad_v[12];
-    int bad;
+    int bad, late;
     MmAhead now, ahead[MM_WARPS];                         // the segment being computed; of each warp's next chunk
 };
 
@@ -1675,74 +1661,104 @@ __device__ __forceinline__ void mm_finish(const Att& P, MmWarp<D>& w, MmShared<D
     for (int r = 0; r < 2; ++r) {
         w.l[r] += __shfl_xor_sync(FULL, w.l[r], 1);
         w.l[r] += __shfl_xor_sync(FULL, w.l[r], 2);
-        const int row = w.g + 8 * r;
         if (w.c == 0) {
-            sh.m[w.warp][row] = w.m[r];
-            sh.l[w.warp][row] = w.l[r];
+            sh.m[w.warp][w.g + 8 * r] = w.m[r];
+            sh.l[w.warp][w.g + 8 * r] = w.l[r];
         }
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int j = 0; j < NT; j += 4)
-                *reinterpret_cast<float4*>(&sh.o[w.warp][row][(2 * w.c + s) * NT + j]) =
-                    make_float4(w.o[j][2 * r + s], w.o[j + 1][2 * r + s], w.o[j + 2][2 * r + s], w.o[j + 3][2 * r + s]);
     }
     if (bad) sh.bad = 1;
+    __syncthreads();
+    // every warp's output on the common maximum, then warps 2 and 3 to 0 and 1, and 1 to 0
+    float mm[2], l[2], f[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int row = w.g + 8 * r;
+        mm[r] = fmaxf(fmaxf(sh.m[0][row], sh.m[1][row]), fmaxf(sh.m[2][row], sh.m[3][row]));
+        const float base = mm[r] == NEG_INF ? 0.f : mm[r];
+        f[r] = ex2(w.m[r] - base);
+        l[r] = 0.f;
+#pragma unroll
+        for (int i = 0; i < MM_WARPS; ++i) l[r] = fmaf(ex2(sh.m[i][row] - base), sh.l[i][row], l[r]);
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        w.o[j][0] *= f[0]; w.o[j][1] *= f[0]; w.o[j][2] *= f[1]; w.o[j][3] *= f[1];
+        if (w.warp >= 2) sh.o[w.warp - 2][j][w.lane] = make_float4(w.o[j][0], w.o[j][1], w.o[j][2], w.o[j][3]);
+    }
+    __syncthreads();
+    if (w.warp < 2) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const float4 x = sh.o[w.warp][j][w.lane];
+            w.o[j][0] += x.x; w.o[j][1] += x.y; w.o[j][2] += x.z; w.o[j][3] += x.w;
+            if (w.warp == 1) sh.o[1][j][w.lane] = make_float4(w.o[j][0], w.o[j][1], w.o[j][2], w.o[j][3]);
+        }
+    }
     __syncthreads();
     const bool whole = g.t0 == 0 && g.t1 == g.q.ntiles;
     const bool nan = g.q.bad || sh.bad;
     const float quiet = __int_as_float(0x7fffffff);
     const int slot = g.item_lo + g.t0 == st.lo ? 0 : 1;
-    float* part = partial_of<D>(P, blockIdx.x, slot);
-    uint32_t any_bad = 0;
-    if (g.t1 > g.q.nct)
-        for (int i = 0; i < 12; ++i) any_bad |= sh.bad_v[i];
-    constexpr int LPR = D / 4;                            // lanes of a row, four dims each
-    for (int r = tid / LPR; r < P.R; r += MM_BT / LPR) {
-        const int d = tid % LPR * 4;
-        float mm = NEG_INF;
+    if (w.warp == 0) {
+        float* part = partial_of<D>(P, blockIdx.x, slot);
+        uint32_t any_bad = 0;
+        if (g.t1 > g.q.nct)
+            for (int i = 0; i < 12; ++i) any_bad |= sh.bad_v[i];
 #pragma unroll
-        for (int i = 0; i < MM_WARPS; ++i) mm = fmaxf(mm, sh.m[i][r]);
-        const float base = mm == NEG_INF ? 0.f : mm;
-        float l = 0.f, x[4] = {};
-#pragma unroll
-        for (int i = 0; i < MM_WARPS; ++i) {
-            const float f = ex2(sh.m[i][r] - base);
-            l = fmaf(f, sh.l[i][r], l);
-            const float4 v = *reinterpret_cast<const float4*>(&sh.o[i][r][d]);
-            x[0] = fmaf(f, v.x, x[0]); x[1] = fmaf(f, v.y, x[1]); x[2] = fmaf(f, v.z, x[2]); x[3] = fmaf(f, v.w, x[3]);
+        for (int j = 0; j < NT; ++j) {
+            const float4 x = sh.o[1][j][w.lane];
+            w.o[j][0] += x.x; w.o[j][1] += x.y; w.o[j][2] += x.z; w.o[j][3] += x.w;
         }
-        const int n = r / P.G;
-        if (any_bad) {
-            for (int i = 0; i < 12; ++i) {
-                uint32_t hit = sh.bad_v[i];
-                if (hit) hit &= tail_bits(P, g.b, n, g.q.open, 32 * i);
-                for (; hit; hit &= hit - 1) {
-                    const int e = 32 * i + __ffs(hit) - 1;
-                    const char* src = e < g.q.open
-                        ? static_cast<const char*>(P.c.v_open) +
-                              (((int64_t)g.q.slot * P.Hkv + g.h) * 2 * P.page + (g.q.full + e) % (2 * P.page)) * D * 2
-                        : P.v.p + g.b * P.v.b + (e - g.q.open) * P.v.n + g.h * P.v.h;
-                    const __nv_bfloat16* vv = reinterpret_cast<const __nv_bfloat16*>(src) + d;
-                    for (int j = 0; j < 4; ++j) {
-                        const float y = __bfloat162float(vv[j]);
-                        if (!(fabsf(y) <= 3.402823466e38f)) x[j] += y;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = w.g + 8 * r, n = row / P.G;
+            if (row >= P.R) continue;
+            // this lane's dims: blocks of D / 8 from 2c and 2c + 1 on
+            if (any_bad) {                                // values that could not enter the product
+                for (int i = 0; i < 12; ++i) {
+                    uint32_t hit = sh.bad_v[i];
+                    if (hit) hit &= tail_bits(P, g.b, n, g.q.open, 32 * i);
+                    for (; hit; hit &= hit - 1) {
+                        const int e = 32 * i + __ffs(hit) - 1;
+                        const char* src = e < g.q.open
+                            ? static_cast<const char*>(P.c.v_open) +
+                                  (((int64_t)g.q.slot * P.Hkv + g.h) * 2 * P.page + (g.q.full + e) % (2 * P.page)) * D * 2
+                            : P.v.p + g.b * P.v.b + (e - g.q.open) * P.v.n + g.h * P.v.h;
+                        const __nv_bfloat16* vv = reinterpret_cast<const __nv_bfloat16*>(src) + 2 * w.c * NT;
+#pragma unroll
+                        for (int j = 0; j < 2 * NT; ++j) {
+                            const float y = __bfloat162float(vv[j]);
+                            if (!(fabsf(y) <= 3.402823466e38f)) w.o[j % NT][2 * r + j / NT] += y;
+                        }
                     }
                 }
             }
-        }
-        const int64_t at = ((int64_t)g.b * P.N + n) * P.Hq + g.h * P.G + r - n * P.G;
-        if (nan) x[0] = x[1] = x[2] = x[3] = l = quiet;
-        if (whole) {
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            *reinterpret_cast<uint2*>(P.out + (at * D + d) * 2) =
-                make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
-            if (d == 0 && P.lse) P.lse[at] = nan ? quiet : l == 0.f ? NEG_INF : (mm - P_BIAS + log2f(l)) * LN2;
-        } else {
-            *reinterpret_cast<float4*>(part + (int64_t)r * D + d) = make_float4(x[0], x[1], x[2], x[3]);
-            if (d == 0) {
-                part[(int64_t)P.R * D + r] = mm == NEG_INF ? NEG_INF : mm - P_BIAS;
-                part[(int64_t)P.R * D + P.R + r] = l;
+            const int64_t at = ((int64_t)g.b * P.N + n) * P.Hq + g.h * P.G + row - n * P.G;
+            const float inv = nan ? quiet : l[r] == 0.f ? 0.f : 1.f / l[r];
+            if (whole) {
+                char* dst = P.out + (at * D + 2 * w.c * NT) * 2;
+#pragma unroll
+                for (int j = 0; j < 2 * NT; j += 8) {
+                    float x[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) x[u] = w.o[(j + u) % NT][2 * r + (j + u) / NT] * inv;
+                    *reinterpret_cast<uint4*>(dst + 2 * j) =
+                        make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+                }
+                if (w.c == 0 && P.lse) P.lse[at] = nan ? quiet : l[r] == 0.f ? NEG_INF : (mm[r] - P_BIAS + log2f(l[r])) * LN2;
+            } else {
+                float* dst = part + (int64_t)row * D + 2 * w.c * NT;
+#pragma unroll
+                for (int j = 0; j < 2 * NT; j += 4) {
+                    float x[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) x[u] = nan ? quiet : w.o[(j + u) % NT][2 * r + (j + u) / NT];
+                    *reinterpret_cast<float4*>(dst + j) = make_float4(x[0], x[1], x[2], x[3]);
+                }
+                if (w.c == 0) {
+                    part[(int64_t)P.R * D + row] = mm[r] == NEG_INF ? NEG_INF : mm[r] - P_BIAS;
+                    part[(int64_t)P.R * D + P.R + row] = nan ? quiet : l[r];
+                }
             }
         }
     }
@@ -1761,64 +1777,76 @@ __device__ __forceinline__ void mm_finish(const Att& P, MmWarp<D>& w, MmShared<D
 }
 
 template <int D>
-__global__ void __launch_bounds__(MM_BT, 3) k_attention_mma(const Att P) {
-    extern __shared__ __align__(16) unsigned char mm_smem[];
-    MmShared<D>& sh = *reinterpret_cast<MmShared<D>*>(mm_smem);
+__global__ void __launch_bounds__(MM_BT, MM_CTAS_SM) k_attention_mma(const Att P, const __grid_constant__ CUtensorMap kmap,
+                                                                     const __grid_constant__ CUtensorMap vmap) {
+    extern __shared__ unsigned char mm_smem[];
+    MmShared<D>& sh = *reinterpret_cast<MmShared<D>*>(mm_smem + (-smem_u32(mm_smem) & 1023u));
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Stretch st = find_stretch<MM_BT>(P);
     if (threadIdx.x == 0) P.cut[blockIdx.x].parts = 0;
     if (st.lo >= st.hi) return;
     if (threadIdx.x < 12) sh.bad_v[threadIdx.x] = 0;
-    if (threadIdx.x == 12) sh.bad = 0;
+    if (threadIdx.x == 12) sh.bad = sh.late = 0;
     if (threadIdx.x == 32) {
         sh.now.it.begin(P, st);
         sh.now.more = sh.now.it.next(P, sh.now.s);
     }
+    if (threadIdx.x == 64) {
+        for (int i = 0; i < MM_WARPS * MM_RING; ++i) bar_init(&sh.slots[i / MM_RING].full[i % MM_RING], 3);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        proxy_fence();
+    }
     __syncthreads();
     using W = MmWarp<D>;
     W w(P, threadIdx.x >> 5, sh.ahead[threadIdx.x >> 5]);
+    MmRing<D>& ring = sh.ring[w.warp];
+    MmSlots& slots = sh.slots[w.warp];
     w.begin(st);
-    uint4 k0[2][W::KH], k1[2][W::KH];
-    uint32_t v0[4][W::VW], v1[4][W::VW];
-    float ks0 = 1.f, vs0 = 1.f, ks1 = 1.f, vs1 = 1.f, rq[2];
-    uint4* qf = &sh.q[w.warp][0][0];
-    Chunk x = w.next();
-    int id0 = w.page_id(x);
-    w.fetch(x, id0, k0, v0, ks0, vs0);
-    Chunk y = w.next();
-    int id1 = w.page_id(y);
+    uint4* qf = &sh.q[0][0];
+    float rq[2];
+    int id, idy, idz, parity = -1;
+    // chunk x is computed, y and z are on their way, and the page id of the chunk after
+    Chunk x = w.next(id);
+    w.fetch(x, id, 0, ring, slots, &kmap, &vmap);
+    Chunk y = w.next(idy);
+    w.fetch(y, idy, 1, ring, slots, &kmap, &vmap);
+    Chunk z = y;
+    idz = 0;
+    if (y.kind()) z = w.next(idz);
     bool bad = false;
-    int seg = -1;
-    // chunk x is computed, y's bytes are on their way, z's page id is
-#define MM_STEP(K, V, KS, VS, ID, K2, V2, KS2, VS2, ID2)                                                       \
-    {                                                                                                          \
-        w.fetch(y, ID2, K2, V2, KS2, VS2);                                                                     \
-        if (x.seg != seg) {                                                                                    \
-            seg = x.seg;                                                                                       \
-            w.load_q(x, qf, rq);                                                                               \
-        }                                                                                                      \
-        const Chunk z = y.kind ? w.next() : y;                                                                 \
-        const int id2 = w.page_id(z);                                                                          \
-        if (x.kind == 1) {                                                                                     \
-            if (ID < 0 || ID >= P.c.num_pages) bad = true;                                                     \
-            else w.cached(K, V, KS, VS, qf, rq);                                                               \
-        } else if (x.kind == 2) {                                                                              \
-            w.tail(x, sh.now.s.q, qf, rq, sh.bad_v);                                                           \
-        }                                                                                                      \
-        if (y.kind == 0 || y.seg != x.seg) {                                                                   \
-            mm_finish<D>(P, w, sh, bad);                                                                       \
-            bad = false;                                                                                       \
-        }                                                                                                      \
-        if (y.kind == 0) break;                                                                                \
-        x = y;                                                                                                 \
-        y = z;                                                                                                 \
-        ID = id2;                                                                                              \
+    unsigned full = 0;                                    // parity of each slot's next phase
+    for (int s = 0; x.kind(); s = s == MM_RING - 1 ? 0 : s + 1) {
+        w.fetch(z, idz, s == 0 ? MM_RING - 1 : s - 1, ring, slots, &kmap, &vmap);
+        if (x.parity() != parity) {
+            parity = x.parity();
+            w.load_q(sh.now.s, qf, rq);
+        }
+        Chunk u = z;
+        int idu = 0;
+        if (z.kind()) u = w.next(idu);
+        if (!bar_try(&slots.full[s], full >> s & 1) && !bar_wait_slow(&slots.full[s], full >> s & 1, nullptr)) {
+            bad = true;
+            if (w.lane == 0) {                            // let it land (bounded), whatever becomes of the result
+                atomicOr(P.status, 1u << SPEC_ERR_TIMEOUT);
+                if (!bar_wait_slow(&slots.full[s], full >> s & 1, nullptr)) atomicOr(P.status, 1u << SPEC_ERR_COPY_IN_FLIGHT);
+            }
+            __syncwarp();
+        }
+        full ^= 1u << s;
+        if (x.kind() == 1 && id >= 0 && id < P.c.num_pages) w.cached(ring, slots, s, qf, rq);
+        else if (x.kind() == 2) w.tail(x.tok, sh.now.s, qf, rq, sh.bad_v);
+        bad |= x.kind() == 1 && (id < 0 || id >= P.c.num_pages);
+        if (y.kind() == 0 || y.parity() != x.parity()) {
+            mm_finish<D>(P, w, sh, bad);
+            bad = false;
+        }
+        x = y;
+        y = z;
+        z = u;
+        id = idy;
+        idy = idz;
+        idz = idu;
     }
-    while (true) {
-        MM_STEP(k0, v0, ks0, vs0, id0, k1, v1, ks1, vs1, id1)
-        MM_STEP(k1, v1, ks1, vs1, id1, k0, v0, ks0, vs0, id0)
-    }
-#undef MM_STEP
 }
 
 }  // namespace
@@ -1827,7 +1855,7 @@ using sv_host::fail;
 
 namespace {
 
-constexpr int TC_CTAS = 148, MM_CTAS = 3 * 148;      // CTAs at most
+constexpr int TC_CTAS = 148, MM_CTAS = MM_CTAS_SM * 148;      // CTAs at most
 
 template <int D>
 spec_status launch_merge(const Att& P, int ctas, cudaStream_t st) {
@@ -1845,9 +1873,9 @@ spec_status launch_merge(const Att& P, int ctas, cudaStream_t st) {
     return sv_host::launched("k_attention_merge");
 }
 
-// The cache's keys as a matrix of 8-bit rows: a box is one page of one head.
+// The cache's keys or values as a matrix of 8-bit rows; a box of `rows` of them (a page of one head, or a part of it).
 template <int D>
-spec_status key_map(const Att& P, CUtensorMap* map) {
+spec_status page_map(const Att& P, void* pages, int rows, CUtensorMap* map) {
     static std::atomic<void*> entry{nullptr};
     void* f = entry.load(std::memory_order_acquire);
     if (!f) {
@@ -1860,11 +1888,11 @@ spec_status key_map(const Att& P, CUtensorMap* map) {
     const bool empty = P.c.num_pages == 0;                // nothing is copied then: any address serves
     const cuuint64_t dims[2] = {(cuuint64_t)D, empty ? (cuuint64_t)P.page : (cuuint64_t)P.c.num_pages * P.Hkv * P.page};
     const cuuint64_t strides[1] = {(cuuint64_t)D};
-    const cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)P.page}, step[2] = {1, 1};
+    const cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)rows}, step[2] = {1, 1};
     const CUresult r = reinterpret_cast<CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                                      const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                                      CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill)>(f)(
-        map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, empty ? static_cast<void*>(P.out) : P.c.k_pages, dims, strides, box, step,
+        map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, empty ? static_cast<void*>(P.out) : pages, dims, strides, box, step,
         CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(SPEC_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", (int)r);
@@ -1877,7 +1905,7 @@ spec_status launch_tc(const Att& P, cudaStream_t st) {
     if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "k_attention_tc: %s", cudaGetErrorString(e));
     const int ctas = sv_host::num_sms() < TC_CTAS ? sv_host::num_sms() : TC_CTAS;
     CUtensorMap kmap;
-    if (const spec_status s = key_map<D>(P, &kmap)) return s;
+    if (const spec_status s = page_map<D>(P, P.c.k_pages, P.page, &kmap)) return s;
     k_attention_tc<D><<<ctas, TC_BT, tc_smem<D>(), st>>>(P, kmap);
     const spec_status s = sv_host::launched("k_attention_tc");
     return s == SPEC_OK ? launch_merge<D>(P, ctas, st) : s;
@@ -1885,11 +1913,14 @@ spec_status launch_tc(const Att& P, cudaStream_t st) {
 
 template <int D>
 spec_status launch_mma(const Att& P, cudaStream_t st) {
-    const size_t smem = sizeof(MmShared<D>);
+    const size_t smem = sizeof(MmShared<D>) + 1024;
     const cudaError_t e = cudaFuncSetAttribute(k_attention_mma<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "k_attention_mma: %s", cudaGetErrorString(e));
-    const int ctas = 3 * sv_host::num_sms() < MM_CTAS ? 3 * sv_host::num_sms() : MM_CTAS;
-    k_attention_mma<D><<<ctas, MM_BT, smem, st>>>(P);
+    CUtensorMap kmap, vmap;
+    if (const spec_status s = page_map<D>(P, P.c.k_pages, 16, &kmap)) return s;
+    if (const spec_status s = page_map<D>(P, P.c.v_pages, 16, &vmap)) return s;
+    const int want = MM_CTAS_SM * sv_host::num_sms(), ctas = want < MM_CTAS ? want : MM_CTAS;
+    k_attention_mma<D><<<ctas, MM_BT, smem, st>>>(P, kmap, vmap);
     const spec_status s = sv_host::launched("k_attention_mma");
     return s == SPEC_OK ? launch_merge<D>(P, ctas, st) : s;
 }
