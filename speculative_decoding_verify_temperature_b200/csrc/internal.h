@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "spec_verify.h"
 
 #define SV_HIDDEN __attribute__((visibility("hidden")))
@@ -25,6 +27,19 @@ struct Range {
     Range(const Range&) = delete;
     Range& operator=(const Range&) = delete;
 };
+
+// Dynamic shared memory for a kernel on the current device, set once per device: `done` is a
+// static of the caller, one for each kernel.
+inline spec_status allow_smem(const void* kernel, const char* what, size_t bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (e == cudaSuccess && (done.load(std::memory_order_acquire) & bit) != 0) return SPEC_OK;
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+    done.fetch_or(bit, std::memory_order_release);
+    return SPEC_OK;
+}
 
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 

@@ -1901,8 +1901,8 @@ spec_status page_map(const Att& P, void* pages, int rows, CUtensorMap* map) {
 
 template <int D>
 spec_status launch_tc(const Att& P, cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(k_attention_tc<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tc_smem<D>());
-    if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "k_attention_tc: %s", cudaGetErrorString(e));
+    static std::atomic<uint64_t> done{0};
+    if (const spec_status s = sv_host::allow_smem(reinterpret_cast<const void*>(k_attention_tc<D>), "k_attention_tc", tc_smem<D>(), done)) return s;
     const int ctas = sv_host::num_sms() < TC_CTAS ? sv_host::num_sms() : TC_CTAS;
     CUtensorMap kmap;
     if (const spec_status s = page_map<D>(P, P.c.k_pages, P.page, &kmap)) return s;
@@ -1914,8 +1914,8 @@ spec_status launch_tc(const Att& P, cudaStream_t st) {
 template <int D>
 spec_status launch_mma(const Att& P, cudaStream_t st) {
     const size_t smem = sizeof(MmShared<D>) + 1024;
-    const cudaError_t e = cudaFuncSetAttribute(k_attention_mma<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "k_attention_mma: %s", cudaGetErrorString(e));
+    static std::atomic<uint64_t> done{0};
+    if (const spec_status s = sv_host::allow_smem(reinterpret_cast<const void*>(k_attention_mma<D>), "k_attention_mma", smem, done)) return s;
     CUtensorMap kmap, vmap;
     if (const spec_status s = page_map<D>(P, P.c.k_pages, 16, &kmap)) return s;
     if (const spec_status s = page_map<D>(P, P.c.v_pages, 16, &vmap)) return s;

@@ -393,8 +393,9 @@ template <int DT, int R>
 spec_status launch_append_rows(const Append& P, dim3 grid, cudaStream_t st) {
     const size_t smem = (size_t)P.page * (P.rot / 2) * sizeof(float2);      // up to 64 KB
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(k_append<DT, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return sv_host::fail(SPEC_ERR_CUDA, "k_append: %s", cudaGetErrorString(e));
+        static std::atomic<uint64_t> done{0};
+        if (const spec_status s = sv_host::allow_smem(reinterpret_cast<const void*>(k_append<DT, R>), "k_append", 64 * 1024, done))
+            return s;
     }
     k_append<DT, R><<<grid, AP_BT, smem, st>>>(P);
     return sv_host::launched("k_append");

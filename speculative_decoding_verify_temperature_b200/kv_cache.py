@@ -39,6 +39,9 @@ class _CCache(ctypes.Structure):
 
 
 def _need(t, name, dtype, shape, device):
+    """A contiguous tensor of this type, shape and device, or an error that says what it is."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device:
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype != dtype:
@@ -47,24 +50,31 @@ def _need(t, name, dtype, shape, device):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+_strides = {}
 
 
 def _rows4(t, name, shape, dtype, device):
     """A [B, N, H, D] tensor with unit stride in D; its pointer and strides for the library."""
     if not isinstance(t, torch.Tensor) or t.dim() != 4:
         raise ValueError(f"{name} must be a [B, N, heads, D] tensor")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     s = t.stride()
     if s[3] != 1 and shape[3] > 1:
         raise ValueError(f"{name} must have unit stride in its last dim")
-    return t.data_ptr(), (ctypes.c_int64 * 3)(s[0], s[1], s[2])
+    c = _strides.get(s)
+    if c is None:
+        if len(_strides) > 4096:
+            _strides.clear()
+        c = _strides[s] = (ctypes.c_int64 * 3)(s[0], s[1], s[2])
+    return t.data_ptr(), c
 
 
 class KvCache:
@@ -145,20 +155,22 @@ _cache_ws = {}
 _ws_bytes = {}
 
 
+_same = contextlib.nullcontext()
+
+
 def _on(device, stream):
-    """The stream of a call and the context that makes it and its device current."""
+    """The handle of a call's stream and the context that makes it and its device current."""
     if device.type != "cuda":
         raise ValueError(f"tensors must be on a CUDA device, got {device}")
     if stream is not None:
         if stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        return stream, torch.cuda.stream(stream)
-    if torch.cuda.current_device() != device.index:
-        return torch.cuda.current_stream(device), torch.cuda.device(device)
-    return torch.cuda.current_stream(device), contextlib.nullcontext()
+        return stream.cuda_stream, torch.cuda.stream(stream)
+    handle = torch._C._cuda_getCurrentRawStream(device.index)
+    return handle, _same if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
 
 
-def _workspace(workspace, device, stream, B, N, q_heads, head_dim):
+def _workspace(workspace, device, handle, B, N, q_heads, head_dim):
     """The caller's workspace, or the stream's own; the stream and its device are current."""
     if workspace is not None:
         if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != device:
@@ -167,16 +179,17 @@ def _workspace(workspace, device, stream, B, N, q_heads, head_dim):
     key = (B, N, q_heads, head_dim)
     need = _ws_bytes.get(key)
     if need is None:
-        need = _ws_bytes[key] = spec_cache_workspace_bytes(*key)
-    if torch.cuda.is_current_stream_capturing():   # replays of several graphs may overlap: one each
-        buf = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
-        spec_workspace_init(buf, stream)
-        return buf
-    at = (device.index, stream.cuda_stream)
+        if len(_ws_bytes) > 4096:
+            _ws_bytes.clear()
+        need = _ws_bytes[key] = max(spec_cache_workspace_bytes(*key), 256)
+    at = (device.index, handle)
     buf = _cache_ws.get(at)
-    if buf is None or buf.numel() < need:
-        buf = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
-        spec_workspace_init(buf, stream)
+    if torch._C._cuda_isCurrentStreamCapturing():  # replays of several graphs may overlap: one each
+        buf = torch.empty(need, dtype=torch.uint8, device=device)
+        spec_workspace_init(buf)
+    elif buf is None or buf.numel() < need:
+        buf = torch.empty(need, dtype=torch.uint8, device=device)
+        spec_workspace_init(buf)
         _cache_ws[at] = buf
     return buf
 
@@ -201,17 +214,17 @@ def spec_tree_plan(parents, lengths, max_depth: int = 64, *, N: int | None = Non
     s, current = _on(dev, stream)
     with current:
         if out_positions is None:
-            out_positions = torch.empty((B, N), dtype=_I32, device=dev)
+            out_positions = lengths.new_empty((B, N))
         else:
             _need(out_positions, "out_positions", _I32, (B, N), dev)
         if out_ancestors is None:
-            out_ancestors = torch.empty((B, N, (N + 31) // 32), dtype=_I32, device=dev)
+            out_ancestors = lengths.new_empty((B, N, (N + 31) // 32))
         else:
             _need(out_ancestors, "out_ancestors", _I32, (B, N, (N + 31) // 32), dev)
         ws = _workspace(workspace, dev, s, 1, 1, 1, 64)
         _check(lib().spec_tree_plan(B, N, int(max_depth), None if parents is None else parents.data_ptr(),
                                     lengths.data_ptr(), out_positions.data_ptr(), out_ancestors.data_ptr(),
-                                    ws.data_ptr(), ws.numel(), s.cuda_stream), "spec_tree_plan")
+                                    ws.data_ptr(), ws.numel(), s), "spec_tree_plan")
     return out_positions, out_ancestors
 
 
@@ -260,13 +273,13 @@ def spec_qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None
     s, current = _on(dev, stream)
     with current:
         if q_out is None:
-            q_out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=dev)
+            q_out = q.new_empty((B, N, Hq, D))
         if k_out is None:
-            k_out = torch.empty((B, N, Hk, D), dtype=q.dtype, device=dev)
+            k_out = q.new_empty((B, N, Hk, D))
         qop, qos = _rows4(q_out, "q_out", (B, N, Hq, D), q.dtype, dev)
         kop, kos = _rows4(k_out, "k_out", (B, N, Hk, D), q.dtype, dev)
         _check(lib().spec_qk_norm_rope(B, N, Hq, Hk, D, qp, qs, kp, ks, dt, positions.data_ptr(), freq, rot,
-                                       int(bool(interleaved)), qw, kw, wdt, eps, qop, qos, kop, kos, s.cuda_stream),
+                                       int(bool(interleaved)), qw, kw, wdt, eps, qop, qos, kop, kos, s),
                "spec_qk_norm_rope")
     return q_out, k_out
 
@@ -291,19 +304,19 @@ def spec_tree_attention(q, k, v, cache: KvCache, ancestors=None, *, scale: float
     s, current = _on(dev, stream)
     with current:
         if out is None:
-            out = torch.empty((B, N, Hq, D), dtype=bf, device=dev)
+            out = q.new_empty((B, N, Hq, D))
         else:
             _need(out, "out", bf, (B, N, Hq, D), dev)
         if lse is not None:
             _need(lse, "lse", _F32, (B, N, Hq), dev)
         elif return_lse:
-            lse = torch.empty((B, N, Hq), dtype=_F32, device=dev)
+            lse = q.new_empty((B, N, Hq), dtype=_F32)
         ws = _workspace(workspace, dev, s, B, N, Hq, D)
         _check(lib().spec_tree_attention(B, N, Hq, cache._ref, qp, qs, kp, ks, vp, vs,
                                          None if ancestors is None else ancestors.data_ptr(),
                                          1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(),
                                          None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
-                                         s.cuda_stream), "spec_tree_attention")
+                                         s), "spec_tree_attention")
     return (out, lse) if return_lse else out
 
 
@@ -342,5 +355,5 @@ def spec_kv_append(k, v, num_accepted, cache: KvCache, *, accept_index=None, inv
                                     None if num_accepted is None else num_accepted.data_ptr(),
                                     None if accept_index is None else accept_index.data_ptr(), freq, rot,
                                     int(bool(interleaved)), kw, wdt, eps, out_lengths.data_ptr(), ws.data_ptr(),
-                                    ws.numel(), s.cuda_stream), "spec_kv_append")
+                                    ws.numel(), s), "spec_kv_append")
     return out_lengths
