@@ -78,8 +78,47 @@ __device__ __forceinline__ float2 cos_sin(int pos, float f) {
     return make_float2(c, s);
 }
 
+// Four consecutive elements.
+template <int DT> struct Quad;
+template <> struct Quad<SPEC_BF16> {
+    uint2 a;
+    __device__ __forceinline__ void load(const char* p) { a = *reinterpret_cast<const uint2*>(p); }
+    __device__ __forceinline__ void load_bf16(const char* p) { load(p); }
+    __device__ __forceinline__ void zero() { a = make_uint2(0, 0); }
+    __device__ __forceinline__ void get(float* x) const { x[0] = bf_lo(a.x); x[1] = bf_hi(a.x); x[2] = bf_lo(a.y); x[3] = bf_hi(a.y); }
+    __device__ __forceinline__ void set(const float* x) { a = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])); }
+    __device__ __forceinline__ void store(char* p) const { *reinterpret_cast<uint2*>(p) = a; }
+};
+template <> struct Quad<SPEC_F32> {
+    float4 a;
+    __device__ __forceinline__ void load(const char* p) { a = *reinterpret_cast<const float4*>(p); }
+    __device__ __forceinline__ void load_bf16(const char* p) {
+        const uint2 w = *reinterpret_cast<const uint2*>(p);
+        a = make_float4(bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y));
+    }
+    __device__ __forceinline__ void zero() { a = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float* x) const { x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; }
+    __device__ __forceinline__ void set(const float* x) { a = make_float4(x[0], x[1], x[2], x[3]); }
+    __device__ __forceinline__ void store(char* p) const { *reinterpret_cast<float4*>(p) = a; }
+};
+
 // A head row of D elements lies in D / 8 consecutive lanes of an aligned group
-// of GW lanes, eight elements each; the lanes behind hold zeros.  l: lane of the group.
+// of GW lanes, two quads (four consecutive elements) in each; the lanes behind
+// hold zeros.  The quads are chosen so that both elements of a rotated pair are
+// in one lane: quads l and l + rot / 8 where the pairs are half a rotation apart,
+// neighbours elsewhere.  In both orders lane l turns the pairs 4l to 4l + 3.
+struct Quads {
+    int q0, q1;
+    bool turns;
+    __device__ __forceinline__ Quads(int l, int rot, bool interleaved) {
+        const int n = rot / 8;
+        turns = l < n;
+        const bool split = turns && !interleaved;
+        q0 = split ? l : 2 * l;
+        q1 = split ? l + n : 2 * l + 1;
+    }
+};
+
 // 1 / rms of the row, in every lane of the group; all lanes of the warp call it.
 __device__ __forceinline__ float row_rms(const float (&x)[8], int GW, float inv_d, float eps) {
     float ss = 0.f;
@@ -89,33 +128,23 @@ __device__ __forceinline__ float row_rms(const float (&x)[8], int GW, float inv_
     return rsqrtf(fmaf(ss, inv_d, eps));
 }
 
-// First index of the eight (split halves) or four (interleaved) pairs whose
-// angles lane l uses.
-__device__ __forceinline__ int pair_base(int l, int rot, bool interleaved) {
-    return interleaved ? 4 * l : (8 * l < rot / 2 ? 8 * l : 8 * l - rot / 2);
-}
-
-// Rotate the row's first `rot` elements; c, s are the angles of the lane's pairs.
-// All lanes of the warp call it.
-__device__ __forceinline__ void row_rotate(float (&x)[8], const float (&c)[8], const float (&s)[8], int l, int lane,
-                                           int rot, bool interleaved) {
+// Turn the lane's four pairs: (x[i], x[4 + i]), or neighbours.
+__device__ __forceinline__ void row_rotate(float (&x)[8], const float4& c, const float4& s, bool interleaved) {
+    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
     if (interleaved) {
-        if (8 * l < rot) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float a = x[2 * i], b = x[2 * i + 1];
-                x[2 * i] = a * c[i] - b * s[i];
-                x[2 * i + 1] = b * c[i] + a * s[i];
-            }
+        for (int i = 0; i < 4; ++i) {
+            const float a = x[2 * i], b = x[2 * i + 1];
+            x[2 * i] = a * cc[i] - b * ss[i];
+            x[2 * i + 1] = b * cc[i] + a * ss[i];
         }
-        return;
-    }
-    const bool first = 8 * l < rot / 2;
-    const int src = 8 * l < rot ? (first ? lane + rot / 16 : lane - rot / 16) : lane;
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float o = __shfl_sync(FULL, x[i], src);
-        if (8 * l < rot) x[i] = first ? x[i] * c[i] - o * s[i] : x[i] * c[i] + o * s[i];
+        for (int i = 0; i < 4; ++i) {
+            const float a = x[i], b = x[4 + i];
+            x[i] = a * cc[i] - b * ss[i];
+            x[4 + i] = b * cc[i] + a * ss[i];
+        }
     }
 }
 

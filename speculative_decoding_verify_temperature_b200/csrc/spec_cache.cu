@@ -71,71 +71,68 @@ struct NormRope {
     float eps;
 };
 
-__device__ __forceinline__ void load_weight(const char* w, int f32, int e, float (&x)[8]) {
-    if (f32) {
-        Vec8<SPEC_F32> v;
-        v.load(w + 4 * e);
-        v.get(x);
-    } else {
-        Vec8<SPEC_BF16> v;
-        v.load(w + 2 * e);
-        v.get(x);
-    }
+constexpr int NR_BT = 128;
+constexpr int NR_U = 3;                 // head rows in flight per group of lanes
+
+__device__ __forceinline__ float weight_at(const char* w, int f32, int e) {
+    return f32 ? __ldg(reinterpret_cast<const float*>(w) + e)
+               : __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short*>(w) + e) << 16);
 }
 
-constexpr int NR_BT = 256;
-constexpr int NR_U = 4;                 // head rows in flight per group of lanes
-
 // A CTA holds one token and some of its heads: a group of GW lanes takes a head
-// row, eight elements per lane, so a bf16 row of 128 is one 16-byte load per
-// lane and the sum of squares is a reduction in the group.  The angles of a
-// token are the same for all of its heads: each is formed once per CTA, in
-// f64, while the first rows are on their way.  Bound by HBM: each element is
-// read and written once.
+// row, eight elements per lane, both elements of a rotated pair in the same one, so
+// that the only traffic between lanes is the sum of squares.  The angles of a
+// token are the same for all of its heads: each is formed once per CTA, in f64,
+// while the first rows are on their way.  Bound by HBM: each element is read and written once.
 template <int DT>
 __global__ void __launch_bounds__(NR_BT) k_norm_rope(const NormRope P) {
-    __shared__ float2 cs[128];
-    const int tok = blockIdx.x, b = tok / P.N, n = tok % P.N;
-    const int lane = threadIdx.x & 31, GW = P.GW, l = lane & (GW - 1);
+    __shared__ __align__(16) float cs[2][128], wt[2][256];
+    constexpr int ESZ = Vec8<DT>::ESZ;
+    const int tok = blockIdx.x, b = tok / P.N, n = tok - b * P.N;
+    const int GW = P.GW, l = threadIdx.x & (GW - 1);
     const int groups = NR_BT / GW, grp = threadIdx.x / GW;
     const int heads = P.Hq + P.Hk;
     const int per = (heads + gridDim.y - 1) / gridDim.y;
     const int h0 = blockIdx.y * per, h1 = min(heads, h0 + per);
     const bool on = 8 * l < P.D;
-    const int64_t e = 8 * (int64_t)l * Vec8<DT>::ESZ;
-    const char* q = P.q.p + b * P.q.b + n * P.q.n + e;
-    const char* k = P.k.p + b * P.k.b + n * P.k.n + e;
-    char* qo = P.qo.p + b * P.qo.b + n * P.qo.n + e;
-    char* ko = P.ko.p + b * P.ko.b + n * P.ko.n + e;
+    const Quads at(l, P.rot, P.interleaved);
+    const char* q = P.q.p + b * P.q.b + n * P.q.n;
+    const char* k = P.k.p + b * P.k.b + n * P.k.n;
+    char* qo = P.qo.p + b * P.qo.b + n * P.qo.n;
+    char* ko = P.ko.p + b * P.ko.b + n * P.ko.n;
+    const int o0 = at.q0 * 4 * ESZ, o1 = at.q1 * 4 * ESZ;
     const int pos = P.pos[tok];
-    float c[8], s[8], qw[8], kw[8];
-    if (P.qw && on) load_weight(P.qw, P.w_f32, 8 * l, qw);
-    if (P.kw && on) load_weight(P.kw, P.w_f32, 8 * l, kw);
     const float inv_d = 1.f / (float)P.D;
-    bool first = true;
+    float4 c, s;
     for (int base = h0; base < h1; base += groups * NR_U) {
-        Vec8<DT> r[NR_U];
+        Quad<DT> r[NR_U][2];
 #pragma unroll
         for (int u = 0; u < NR_U; ++u) {
             const int h = base + u * groups + grp;
-            r[u].zero();
-            if (h < h1 && on && pos >= 0) r[u].load_plain(h < P.Hq ? q + h * P.q.h : k + (h - P.Hq) * P.k.h);
-        }
-        if (first) {
-            first = false;
-            if (P.rot && pos >= 0) {
-                for (int j = threadIdx.x; j < P.rot / 2; j += NR_BT) cs[j] = cos_sin(pos, P.inv_freq[j]);
+            r[u][0].zero();
+            r[u][1].zero();
+            if (h < h1 && on && pos >= 0) {
+                const char* p = h < P.Hq ? q + h * P.q.h : k + (h - P.Hq) * P.k.h;
+                r[u][0].load(p + o0);
+                r[u][1].load(p + o1);
             }
-            __syncthreads();
-            if (8 * l < P.rot) {
-                const int j = pair_base(l, P.rot, P.interleaved);
-                const int cnt = P.interleaved ? 4 : 8;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 v = i < cnt ? cs[j + i] : make_float2(0.f, 0.f);
-                    c[i] = v.x;
-                    s[i] = v.y;
+        }
+        if (base == h0) {
+            if (pos >= 0)
+                for (int j = threadIdx.x; j < P.rot / 2; j += NR_BT) {
+                    const float2 v = cos_sin(pos, P.inv_freq[j]);
+                    cs[0][j] = v.x;
+                    cs[1][j] = v.y;
                 }
+            if (P.qw || P.kw)
+                for (int e = threadIdx.x; e < P.D; e += NR_BT) {
+                    if (P.qw) wt[0][e] = weight_at(P.qw, P.w_f32, e);
+                    if (P.kw) wt[1][e] = weight_at(P.kw, P.w_f32, e);
+                }
+            __syncthreads();
+            if (at.turns) {
+                c = *reinterpret_cast<const float4*>(&cs[0][4 * l]);
+                s = *reinterpret_cast<const float4*>(&cs[1][4 * l]);
             }
         }
 #pragma unroll
@@ -143,22 +140,28 @@ __global__ void __launch_bounds__(NR_BT) k_norm_rope(const NormRope P) {
             if (base + u * groups >= h1) break;           // the same for the whole CTA
             const int h = base + u * groups + grp;
             float x[8];
-            r[u].get(x);
+            r[u][0].get(x);
+            r[u][1].get(x + 4);
             if (P.qw || P.kw) {                           // a warp may hold query and key rows: all lanes reduce
                 const float rs = row_rms(x, GW, inv_d, P.eps);
-                if ((h < P.Hq ? P.qw : P.kw) != nullptr) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = x[i] * rs * (h < P.Hq ? qw[i] : kw[i]);
+                if ((h < P.Hq ? P.qw : P.kw) != nullptr && on) {
+                    const float* w = wt[h < P.Hq ? 0 : 1];
+                    const float4 w0 = *reinterpret_cast<const float4*>(w + 4 * at.q0), w1 = *reinterpret_cast<const float4*>(w + 4 * at.q1);
+                    x[0] = x[0] * rs * w0.x; x[1] = x[1] * rs * w0.y; x[2] = x[2] * rs * w0.z; x[3] = x[3] * rs * w0.w;
+                    x[4] = x[4] * rs * w1.x; x[5] = x[5] * rs * w1.y; x[6] = x[6] * rs * w1.z; x[7] = x[7] * rs * w1.w;
                 }
             }
-            if (P.rot) row_rotate(x, c, s, l, lane, P.rot, P.interleaved);
+            if (at.turns) row_rotate(x, c, s, P.interleaved);
             if (h < h1 && on) {
                 if (pos < 0) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) x[i] = 0.f;
                 }
-                r[u].set(x);
-                r[u].store(h < P.Hq ? qo + h * P.qo.h : ko + (h - P.Hq) * P.ko.h);
+                char* p = h < P.Hq ? qo + h * P.qo.h : ko + (h - P.Hq) * P.ko.h;
+                r[u][0].set(x);
+                r[u][1].set(x + 4);
+                r[u][0].store(p + o0);
+                r[u][1].store(p + o1);
             }
         }
     }
@@ -200,15 +203,18 @@ __device__ __forceinline__ float block_scale(float amax) {
 // and its 8-bit form written once), by latency for a round's few rows.
 template <int DT, int R>
 __global__ void __launch_bounds__(AP_BT) k_append(const Append P) {
-    extern __shared__ float2 cs[];                    // [row of the block][pair]
-    __shared__ float red[2][AP_BT / 32];
+    // cosines, then sines [row of the block][pair]; the partial rotations that they are made of
+    extern __shared__ __align__(16) float ct[];
+    float* st = ct + P.page * (P.rot / 2);
+    float2* tr = reinterpret_cast<float2*>(st + P.page * (P.rot / 2));
+    __shared__ __align__(16) float wt[128];
+    __shared__ uint32_t red[2][AP_BT / 32];
     __shared__ int sh_len;
     const int page = P.page, D = P.D, GW = P.GW;
     const int hgroups = (P.Hkv + P.heads_per_cta - 1) / P.heads_per_cta;
     const int b = blockIdx.y / hgroups, h0 = (blockIdx.y % hgroups) * P.heads_per_cta;
     const int h1 = min(P.Hkv, h0 + P.heads_per_cta);
     const int tid = threadIdx.x, lane = tid & 31, l = lane & (GW - 1), grp = tid / GW;
-    constexpr int WARPS = AP_BT / 32;
 
     // every CTA of the sequence comes to the same verdict; the last to have read
     // the length writes the new one, which may be the same word
@@ -255,12 +261,11 @@ __global__ void __launch_bounds__(AP_BT) k_append(const Append P) {
     const bool chained = len % page != 0 && newlen % page != 0 && last >= first + 2 && ((last - first) & 1) == 0;
     if (chained && blk == last) return;
 
-    const bool on = 8 * l < D;
-    const int groups = AP_BT / GW;
-    float kw[8];
-    if (P.kw && on) load_weight(P.kw, P.w_f32, 8 * l, kw);
+    const int groups = AP_BT / GW;                        // D / 8 is 8 or 16: all lanes of a group hold elements
     const float inv_d = 1.f / (float)D;
     const int half = P.rot / 2;
+    if (P.kw)
+        for (int e = tid; e < D; e += AP_BT) wt[e] = weight_at(P.kw, P.w_f32, e);
 
     while (true) {
         const int start = blk * page;
@@ -268,133 +273,143 @@ __global__ void __launch_bounds__(AP_BT) k_append(const Append P) {
         int page_id = 0;
         if (full) page_id = P.c.page_table[b * P.c.page_table_stride + blk];
         if (half) {
-            for (int i = tid; i < page * half; i += AP_BT) {
-                const int r = i / half, t = start + r;
-                if (t >= len && t < newlen) cs[i] = cos_sin(t, P.inv_freq[i - r * half]);
+            // The angle of row r is the block's first plus 8 (r / 8) steps plus r mod 8: 1 + page / 8 + 8 sines and
+            // cosines per pair and a product of three rotations for each row, instead of `page` of them.
+            const int parts = 1 + (page >> 3) + 8;
+            for (int i = tid; i < parts * half; i += AP_BT) {
+                const int m = i / half, j = i - m * half;
+                const int steps = m == 0 ? start : m <= (page >> 3) ? 8 * (m - 1) : m - 1 - (page >> 3);
+                tr[i] = cos_sin(steps, P.inv_freq[j]);
             }
             __syncthreads();
+            for (int i = tid; i < page * half; i += AP_BT) {
+                const int r = i / half, j = i - r * half;
+                const float2 a = tr[j], u = tr[(1 + (r >> 3)) * half + j], v = tr[(1 + (page >> 3) + (r & 7)) * half + j];
+                const float2 w = make_float2(a.x * u.x - a.y * u.y, a.x * u.y + a.y * u.x);
+                ct[i] = w.x * v.x - w.y * v.y;
+                st[i] = w.x * v.y + w.y * v.x;
+            }
         }
-        for (int h = h0; h < h1; ++h) {
-            Vec8<SPEC_BF16> val[2][R];
-            float amax[2] = {0.f, 0.f};
+        __syncthreads();
+        // one (head, keys or values) after the other, the next one's rows on their way
+        Quad<DT> raw[R][2];
+        const int items = 2 * (h1 - h0);
+        auto fetch = [&](int it) {
+            const int which = it & 1, h = h0 + (it >> 1);
+            const Quads at(l, which ? 0 : P.rot, P.interleaved);
+            const sv_host::Rows& src = which ? P.v : P.k;
+            const char* ring = static_cast<const char*>(which ? P.c.v_open : P.c.k_open) + ((int64_t)slot * P.Hkv + h) * 2 * page * D * 2;
 #pragma unroll
-            for (int which = 0; which < 2; ++which) {
-                const sv_host::Rows& src = which ? P.v : P.k;
-                const char* ring = static_cast<const char*>(which ? P.c.v_open : P.c.k_open) +
-                                   ((int64_t)slot * P.Hkv + h) * 2 * page * D * 2;
-                Vec8<DT> raw[R];
-#pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    const int r = grp + i * groups, t = start + r;
-                    raw[i].zero();
-                    val[which][i].zero();
-                    if (r < page && on) {
-                        if (t < len) {
-                            val[which][i].load_plain(ring + ((int64_t)(t % (2 * page)) * D + 8 * l) * 2);
-                        } else if (t < newlen) {
-                            const int row = P.index ? P.index[(int64_t)b * P.W + (t - len)] : t - len;
-                            raw[i].load(src.p + b * src.b + row * src.n + h * src.h + 8 * (int64_t)l * Vec8<DT>::ESZ);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    const int r = grp + i * groups, t = start + r;
-                    float x[8];
-                    raw[i].get(x);
-                    if (which == 0) {
-                        if (P.kw) {
-                            const float rs = row_rms(x, GW, inv_d, P.eps);
-#pragma unroll
-                            for (int u = 0; u < 8; ++u) x[u] = x[u] * rs * kw[u];
-                        }
-                        if (half) {
-                            float c[8], s[8];
-                            if (8 * l < P.rot && r < page) {
-                                const int j = r * half + pair_base(l, P.rot, P.interleaved);
-                                const int n = P.interleaved ? 4 : 8;
-#pragma unroll
-                                for (int u = 0; u < 8; ++u) {
-                                    const float2 w = u < n ? cs[j + u] : make_float2(0.f, 0.f);
-                                    c[u] = w.x;
-                                    s[u] = w.y;
-                                }
-                            }
-                            row_rotate(x, c, s, l, lane, P.rot, P.interleaved);
-                        }
-                    }
-                    if (r < page && on && t >= len && t < newlen) val[which][i].set(x);
-                    val[which][i].get(x);
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) {
-                        const float a = fabsf(x[u]);
-                        if (a <= 3.402823466e38f) amax[which] = fmaxf(amax[which], a);
-                    }
+            for (int i = 0; i < R; ++i) {
+                const int r = grp + i * groups, t = start + r;
+                raw[i][0].zero();
+                raw[i][1].zero();
+                if (r >= page) continue;
+                if (t < len) {
+                    const char* p = ring + (int64_t)(t & (2 * page - 1)) * D * 2;
+                    raw[i][0].load_bf16(p + 8 * at.q0);
+                    raw[i][1].load_bf16(p + 8 * at.q1);
+                } else if (t < newlen) {
+                    const int row = P.index ? P.index[(int64_t)b * P.W + (t - len)] : t - len;
+                    const char* p = src.p + b * src.b + row * src.n + h * src.h;
+                    raw[i][0].load(p + at.q0 * 4 * Vec8<DT>::ESZ);
+                    raw[i][1].load(p + at.q1 * 4 * Vec8<DT>::ESZ);
                 }
             }
-            if (full) {
+        };
+        fetch(0);
+        for (int it = 0; it < items; ++it) {
+            const int which = it & 1, h = h0 + (it >> 1);
+            const Quads at(l, which ? 0 : P.rot, P.interleaved);
+            Quad<SPEC_BF16> val[R][2];
+            uint32_t m = 0;
 #pragma unroll
-                for (int o = 16; o; o >>= 1) {
-                    amax[0] = fmaxf(amax[0], __shfl_xor_sync(FULL, amax[0], o));
-                    amax[1] = fmaxf(amax[1], __shfl_xor_sync(FULL, amax[1], o));
-                }
-                __syncthreads();                      // the values of the head before have been read
-                if (lane == 0) {
-                    red[0][tid >> 5] = amax[0];
-                    red[1][tid >> 5] = amax[1];
-                }
-                __syncthreads();
-#pragma unroll
-                for (int which = 0; which < 2; ++which) {
-                    float m = red[which][0];
-#pragma unroll
-                    for (int w = 1; w < WARPS; ++w) m = fmaxf(m, red[which][w]);
-                    const float sc = block_scale(m), inv = 1.f / sc;      // exact: a power of two
-                    const int64_t ph = (int64_t)page_id * P.Hkv + h;
-                    if (tid == 0) (which ? P.c.v_scale : P.c.k_scale)[ph] = sc;
-                    char* dst = static_cast<char*>(which ? P.c.v_pages : P.c.k_pages) + ph * page * D;
-#pragma unroll
-                    for (int i = 0; i < R; ++i) {
-                        const int r = grp + i * groups;
-                        if (r < page && on) {
-                            float x[8];
-                            val[which][i].get(x);
-#pragma unroll
-                            for (int u = 0; u < 8; ++u)
-                                x[u] = fabsf(x[u]) <= 3.402823466e38f ? x[u] * inv : __int_as_float(0x7fffffff);
-                            uint2 o;
-                            o.x = pack_e4m3(x[0], x[1]) | pack_e4m3(x[2], x[3]) << 16;
-                            o.y = pack_e4m3(x[4], x[5]) | pack_e4m3(x[6], x[7]) << 16;
-                            *reinterpret_cast<uint2*>(dst + (int64_t)r * D + 8 * l) = o;
+            for (int i = 0; i < R; ++i) {
+                const int r = grp + i * groups, t = start + r;
+                float x[8];
+                raw[i][0].get(x);
+                raw[i][1].get(x + 4);
+                if (which == 0) {                         // rows of the ring are what they are
+                    if (P.kw) {
+                        const float rs = row_rms(x, GW, inv_d, P.eps);
+                        const float4 w0 = *reinterpret_cast<const float4*>(wt + 4 * at.q0), w1 = *reinterpret_cast<const float4*>(wt + 4 * at.q1);
+                        if (t >= len) {
+                            x[0] = x[0] * rs * w0.x; x[1] = x[1] * rs * w0.y; x[2] = x[2] * rs * w0.z; x[3] = x[3] * rs * w0.w;
+                            x[4] = x[4] * rs * w1.x; x[5] = x[5] * rs * w1.y; x[6] = x[6] * rs * w1.z; x[7] = x[7] * rs * w1.w;
                         }
                     }
+                    if (at.turns && r < page && t >= len)
+                        row_rotate(x, *reinterpret_cast<const float4*>(ct + r * half + 4 * l),
+                                   *reinterpret_cast<const float4*>(st + r * half + 4 * l), P.interleaved);
                 }
-            } else {
+                val[i][0].set(x);
+                val[i][1].set(x + 4);
+                m = __vmaxu2(m, __vmaxu2(__vmaxu2(val[i][0].a.x & 0x7fff7fffu, val[i][0].a.y & 0x7fff7fffu),
+                                         __vmaxu2(val[i][1].a.x & 0x7fff7fffu, val[i][1].a.y & 0x7fff7fffu)));
+            }
+            if (it + 1 < items) fetch(it + 1);
+            if (!full) {
+                char* ring = static_cast<char*>(which ? P.c.v_open : P.c.k_open) + ((int64_t)slot * P.Hkv + h) * 2 * page * D * 2;
 #pragma unroll
-                for (int which = 0; which < 2; ++which) {
-                    char* ring = static_cast<char*>(which ? P.c.v_open : P.c.k_open) +
-                                 ((int64_t)slot * P.Hkv + h) * 2 * page * D * 2;
-#pragma unroll
-                    for (int i = 0; i < R; ++i) {
-                        const int r = grp + i * groups, t = start + r;
-                        if (r < page && on && t >= len && t < newlen)
-                            val[which][i].store(ring + ((int64_t)(t % (2 * page)) * D + 8 * l) * 2);
+                for (int i = 0; i < R; ++i) {
+                    const int r = grp + i * groups, t = start + r;
+                    if (r < page && t >= len && t < newlen) {
+                        char* p = ring + (int64_t)(t & (2 * page - 1)) * D * 2;
+                        val[i][0].store(p + 8 * at.q0);
+                        val[i][1].store(p + 8 * at.q1);
                     }
                 }
+                continue;
+            }
+            m = max(m & 0xffffu, m >> 16);                // bits of the largest magnitude
+            const bool odd = m >= 0x7f80u;                // something here is not finite
+            if (odd) {
+                m = 0;
+                for (int i = 0; i < R; ++i)
+                    for (int u = 0; u < 8; ++u) {
+                        const uint2 w = val[i][u >> 2].a;
+                        const uint32_t a = ((u & 2 ? w.y : w.x) >> (u & 1 ? 16 : 0)) & 0x7fffu;
+                        if (a < 0x7f80u) m = max(m, a);
+                    }
+            }
+            m = __reduce_max_sync(FULL, m);
+            if (lane == 0) red[it & 1][tid >> 5] = m;
+            __syncthreads();                              // of the two rows of `red`, the other is still being read
+            m = red[it & 1][0];
+#pragma unroll
+            for (int w = 1; w < AP_BT / 32; ++w) m = max(m, red[it & 1][w]);
+            const float sc = block_scale(__uint_as_float(m << 16)), inv = 1.f / sc;      // exact: a power of two
+            const int64_t ph = (int64_t)page_id * P.Hkv + h;
+            if (tid == 0) (which ? P.c.v_scale : P.c.k_scale)[ph] = sc;
+            char* dst = static_cast<char*>(which ? P.c.v_pages : P.c.k_pages) + ph * page * D;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int r = grp + i * groups;
+                if (r >= page) continue;
+                float x[8];
+                val[i][0].get(x);
+                val[i][1].get(x + 4);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    x[u] *= inv;
+                    if (odd && !(fabsf(x[u]) <= 448.f)) x[u] = __int_as_float(0x7fffffff);
+                }
+                *reinterpret_cast<uint32_t*>(dst + (int64_t)r * D + 4 * at.q0) = pack_e4m3(x[0], x[1]) | pack_e4m3(x[2], x[3]) << 16;
+                *reinterpret_cast<uint32_t*>(dst + (int64_t)r * D + 4 * at.q1) = pack_e4m3(x[4], x[5]) | pack_e4m3(x[6], x[7]) << 16;
             }
         }
         if (!chained || blk != first) break;
-        __syncthreads();                              // the first block's ring rows have been read
+        __syncthreads();                                  // the first block's ring rows and angles have been read
         blk = last;
     }
 }
 
 template <int DT, int R>
 spec_status launch_append_rows(const Append& P, dim3 grid, cudaStream_t st) {
-    const size_t smem = (size_t)P.page * (P.rot / 2) * sizeof(float2);      // up to 64 KB
+    const size_t smem = (size_t)(P.page + 1 + P.page / 8 + 8) * (P.rot / 2) * sizeof(float2);   // up to 76.5 KB
     if (smem > 48 * 1024) {
         static std::atomic<uint64_t> done{0};
-        if (const spec_status s = sv_host::allow_smem(reinterpret_cast<const void*>(k_append<DT, R>), "k_append", 64 * 1024, done))
+        if (const spec_status s = sv_host::allow_smem(reinterpret_cast<const void*>(k_append<DT, R>), "k_append", 80 * 1024, done))
             return s;
     }
     k_append<DT, R><<<grid, AP_BT, smem, st>>>(P);
