@@ -184,13 +184,10 @@ struct Append {
 
 constexpr int AP_BT = 256;
 
-// Scale of a block: the least power of two s (at least 2^-126) with amax / s <= 448.
-__device__ __forceinline__ float block_scale(float amax) {
-    if (!(amax > 0.f)) return 1.f;
-    int e;
-    const float m = frexpf(amax, &e);                 // amax = m 2^e, m in [1/2, 1); 448 = 0.875 * 2^9
-    e += m > 0.875f ? -8 : -9;
-    return ldexpf(1.f, max(e, -126));
+// Exponent bits of a block's scale, from the bits of its largest (bf16) magnitude: the least power of two s, 2^-126 or
+// more, with amax / s <= 448 = 1.75 * 2^8; 1 for a block of zeros.
+__device__ __forceinline__ uint32_t block_scale(uint32_t m) {
+    return m == 0 ? 127u : (uint32_t)max((int)(m >> 7) - 8 + ((m & 127u) > 96u ? 1 : 0), 1);
 }
 
 // One CTA: one block of tokens (blockIdx.x-th from the sequence's unfilled
@@ -202,7 +199,7 @@ __device__ __forceinline__ float block_scale(float amax) {
 // the new rows go to the ring.  Bound by HBM for prompts (each row is read once
 // and its 8-bit form written once), by latency for a round's few rows.
 template <int DT, int R>
-__global__ void __launch_bounds__(AP_BT) k_append(const Append P) {
+__global__ void __launch_bounds__(AP_BT, R <= 4 ? 3 : 2) k_append(const Append P) {
     // cosines, then sines [row of the block][pair]; the partial rotations that they are made of
     extern __shared__ __align__(16) float ct[];
     float* st = ct + P.page * (P.rot / 2);
@@ -276,19 +273,28 @@ __global__ void __launch_bounds__(AP_BT) k_append(const Append P) {
             // The angle of row r is the block's first plus 8 (r / 8) steps plus r mod 8: 1 + page / 8 + 8 sines and
             // cosines per pair and a product of three rotations for each row, instead of `page` of them.
             const int parts = 1 + (page >> 3) + 8;
-            for (int i = tid; i < parts * half; i += AP_BT) {
-                const int m = i / half, j = i - m * half;
+            for (int m = tid >> 5; m < parts; m += AP_BT / 32) {
                 const int steps = m == 0 ? start : m <= (page >> 3) ? 8 * (m - 1) : m - 1 - (page >> 3);
-                tr[i] = cos_sin(steps, P.inv_freq[j]);
+                for (int j = lane; j < half; j += 32) tr[m * half + j] = cos_sin(steps, P.inv_freq[j]);
             }
             __syncthreads();
-            for (int i = tid; i < page * half; i += AP_BT) {
-                const int r = i / half, j = i - r * half;
-                const float2 a = tr[j], u = tr[(1 + (r >> 3)) * half + j], v = tr[(1 + (page >> 3) + (r & 7)) * half + j];
-                const float2 w = make_float2(a.x * u.x - a.y * u.y, a.x * u.y + a.y * u.x);
-                ct[i] = w.x * v.x - w.y * v.y;
-                st[i] = w.x * v.y + w.y * v.x;
+            for (int r = tid >> 5; r < page; r += AP_BT / 32) {
+                const float2* u8 = tr + (1 + (r >> 3)) * half;
+                const float2* v8 = tr + (1 + (page >> 3) + (r & 7)) * half;
+                for (int j = lane; j < half; j += 32) {
+                    const float2 a = tr[j], u = u8[j], v = v8[j];
+                    const float2 w = make_float2(a.x * u.x - a.y * u.y, a.x * u.y + a.y * u.x);
+                    ct[r * half + j] = w.x * v.x - w.y * v.y;
+                    st[r * half + j] = w.x * v.y + w.y * v.x;
+                }
             }
+        }
+        // where the rows of the block come from: a row of k and v, the ring (-1), nowhere (-2)
+        int from[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int r = grp + i * groups, t = start + r;
+            from[i] = r >= page || t >= newlen ? -2 : t < len ? -1 : P.index ? P.index[(int64_t)b * P.W + (t - len)] : t - len;
         }
         __syncthreads();
         // one (head, keys or values) after the other, the next one's rows on their way
@@ -297,23 +303,22 @@ __global__ void __launch_bounds__(AP_BT) k_append(const Append P) {
         auto fetch = [&](int it) {
             const int which = it & 1, h = h0 + (it >> 1);
             const Quads at(l, which ? 0 : P.rot, P.interleaved);
-            const sv_host::Rows& src = which ? P.v : P.k;
-            const char* ring = static_cast<const char*>(which ? P.c.v_open : P.c.k_open) + ((int64_t)slot * P.Hkv + h) * 2 * page * D * 2;
+            const int64_t sn = which ? P.v.n : P.k.n;
+            const char* src = which ? P.v.p + b * P.v.b + h * P.v.h : P.k.p + b * P.k.b + h * P.k.h;
+            const int o0 = at.q0 * 4 * Vec8<DT>::ESZ, o1 = at.q1 * 4 * Vec8<DT>::ESZ;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const int r = grp + i * groups, t = start + r;
                 raw[i][0].zero();
                 raw[i][1].zero();
-                if (r >= page) continue;
-                if (t < len) {
-                    const char* p = ring + (int64_t)(t & (2 * page - 1)) * D * 2;
+                if (from[i] >= 0) {
+                    const char* p = src + from[i] * sn;
+                    raw[i][0].load(p + o0);
+                    raw[i][1].load(p + o1);
+                } else if (from[i] == -1) {
+                    const char* p = static_cast<const char*>(which ? P.c.v_open : P.c.k_open) +
+                                    (((int64_t)slot * P.Hkv + h) * 2 * page + ((start + grp + i * groups) & (2 * page - 1))) * D * 2;
                     raw[i][0].load_bf16(p + 8 * at.q0);
                     raw[i][1].load_bf16(p + 8 * at.q1);
-                } else if (t < newlen) {
-                    const int row = P.index ? P.index[(int64_t)b * P.W + (t - len)] : t - len;
-                    const char* p = src.p + b * src.b + row * src.n + h * src.h;
-                    raw[i][0].load(p + at.q0 * 4 * Vec8<DT>::ESZ);
-                    raw[i][1].load(p + at.q1 * 4 * Vec8<DT>::ESZ);
                 }
             }
         };
@@ -325,7 +330,7 @@ __global__ void __launch_bounds__(AP_BT) k_append(const Append P) {
             uint32_t m = 0;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const int r = grp + i * groups, t = start + r;
+                const int r = grp + i * groups;
                 float x[8];
                 raw[i][0].get(x);
                 raw[i][1].get(x + 4);
@@ -333,12 +338,12 @@ __global__ void __launch_bounds__(AP_BT) k_append(const Append P) {
                     if (P.kw) {
                         const float rs = row_rms(x, GW, inv_d, P.eps);
                         const float4 w0 = *reinterpret_cast<const float4*>(wt + 4 * at.q0), w1 = *reinterpret_cast<const float4*>(wt + 4 * at.q1);
-                        if (t >= len) {
+                        if (from[i] >= 0) {
                             x[0] = x[0] * rs * w0.x; x[1] = x[1] * rs * w0.y; x[2] = x[2] * rs * w0.z; x[3] = x[3] * rs * w0.w;
                             x[4] = x[4] * rs * w1.x; x[5] = x[5] * rs * w1.y; x[6] = x[6] * rs * w1.z; x[7] = x[7] * rs * w1.w;
                         }
                     }
-                    if (at.turns && r < page && t >= len)
+                    if (at.turns && from[i] >= 0)
                         row_rotate(x, *reinterpret_cast<const float4*>(ct + r * half + 4 * l),
                                    *reinterpret_cast<const float4*>(st + r * half + 4 * l), P.interleaved);
                 }
@@ -352,9 +357,8 @@ __global__ void __launch_bounds__(AP_BT) k_append(const Append P) {
                 char* ring = static_cast<char*>(which ? P.c.v_open : P.c.k_open) + ((int64_t)slot * P.Hkv + h) * 2 * page * D * 2;
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
-                    const int r = grp + i * groups, t = start + r;
-                    if (r < page && t >= len && t < newlen) {
-                        char* p = ring + (int64_t)(t & (2 * page - 1)) * D * 2;
+                    if (from[i] >= 0) {
+                        char* p = ring + (int64_t)((start + grp + i * groups) & (2 * page - 1)) * D * 2;
                         val[i][0].store(p + 8 * at.q0);
                         val[i][1].store(p + 8 * at.q1);
                     }
@@ -378,9 +382,10 @@ __global__ void __launch_bounds__(AP_BT) k_append(const Append P) {
             m = red[it & 1][0];
 #pragma unroll
             for (int w = 1; w < AP_BT / 32; ++w) m = max(m, red[it & 1][w]);
-            const float sc = block_scale(__uint_as_float(m << 16)), inv = 1.f / sc;      // exact: a power of two
+            const uint32_t sc = block_scale(m);
+            const float inv = __uint_as_float((254u - sc) << 23);
             const int64_t ph = (int64_t)page_id * P.Hkv + h;
-            if (tid == 0) (which ? P.c.v_scale : P.c.k_scale)[ph] = sc;
+            if (tid == 0) (which ? P.c.v_scale : P.c.k_scale)[ph] = __uint_as_float(sc << 23);
             char* dst = static_cast<char*>(which ? P.c.v_pages : P.c.k_pages) + ph * page * D;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
