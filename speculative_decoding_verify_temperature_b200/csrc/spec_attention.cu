@@ -19,6 +19,7 @@ constexpr float LN2 = 0.69314718055994530942f;
 struct Att {
     int B, N, Hq, Hkv, G, page, pshift, R;   // page = 1 << pshift; R = N * G rows of a kv head
     int mtiles;                           // items per (sequence, kv head)
+    int over;                             // what an item costs beside its tiles, in tiles
     sv_host::Rows q, k, v;
     spec_kv_cache c;
     const uint32_t* anc;                  // nullable: chains
@@ -30,10 +31,10 @@ struct Att {
     float* partial;                       // [gridDim.x][2][rows of an item][D + 2]
 };
 
-// An item whose tiles several CTAs share: they leave partial results, CTA c its
-// first tiles in slot `slot0` of its workspace and the CTAs after it theirs in slot 0.
+// An item whose tiles several CTAs share: they leave partial results, the CTA that
+// begins it in slot 1 of its workspace and those after it in slot 0 of theirs.
 struct Cut {
-    int b, h, mt, parts, slot0;           // parts = 0: none
+    int b, h, mt, parts;                  // parts = 0: none
 };
 
 // ----------------------------------------------------------------------------- the work and its split
@@ -61,18 +62,20 @@ __device__ __forceinline__ Seq seq_of(const Att& P, int b) {
     return s;
 }
 
-// The tiles of all items (sequence, kv head, rows), in that order, are one line;
-// every CTA takes an equal stretch of it, whatever the lengths are.  An item
-// that a stretch border cuts leaves partial results, which a second kernel puts together.
+// The items (sequence, kv head, rows), in that order, are one line: each takes
+// `over` units (its queries, its tail and its results) and one for each of its
+// tiles.  Every CTA takes an equal stretch of the line, whatever the lengths are.
+// An item whose tiles a stretch border cuts leaves partial results, which a second
+// kernel puts together.
 struct Stretch {
-    long long lo, hi, total;              // tiles
-    int ctas;                             // CTAs that share the line: each has at least one tile
-    int b;                                // sequence of tile lo
-    long long b_lo;                       // first tile of that sequence
+    long long lo, hi, total;              // units
+    int ctas;                             // CTAs that share the line: each has at least one unit
+    int b;                                // sequence of unit lo
+    long long b_lo;                       // first unit of that sequence
 };
 
 __device__ __forceinline__ long long stretch_at(long long total, int cta, int ctas) { return total * cta / ctas; }
-// CTA that holds tile x.
+// CTA that holds unit x.
 __device__ __forceinline__ int cta_of(long long x, long long total, int ctas) {
     int c = (int)(x * ctas / total);
     while (stretch_at(total, c + 1, ctas) <= x) ++c;
@@ -92,7 +95,7 @@ __device__ Stretch find_stretch(const Att& P) {
     Stretch s{};
     long long mine = 0, first = 0;
     for (int b = tid; b < P.B; b += BT) {
-        const long long n = (long long)seq_of(P, b).ntiles * items;
+        const long long n = (long long)(seq_of(P, b).ntiles + P.over) * items;
         if (b == tid) first = n;
         mine += n;
     }
@@ -109,7 +112,7 @@ __device__ Stretch find_stretch(const Att& P) {
     long long before = 0;
     for (int base = 0; base < P.B; base += BT) {
         const int b = base + tid;
-        const long long n = base == 0 ? first : b < P.B ? (long long)seq_of(P, b).ntiles * items : 0;
+        const long long n = base == 0 ? first : b < P.B ? (long long)(seq_of(P, b).ntiles + P.over) * items : 0;
         long long inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -138,12 +141,13 @@ __device__ Stretch find_stretch(const Att& P) {
     return s;
 }
 
-// A CTA's part of one item.
+// A CTA's part of one item: at least one of its tiles.
 struct Seg {
     Seq q;
     int b, h, mt;
     int t0, t1;                           // tiles of the item
-    long long item_lo;                    // the item's first tile on the line
+    long long item_lo;                    // the item's first unit on the line
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == q.ntiles; }
 };
 
 struct SegIter {
@@ -159,24 +163,34 @@ struct SegIter {
         if (at < s.hi) q = seq_of(P, b);
     }
     __device__ __forceinline__ bool next(const Att& P, Seg& g) {
-        if (at >= s.hi) return false;
         const int items = P.Hkv * P.mtiles;
-        while (at >= b_lo + (long long)q.ntiles * items) {
-            b_lo += (long long)q.ntiles * items;
-            q = seq_of(P, ++b);
+        while (at < s.hi) {
+            while (at >= b_lo + (long long)(q.ntiles + P.over) * items) {
+                b_lo += (long long)(q.ntiles + P.over) * items;
+                q = seq_of(P, ++b);
+            }
+            const int units = q.ntiles + P.over;
+            const int item = (int)((at - b_lo) / units);
+            g.q = q;
+            g.b = b;
+            g.h = item / P.mtiles;
+            g.mt = item - g.h * P.mtiles;
+            g.item_lo = b_lo + (long long)item * units;
+            g.t0 = max((int)(at - g.item_lo) - P.over, 0);
+            g.t1 = (int)min((long long)units, s.hi - g.item_lo) - P.over;
+            at = g.item_lo + P.over + max(g.t1, 0);
+            if (g.t1 > g.t0) return true;
+            if (at < s.hi) continue;
+            return false;                 // the stretch ends before the item's first tile
         }
-        const int item = (int)((at - b_lo) / q.ntiles);
-        g.q = q;
-        g.b = b;
-        g.h = item / P.mtiles;
-        g.mt = item % P.mtiles;
-        g.item_lo = b_lo + (long long)item * q.ntiles;
-        g.t0 = (int)(at - g.item_lo);
-        g.t1 = (int)min((long long)q.ntiles, s.hi - g.item_lo);
-        at = g.item_lo + g.t1;
-        return true;
+        return false;
     }
 };
+
+// CTAs that hold tiles of the item which this CTA begins and does not end.
+__device__ __forceinline__ int parts_of(const Att& P, const Seg& g, const Stretch& st, int cta) {
+    return cta_of(g.item_lo + P.over + g.q.ntiles - 1, st.total, st.ctas) - cta + 1;
+}
 
 // 32 bits of the mask of node n over the tail's keys [e0, e0 + 32): the open
 // tokens are seen by every node, node m by the rows whose mask holds it.
@@ -206,10 +220,10 @@ __device__ __forceinline__ uint32_t tail_bits(const Att& P, int b, int n, int op
 
 // ----------------------------------------------------------------------------- tensor-core kernel (tcgen05)
 
-// Roles of the CTA's warps: 0-3 and 4-7 the softmax of one stream each, 8-15 make
-// operands (f16 values from e4m3 bytes, queries, the tail), 16 issues the matrix
-// instructions (one thread), 17 copies pages to shared memory, 18 gathers the
-// pages' scales, 19 nothing.
+// Roles of the CTA's warps: 0-3 and 4-7 the softmax of one stream each, 8-11 make
+// operands (f16 values from e4m3 bytes, queries, the tail), 12 issues the matrix
+// instructions (one thread), 13 copies pages to shared memory, 14 gathers the
+// pages' scales, 15 nothing.
 //
 // An item holds up to 256 rows.  With more than 128 the two streams are its two
 // halves and both take every tile; with 128 or fewer both streams hold the same
@@ -236,8 +250,8 @@ __device__ __forceinline__ uint32_t tail_bits(const Att& P, int b, int n, int op
 // leading P whatever the blocks' scales are.  O is rescaled only when M grows by
 // more than 2^4; P_BIAS lifts P to at most 2^15, so that f16's smallest step is
 // 2^-35 of the leading one.
-constexpr int TC_SOFTMAX = 256, TC_CONV = 256, TC_BT = 640;
-constexpr int TC_W_CONV = 8, TC_W_MMA = 16, TC_W_COPY = 17, TC_W_SCALE = 18;
+constexpr int TC_SOFTMAX = 256, TC_CONV = 128, TC_BT = 512;
+constexpr int TC_W_CONV = 8, TC_W_MMA = 12, TC_W_COPY = 13, TC_W_SCALE = 14;
 constexpr int TC_META = 4;                // tiles whose scales are kept
 constexpr float P_BIAS = 11.f, M_SLACK = 4.f;
 
@@ -388,7 +402,15 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
                  :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
 }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The registers are operands, so that nothing that uses them comes before the wait.
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :: "memory");
+}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t (&r)[32]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -826,7 +848,62 @@ __device__ __forceinline__ void tile_mask(const Att& P, const Seg& g, int t, int
     }
 }
 
-// MODE 0: cached tile, all keys; 1: cached tile, masked; 2: tail (masked, scales per key).
+// MODE 1: cached tile, masked; 2: tail (masked, scales per key).
+// The usual case (a cached tile, all keys): scores come from tensor memory 32 columns ahead of their use.
+__device__ __forceinline__ float group_max(const uint32_t (&r)[32], int u) {
+    float a = __uint_as_float(r[16 * u]), b = __uint_as_float(r[16 * u + 1]);
+#pragma unroll
+    for (int j = 2; j < 14; j += 4) {
+        a = max3(a, __uint_as_float(r[16 * u + j]), __uint_as_float(r[16 * u + j + 1]));
+        b = max3(b, __uint_as_float(r[16 * u + j + 2]), __uint_as_float(r[16 * u + j + 3]));
+    }
+    a = max3(a, __uint_as_float(r[16 * u + 14]), __uint_as_float(r[16 * u + 15]));
+    return fmaxf(a, b);
+}
+__device__ __forceinline__ float group_probs(const uint32_t (&r)[32], int u, float a, float b, uint32_t (&p)[16]) {
+    float2 gs = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+        float2 x = fma2(make_float2(__uint_as_float(r[16 * u + j]), __uint_as_float(r[16 * u + j + 1])), make_float2(a, a),
+                        make_float2(b, b));
+        x.x = ex2(x.x);
+        x.y = ex2(x.y);
+        gs = add2(gs, x);
+        p[8 * u + j / 2] = pack_f16(x.x, x.y);
+    }
+    return gs.x + gs.y;
+}
+__device__ __forceinline__ float full_max(uint32_t s_col, const float* meta, float rq) {
+    uint32_t r[2][32];
+    float mx = NEG_INF;
+    tc_ld32(s_col, r[0]);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        tc_wait_ld(r[c & 1]);
+        if (c < 3) tc_ld32(s_col + 32 * (c + 1), r[(c + 1) & 1]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            mx = fmaxf(mx, fmaf(group_max(r[c & 1], u), fmaxf(meta[2 * c + u] * rq, 1.2e-38f), meta[TILE + 2 * c + u]));
+    }
+    return mx;
+}
+__device__ __forceinline__ float full_probs(uint32_t s_col, const float* meta, float rq, float sub) {
+    uint32_t r[2][32];
+    float l = 0.f;
+    tc_ld32(s_col, r[0]);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        tc_wait_ld(r[c & 1]);
+        if (c < 3) tc_ld32(s_col + 32 * (c + 1), r[(c + 1) & 1]);
+        uint32_t p[16];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            l = fmaf(group_probs(r[c & 1], u, fmaxf(meta[2 * c + u] * rq, 1.2e-38f), meta[TILE + 2 * c + u] + sub, p),
+                     meta[2 * TILE + 2 * c + u], l);
+        tc_st16(s_col + 16 * c, p);      // columns that have been read
+    }
+    return l;
+}
 // The largest w of the row's keys.
 template <int MODE>
 __device__ __forceinline__ float tile_max(uint32_t s_col, const float* meta, float rq, const uint32_t (&mk)[4]) {
@@ -835,25 +912,15 @@ __device__ __forceinline__ float tile_max(uint32_t s_col, const float* meta, flo
     for (int c = 0; c < 4; ++c) {
         uint32_t r[32];
         tc_ld32(s_col + 32 * c, r);
-        tc_wait_ld();
-        if (MODE > 0) {
-            const uint32_t bits = mk[c];
+        tc_wait_ld(r);
+        const uint32_t bits = mk[c];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (!((bits >> j) & 1)) r[j] = 0xff800000u;
-        }
-        if (MODE < 2) {
+        for (int j = 0; j < 32; ++j)
+            if (!((bits >> j) & 1)) r[j] = 0xff800000u;
+        if (MODE == 1) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float a = __uint_as_float(r[16 * u]), b = __uint_as_float(r[16 * u + 1]);
-#pragma unroll
-                for (int j = 2; j < 14; j += 4) {
-                    a = max3(a, __uint_as_float(r[16 * u + j]), __uint_as_float(r[16 * u + j + 1]));
-                    b = max3(b, __uint_as_float(r[16 * u + j + 2]), __uint_as_float(r[16 * u + j + 3]));
-                }
-                a = max3(a, __uint_as_float(r[16 * u + 14]), __uint_as_float(r[16 * u + 15]));
-                mx = fmaxf(mx, fmaf(fmaxf(a, b), fmaxf(meta[2 * c + u] * rq, 1.2e-38f), meta[TILE + 2 * c + u]));
-            }
+            for (int u = 0; u < 2; ++u)
+                mx = fmaxf(mx, fmaf(group_max(r, u), fmaxf(meta[2 * c + u] * rq, 1.2e-38f), meta[TILE + 2 * c + u]));
         } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -870,29 +937,16 @@ __device__ __forceinline__ float tile_probs(uint32_t s_col, const float* meta, f
     for (int c = 0; c < 4; ++c) {
         uint32_t r[32], p[16];
         tc_ld32(s_col + 32 * c, r);
-        tc_wait_ld();
-        if (MODE > 0) {
-            const uint32_t bits = mk[c];
+        tc_wait_ld(r);
+        const uint32_t bits = mk[c];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (!((bits >> j) & 1)) r[j] = 0xff800000u;
-        }
-        if (MODE < 2) {
+        for (int j = 0; j < 32; ++j)
+            if (!((bits >> j) & 1)) r[j] = 0xff800000u;
+        if (MODE == 1) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const float a = fmaxf(meta[2 * c + u] * rq, 1.2e-38f), b = meta[TILE + 2 * c + u] + sub;
-                float2 gs = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                    float2 x = fma2(make_float2(__uint_as_float(r[16 * u + j]), __uint_as_float(r[16 * u + j + 1])),
-                                    make_float2(a, a), make_float2(b, b));
-                    x.x = ex2(x.x);
-                    x.y = ex2(x.y);
-                    gs = add2(gs, x);
-                    p[8 * u + j / 2] = pack_f16(x.x, x.y);
-                }
-                l = fmaf(gs.x + gs.y, meta[2 * TILE + 2 * c + u], l);
-            }
+            for (int u = 0; u < 2; ++u)
+                l = fmaf(group_probs(r, u, fmaxf(meta[2 * c + u] * rq, 1.2e-38f), meta[TILE + 2 * c + u] + sub, p),
+                         meta[2 * TILE + 2 * c + u], l);
         } else {
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
@@ -910,9 +964,11 @@ __device__ __forceinline__ float tile_probs(uint32_t s_col, const float* meta, f
 }
 
 // What a CTA leaves of an item that it does not hold whole.
+// A partial result: the output rows, then the rows' maxima and sums; a multiple of 16 bytes.
+__host__ __device__ constexpr size_t partial_floats(size_t rows, int D) { return (rows * (D + 2) + 3) / 4 * 4; }
 template <int D>
 __device__ __forceinline__ float* partial_of(const Att& P, int cta, int slot) {
-    return P.partial + ((int64_t)cta * 2 + slot) * (min(P.R, 256) * (int64_t)(D + 2));
+    return P.partial + ((int64_t)cta * 2 + slot) * partial_floats(min(P.R, 256), D);
 }
 
 __device__ __forceinline__ int rows_of(const Att& P) { return min(P.R, 256); }
@@ -1077,7 +1133,7 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
                 uint32_t mk[4] = {};
                 float mx;
                 if (mode == 0) {
-                    mx = tile_max<0>(s_col, meta, rq, mk);
+                    mx = full_max(s_col, meta, rq);
                 } else {
                     tile_mask(P, g, t, n, mk);
                     mx = mode == 1 ? tile_max<1>(s_col, meta, rq, mk) : tile_max<2>(s_col, meta, rq, mk);
@@ -1094,14 +1150,14 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
                     for (int c = 0; c < D; c += 32) {
                         uint32_t o[32];
                         tc_ld32(o_col + i * D + c, o);
-                        tc_wait_ld();
+                        tc_wait_ld(o);
 #pragma unroll
                         for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
                         tc_st32(o_col + i * D + c, o);
                     }
                 }
                 const float sub = P_BIAS - (m == NEG_INF ? 0.f : m);
-                l += mode == 0 ? tile_probs<0>(s_col, meta, rq, mk, sub)
+                l += mode == 0 ? full_probs(s_col, meta, rq, sub)
                      : mode == 1 ? tile_probs<1>(s_col, meta, rq, mk, sub) : tile_probs<2>(s_col, meta, rq, mk, sub);
                 tc_wait_st();
                 tc_before();
@@ -1128,7 +1184,7 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
                 c_lo = i * (D / 2);
                 c_hi = c_lo + D / 2;
             }
-            const bool whole = g.t0 == 0 && g.t1 == g.q.ntiles;
+            const bool whole = g.whole();
             const bool nan = g.q.bad || *reinterpret_cast<volatile int*>(&sh.bad_seg[seg & 7]) == seg + 1;
             if (nan && r == 0) atomicOr(P.status, 1u << SPEC_ERR_DEVICE_INPUT);
             uint32_t bad_v = 0;
@@ -1138,19 +1194,18 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
             }
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const int64_t orow = ((int64_t)g.b * P.N + n) * P.Hq + head;
-            const int slot = g.item_lo + g.t0 == st.lo ? 0 : 1;
-            float* part = partial_of<D>(P, blockIdx.x, slot);
+            float* part = partial_of<D>(P, blockIdx.x, g.t0 == 0 ? 1 : 0);
             const float quiet = __int_as_float(0x7fffffff);
 #pragma unroll 1
             for (int c = c_lo; c < (idle ? c_lo : c_hi); c += 32) {
                 uint32_t o[32];
                 tc_ld32(o_col + (dual ? i * D : 0) + c, o);
-                tc_wait_ld();
+                tc_wait_ld(o);
                 if (!dual) {
                     if (nt > 1) {
                         uint32_t o2[32];
                         tc_ld32(o_col + D + c, o2);
-                        tc_wait_ld();
+                        tc_wait_ld(o2);
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             o[j] = __float_as_uint(__uint_as_float(o[j]) * f[0] + __uint_as_float(o2[j]) * f[1]);
@@ -1204,10 +1259,7 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
                     part[(int64_t)rows_of(P) * D + ri] = m == NEG_INF ? NEG_INF : m - P_BIAS;
                     part[(int64_t)rows_of(P) * D + rows_of(P) + ri] = nan ? quiet : l;
                 }
-                if (g.t0 == 0 && tid == 0) {
-                    const int c1 = cta_of(g.item_lo + g.q.ntiles - 1, st.total, st.ctas);
-                    P.cut[blockIdx.x] = Cut{g.b, g.h, g.mt, c1 - (int)blockIdx.x + 1, slot};
-                }
+                if (g.t0 == 0 && tid == 0) P.cut[blockIdx.x] = Cut{g.b, g.h, g.mt, parts_of(P, g, st, blockIdx.x)};
             }
             // the next segment's products may write O again once every reader is through
             tc_before();
@@ -1236,7 +1288,7 @@ __global__ void __launch_bounds__(MERGE_BT) k_attention_merge(const Att P) {
     if (cut.parts == 0) return;
     constexpr int E = D / 32;
     for (int r = blockIdx.y * MERGE_ROWS + (threadIdx.x >> 5); r < upto; r += MERGE_BT / 32) {
-        auto part = [&](int i) { return partial_of<D>(P, blockIdx.x + i, i == 0 ? cut.slot0 : 0); };
+        auto part = [&](int i) { return partial_of<D>(P, blockIdx.x + i, i == 0 ? 1 : 0); };
         float M = NEG_INF, m0 = NEG_INF, l0 = 0.f;
         for (int i = lane; i < cut.parts; i += 32) {
             const float* p = part(i) + (int64_t)rows * D;
@@ -1655,7 +1707,6 @@ template <int D>
 __device__ __forceinline__ void mm_finish(const Att& P, MmWarp<D>& w, MmShared<D>& sh, bool bad) {
     const int tid = threadIdx.x;
     const Seg& g = sh.now.s;
-    const Stretch& st = sh.now.it.s;
     constexpr int NT = D / 8;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -1695,12 +1746,11 @@ __device__ __forceinline__ void mm_finish(const Att& P, MmWarp<D>& w, MmShared<D
         }
     }
     __syncthreads();
-    const bool whole = g.t0 == 0 && g.t1 == g.q.ntiles;
+    const bool whole = g.whole();
     const bool nan = g.q.bad || sh.bad;
     const float quiet = __int_as_float(0x7fffffff);
-    const int slot = g.item_lo + g.t0 == st.lo ? 0 : 1;
     if (w.warp == 0) {
-        float* part = partial_of<D>(P, blockIdx.x, slot);
+        float* part = partial_of<D>(P, blockIdx.x, g.t0 == 0 ? 1 : 0);
         uint32_t any_bad = 0;
         if (g.t1 > g.q.nct)
             for (int i = 0; i < 12; ++i) any_bad |= sh.bad_v[i];
@@ -1764,10 +1814,7 @@ __device__ __forceinline__ void mm_finish(const Att& P, MmWarp<D>& w, MmShared<D
     }
     if (tid == 0) {
         if (nan) atomicOr(P.status, 1u << SPEC_ERR_DEVICE_INPUT);
-        if (!whole && g.t0 == 0) {
-            const int c1 = cta_of(g.item_lo + g.q.ntiles - 1, st.total, st.ctas);
-            P.cut[blockIdx.x] = Cut{g.b, g.h, g.mt, c1 - (int)blockIdx.x + 1, slot};
-        }
+        if (!whole && g.t0 == 0) P.cut[blockIdx.x] = Cut{g.b, g.h, g.mt, parts_of(P, g, sh.now.it.s, blockIdx.x)};
     }
     __syncthreads();
     if (tid < 12) sh.bad_v[tid] = 0;
@@ -1855,6 +1902,13 @@ using sv_host::fail;
 
 namespace {
 
+#ifndef TC_OVER_N
+#define TC_OVER_N 4
+#endif
+#ifndef MM_OVER_N
+#define MM_OVER_N 2
+#endif
+constexpr int TC_OVER = TC_OVER_N, MM_OVER = MM_OVER_N;
 constexpr int TC_CTAS = 148, MM_CTAS = MM_CTAS_SM * 148;      // CTAs at most
 
 template <int D>
@@ -1900,8 +1954,9 @@ spec_status page_map(const Att& P, void* pages, int rows, CUtensorMap* map) {
 }
 
 template <int D>
-spec_status launch_tc(const Att& P, cudaStream_t st) {
+spec_status launch_tc(Att P, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
+    P.over = TC_OVER;
     if (const spec_status s = sv_host::allow_smem(reinterpret_cast<const void*>(k_attention_tc<D>), "k_attention_tc", tc_smem<D>(), done)) return s;
     const int ctas = sv_host::num_sms() < TC_CTAS ? sv_host::num_sms() : TC_CTAS;
     CUtensorMap kmap;
@@ -1912,9 +1967,10 @@ spec_status launch_tc(const Att& P, cudaStream_t st) {
 }
 
 template <int D>
-spec_status launch_mma(const Att& P, cudaStream_t st) {
+spec_status launch_mma(Att P, cudaStream_t st) {
     const size_t smem = sizeof(MmShared<D>) + 1024;
     static std::atomic<uint64_t> done{0};
+    P.over = MM_OVER;
     if (const spec_status s = sv_host::allow_smem(reinterpret_cast<const void*>(k_attention_mma<D>), "k_attention_mma", smem, done)) return s;
     CUtensorMap kmap, vmap;
     if (const spec_status s = page_map<D>(P, P.c.k_pages, 16, &kmap)) return s;
@@ -1935,8 +1991,8 @@ size_t spec_cache_workspace_bytes(int B, int N, int q_heads, int head_dim) {
         return 0;
     // rows of an item: at most N * q_heads (one kv head), 16 of them in the kernel with more CTAs
     const size_t rows = (size_t)N * q_heads < 256 ? (size_t)N * q_heads : 256, few = rows < MM_ROWS ? rows : MM_ROWS;
-    const size_t parts = TC_CTAS * rows > MM_CTAS * few ? TC_CTAS * rows : MM_CTAS * few;
-    return sv_host::CACHE_WS_PARTIAL + sv_host::align256(sizeof(float) * 2 * parts * (head_dim + 2));
+    const size_t tc = 2 * TC_CTAS * partial_floats(rows, head_dim), mm = 2 * MM_CTAS * partial_floats(few, head_dim);
+    return sv_host::CACHE_WS_PARTIAL + sv_host::align256(sizeof(float) * (tc > mm ? tc : mm));
 }
 
 spec_status spec_tree_attention(int B, int N, int q_heads, const spec_kv_cache* cache,

@@ -384,6 +384,7 @@ ATT = [  # B, N, Hq, Hkv, D, page, lengths
     (40, 6, 64, 8, 128, 16, [(i * 397) % 1501 for i in range(40)]),      # many tiles and items per CTA
     (24, 33, 64, 8, 128, 32, [(i * 211) % 900 for i in range(24)]), (20, 32, 32, 8, 64, 128, [(i * 533) % 2000 for i in range(20)]),
     (48, 2, 40, 8, 64, 64, [(i * 97) % 700 - 20 for i in range(48)]), (60, 1, 32, 8, 128, 16, [(i * 397) % 3001 for i in range(60)]),
+    (70, 1, 7, 1, 128, 16, [(i * 397) % 3001 for i in range(70)]), (30, 7, 15, 5, 64, 32, [(i * 211) % 900 for i in range(30)]),
     (9, 5, 12, 4, 128, 16, [5, 4000, 17, 1, 90, 2222, 0, 64, 800])]
 
 
