@@ -220,10 +220,10 @@ __device__ __forceinline__ uint32_t tail_bits(const Att& P, int b, int n, int op
 
 // ----------------------------------------------------------------------------- tensor-core kernel (tcgen05)
 
-// Roles of the CTA's warps: 0-3 and 4-7 the softmax of one stream each, 8-11 make
-// operands (f16 values from e4m3 bytes, queries, the tail), 12 issues the matrix
-// instructions (one thread), 13 copies pages to shared memory, 14 gathers the
-// pages' scales, 15 nothing.
+// Roles of the CTA's warps: 0-3 and 4-7 the softmax of one stream each, 8-15 make
+// operands (f16 values from e4m3 bytes, queries, the tail), 16 issues the matrix
+// instructions (one thread), 17 copies pages to shared memory, 18 gathers the
+// pages' scales, 19 nothing.
 //
 // An item holds up to 256 rows.  With more than 128 the two streams are its two
 // halves and both take every tile; with 128 or fewer both streams hold the same
@@ -250,8 +250,8 @@ __device__ __forceinline__ uint32_t tail_bits(const Att& P, int b, int n, int op
 // leading P whatever the blocks' scales are.  O is rescaled only when M grows by
 // more than 2^4; P_BIAS lifts P to at most 2^15, so that f16's smallest step is
 // 2^-35 of the leading one.
-constexpr int TC_SOFTMAX = 256, TC_CONV = 128, TC_BT = 512;
-constexpr int TC_W_CONV = 8, TC_W_MMA = 12, TC_W_COPY = 13, TC_W_SCALE = 14;
+constexpr int TC_SOFTMAX = 256, TC_CONV = 256, TC_BT = 640;
+constexpr int TC_W_CONV = 8, TC_W_MMA = 16, TC_W_COPY = 17, TC_W_SCALE = 18;
 constexpr int TC_META = 4;                // tiles whose scales are kept
 constexpr float P_BIAS = 11.f, M_SLACK = 4.f;
 
@@ -848,8 +848,9 @@ __device__ __forceinline__ void tile_mask(const Att& P, const Seg& g, int t, int
     }
 }
 
-// MODE 1: cached tile, masked; 2: tail (masked, scales per key).
-// The usual case (a cached tile, all keys): scores come from tensor memory 32 columns ahead of their use.
+// MODE 0: cached tile, all keys; 1: cached tile, masked; 2: tail (masked, scales per key).
+// The column loops stay rolled: unrolled (and with the scores of 32 columns loaded ahead) the code no longer fits the
+// instruction caches beside that of the other roles, and a round of 64-node trees took 800 us instead of 630.
 __device__ __forceinline__ float group_max(const uint32_t (&r)[32], int u) {
     float a = __uint_as_float(r[16 * u]), b = __uint_as_float(r[16 * u + 1]);
 #pragma unroll
@@ -873,37 +874,6 @@ __device__ __forceinline__ float group_probs(const uint32_t (&r)[32], int u, flo
     }
     return gs.x + gs.y;
 }
-__device__ __forceinline__ float full_max(uint32_t s_col, const float* meta, float rq) {
-    uint32_t r[2][32];
-    float mx = NEG_INF;
-    tc_ld32(s_col, r[0]);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        tc_wait_ld(r[c & 1]);
-        if (c < 3) tc_ld32(s_col + 32 * (c + 1), r[(c + 1) & 1]);
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-            mx = fmaxf(mx, fmaf(group_max(r[c & 1], u), fmaxf(meta[2 * c + u] * rq, 1.2e-38f), meta[TILE + 2 * c + u]));
-    }
-    return mx;
-}
-__device__ __forceinline__ float full_probs(uint32_t s_col, const float* meta, float rq, float sub) {
-    uint32_t r[2][32];
-    float l = 0.f;
-    tc_ld32(s_col, r[0]);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        tc_wait_ld(r[c & 1]);
-        if (c < 3) tc_ld32(s_col + 32 * (c + 1), r[(c + 1) & 1]);
-        uint32_t p[16];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-            l = fmaf(group_probs(r[c & 1], u, fmaxf(meta[2 * c + u] * rq, 1.2e-38f), meta[TILE + 2 * c + u] + sub, p),
-                     meta[2 * TILE + 2 * c + u], l);
-        tc_st16(s_col + 16 * c, p);      // columns that have been read
-    }
-    return l;
-}
 // The largest w of the row's keys.
 template <int MODE>
 __device__ __forceinline__ float tile_max(uint32_t s_col, const float* meta, float rq, const uint32_t (&mk)[4]) {
@@ -913,11 +883,13 @@ __device__ __forceinline__ float tile_max(uint32_t s_col, const float* meta, flo
         uint32_t r[32];
         tc_ld32(s_col + 32 * c, r);
         tc_wait_ld(r);
-        const uint32_t bits = mk[c];
+        if (MODE > 0) {
+            const uint32_t bits = mk[c];
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (!((bits >> j) & 1)) r[j] = 0xff800000u;
-        if (MODE == 1) {
+            for (int j = 0; j < 32; ++j)
+                if (!((bits >> j) & 1)) r[j] = 0xff800000u;
+        }
+        if (MODE < 2) {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
                 mx = fmaxf(mx, fmaf(group_max(r, u), fmaxf(meta[2 * c + u] * rq, 1.2e-38f), meta[TILE + 2 * c + u]));
@@ -938,11 +910,13 @@ __device__ __forceinline__ float tile_probs(uint32_t s_col, const float* meta, f
         uint32_t r[32], p[16];
         tc_ld32(s_col + 32 * c, r);
         tc_wait_ld(r);
-        const uint32_t bits = mk[c];
+        if (MODE > 0) {
+            const uint32_t bits = mk[c];
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (!((bits >> j) & 1)) r[j] = 0xff800000u;
-        if (MODE == 1) {
+            for (int j = 0; j < 32; ++j)
+                if (!((bits >> j) & 1)) r[j] = 0xff800000u;
+        }
+        if (MODE < 2) {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
                 l = fmaf(group_probs(r, u, fmaxf(meta[2 * c + u] * rq, 1.2e-38f), meta[TILE + 2 * c + u] + sub, p),
@@ -1133,7 +1107,7 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
                 uint32_t mk[4] = {};
                 float mx;
                 if (mode == 0) {
-                    mx = full_max(s_col, meta, rq);
+                    mx = tile_max<0>(s_col, meta, rq, mk);
                 } else {
                     tile_mask(P, g, t, n, mk);
                     mx = mode == 1 ? tile_max<1>(s_col, meta, rq, mk) : tile_max<2>(s_col, meta, rq, mk);
@@ -1157,7 +1131,7 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
                     }
                 }
                 const float sub = P_BIAS - (m == NEG_INF ? 0.f : m);
-                l += mode == 0 ? full_probs(s_col, meta, rq, sub)
+                l += mode == 0 ? tile_probs<0>(s_col, meta, rq, mk, sub)
                      : mode == 1 ? tile_probs<1>(s_col, meta, rq, mk, sub) : tile_probs<2>(s_col, meta, rq, mk, sub);
                 tc_wait_st();
                 tc_before();
