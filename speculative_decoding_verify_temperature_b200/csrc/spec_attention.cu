@@ -222,7 +222,7 @@ __device__ __forceinline__ uint32_t tail_bits(const Att& P, int b, int n, int op
 
 // Roles of the CTA's warps: 0-3 and 4-7 the softmax of one stream each, 8-15 make
 // operands (f16 values from e4m3 bytes, queries, the tail), 16 issues the matrix
-// instructions (one thread), 17 copies pages to shared memory, 18 gathers the
+// instructions, 17 copies pages to shared memory, 18 gathers the
 // pages' scales, 19 nothing.
 //
 // An item holds up to 256 rows.  With more than 128 the two streams are its two
@@ -389,18 +389,28 @@ __device__ __forceinline__ void bar_wait(uint64_t* b, uint32_t parity, TcShared&
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void tc_commit(uint64_t* b) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(smem_u32(b)) : "memory");
+// The warp that issues matrix instructions stays together and one elected lane issues: what all lanes compute alike
+// stays in uniform registers, where these instructions take their operands from.  (From one lane's branch each operand
+// was moved there first: 170 cycles an instruction.)
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
 }
-__device__ __forceinline__ void tc_mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
+__device__ __forceinline__ void tc_commit(uint64_t* b, uint32_t lead) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+                 :: "r"(smem_u32(b)), "r"(lead) : "memory");
 }
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
+__device__ __forceinline__ void tc_mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc, uint32_t lead) {
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"(lead) : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc, uint32_t lead) {
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"(lead) : "memory");
 }
 // The registers are operands, so that nothing that uses them comes before the wait.
 __device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[32]) {
@@ -952,7 +962,7 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
     extern __shared__ unsigned char raw_smem[];
     const uint32_t base = (smem_u32(raw_smem) + 1023u) & ~1023u;
     TcShared& sh = *reinterpret_cast<TcShared*>(raw_smem + (base - smem_u32(raw_smem)) + Tc<D>::END);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(FULL, tid >> 5, 0), lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Stretch st = find_stretch<TC_BT>(P);
     if (tid == 0) P.cut[blockIdx.x].parts = 0;
@@ -990,7 +1000,7 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
     }
     __syncthreads();
     tc_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh.tmem);
+    const uint32_t tmem = __shfl_sync(FULL, *reinterpret_cast<volatile uint32_t*>(&sh.tmem), 0);
 
     if (warp >= TC_W_CONV && warp < TC_W_MMA) {
         TcConv<D>(P, sh, base, tid - TC_SOFTMAX).run(st);
@@ -1000,74 +1010,76 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
         tc_scales<D>(P, sh, st, lane);
     } else if (warp == TC_W_MMA) {
         // ---- matrix instructions
-        if (lane == 0) {
-            SegIter it;
-            Seg g;
-            it.begin(P, st);
-            uint32_t cnt[2] = {0, 0};
-            int g0 = 0, nk0 = 0;
-            constexpr uint32_t ID_QK = tc_idesc(TILE, false), ID_PV = tc_idesc(D, true);
-            constexpr int KR = Tc<D>::KR;
-            for (int seg = 0; it.next(P, g); ++seg) {
-                const bool dual = is_dual(P, g.mt);
-                const int nt = g.t1 - g.t0, nc = max(0, min(nt, g.q.nct - g.t0));    // tiles, cached ones
-                int left = dual ? 2 * nt : nt;            // score products still to issue
-                bar_wait(&sh.qf, seg & 1, sh);
-                tc_after();
-                // Products of the two kinds are not ordered among themselves: a stream's probabilities have to be through
-                // before its next scores are written over them.
-                auto scores = [&](int i, int tl) {
-                    if (cnt[i]) bar_wait(&sh.pv[i], (cnt[i] - 1) & 1, sh);
-                    const uint32_t q = base + Tc<D>::Q + (dual ? i : 0) * Tc<D>::Q_B;
-                    const int parts = tl < nc ? 1 : 2, nk = nk0 + tl + max(0, tl - nc);
-                    for (int part = 0; part < parts; ++part) {
-                        const int s = (nk + part) % KR;
-                        bar_wait(&sh.kf[s], ((nk + part) / KR) & 1, sh);
-                        tc_after();
-                        const uint32_t k = base + Tc<D>::K + s * Tc<D>::RAW_B;
+        const uint32_t lead = elect_one();
+        SegIter it;
+        Seg g;
+        it.begin(P, st);
+        uint32_t cnt[2] = {0, 0};
+        int g0 = 0, nk0 = 0;
+        constexpr uint32_t ID_QK = tc_idesc(TILE, false), ID_PV = tc_idesc(D, true);
+        constexpr int KR = Tc<D>::KR;
+        const uint64_t qd = tc_desc<128>(base + Tc<D>::Q, 16), kd = tc_desc<D>(base + Tc<D>::K, 16);
+        const uint64_t vd = tc_desc<128>(base + Tc<D>::V, Tc<D>::HALF);
+        for (int seg = 0; it.next(P, g); ++seg) {
+            const bool dual = is_dual(P, g.mt);
+            const int nt = g.t1 - g.t0, nc = max(0, min(nt, g.q.nct - g.t0));        // tiles, cached ones
+            int left = dual ? 2 * nt : nt;                // score products still to issue
+            bar_wait(&sh.qf, seg & 1, sh);
+            tc_after();
+            // Products of the two kinds are not ordered among themselves: a stream's probabilities have to be through
+            // before its next scores are written over them.
+            auto scores = [&](int i, int tl) {
+                const uint32_t done = i ? cnt[1] : cnt[0];
+                if (done) bar_wait(&sh.pv[i], (done - 1) & 1, sh);
+                const uint64_t q = qd + (dual && i ? Tc<D>::Q_B >> 4 : 0);
+                const int parts = tl < nc ? 1 : 2, nk = nk0 + tl + max(0, tl - nc);
+                for (int part = 0; part < parts; ++part) {
+                    const int s = (nk + part) % KR;
+                    bar_wait(&sh.kf[s], ((nk + part) / KR) & 1, sh);
+                    tc_after();
+                    const uint64_t k = kd + s * (Tc<D>::RAW_B >> 4);
 #pragma unroll
-                        for (int u = 0; u < 2 * D / 32; ++u) {     // q's first rows, then its second
-                            const uint32_t off = D == 128 ? (u / 4) * Tc<D>::RAW_B + (u % 4) * 32 : u * 32;
-                            tc_mma_e4m3(tmem + i * TILE, tc_desc<128>(q + off, 16), tc_desc<D>(k + (u % (D / 32)) * 32, 16),
-                                        ID_QK, part > 0 || u > 0);
-                        }
-                        if (!dual || i == 1) tc_commit(&sh.ke[s]);
+                    for (int u = 0; u < 2 * D / 32; ++u) {         // q's first rows, then its second
+                        const uint32_t off = D == 128 ? (u / 4) * Tc<D>::RAW_B + (u % 4) * 32 : u * 32;
+                        tc_mma_e4m3(tmem + i * TILE, q + (off >> 4), k + (u % (D / 32)) * 2, ID_QK, part > 0 || u > 0, lead);
                     }
-                    tc_commit(&sh.sf[i]);
-                    if (--left == 0) tc_commit(&sh.qe);
-                };
-                auto tile = [&](int i, int step) { return dual ? step : 2 * step + i; };
-                for (int i = 0; i < 2; ++i)
-                    if (tile(i, 0) < nt) scores(i, tile(i, 0));
-                for (int step = 0; tile(0, step) < nt; ++step) {
-                    for (int i = 0; i < 2; ++i) {
-                        const int tl = tile(i, step);
-                        if (tl >= nt) continue;
-                        const int gt = g0 + tl, s = gt & 1;
-                        bar_wait(&sh.vf[s], (gt >> 1) & 1, sh);
-                        bar_wait(&sh.pf[i], cnt[i] & 1, sh);
-                        tc_after();
-                        const uint32_t v = base + Tc<D>::V + s * Tc<D>::V_B;
-#pragma unroll
-                        for (int u = 0; u < TILE / 16; ++u)
-                            tc_mma_ts(tmem + Tc<D>::O_COL + i * D, tmem + i * TILE + u * 8, tc_desc<128>(v + u * 2048, Tc<D>::HALF),
-                                      ID_PV, step > 0 || u > 0);
-                        ++cnt[i];
-                        if (!dual || i == 1) {
-                            tc_commit(&sh.ve[s]);
-                            tc_commit(&sh.me[gt & (TC_META - 1)]);
-                        }
-                        tc_commit(&sh.pv[i]);
-                        if (tile(i, step + 1) < nt) scores(i, tile(i, step + 1));
-                    }
+                    if (!dual || i == 1) tc_commit(&sh.ke[s], lead);
                 }
-                g0 += nt;
-                nk0 += nt + (nt - nc);
+                tc_commit(&sh.sf[i], lead);
+                if (--left == 0) tc_commit(&sh.qe, lead);
+            };
+            auto tile = [&](int i, int step) { return dual ? step : 2 * step + i; };
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i)
+                if (tile(i, 0) < nt) scores(i, tile(i, 0));
+#pragma unroll 1
+            for (int n = 0; tile(0, n >> 1) < nt; ++n) {  // step n / 2 of stream n mod 2
+                const int i = n & 1, step = n >> 1, tl = tile(i, step);
+                if (tl >= nt) continue;
+                const int gt = g0 + tl, s = gt & 1;
+                const uint32_t done = i ? cnt[1] : cnt[0];
+                bar_wait(&sh.vf[s], (gt >> 1) & 1, sh);
+                bar_wait(&sh.pf[i], done & 1, sh);
+                tc_after();
+                const uint64_t v = vd + s * (Tc<D>::V_B >> 4);
+#pragma unroll
+                for (int u = 0; u < TILE / 16; ++u)
+                    tc_mma_ts(tmem + Tc<D>::O_COL + i * D, tmem + i * TILE + u * 8, v + u * 128, ID_PV, step > 0 || u > 0, lead);
+                cnt[0] += i == 0;
+                cnt[1] += i == 1;
+                if (!dual || i == 1) {
+                    tc_commit(&sh.ve[s], lead);
+                    tc_commit(&sh.me[gt & (TC_META - 1)], lead);
+                }
+                tc_commit(&sh.pv[i], lead);
+                if (tile(i, step + 1) < nt) scores(i, tile(i, step + 1));
             }
-            tc_commit(&sh.drain);
-            // also after a wait that gave up: nothing runs on when the tensor memory is freed
-            if (!bar_try(&sh.drain, 0)) bar_wait_slow(&sh.drain, 0, nullptr);
+            g0 += nt;
+            nk0 += nt + (nt - nc);
         }
+        tc_commit(&sh.drain, lead);
+        // also after a wait that gave up: nothing runs on when the tensor memory is freed
+        if (!bar_try(&sh.drain, 0)) bar_wait_slow(&sh.drain, 0, nullptr);
         __syncwarp();
     } else if (warp < TC_SOFTMAX / 32) {
         // ---- softmax of stream i; thread = row
