@@ -247,13 +247,14 @@ __device__ __forceinline__ uint32_t tail_bits(const Att& P, int b, int n, int op
 //   w_j = x_j + log2 s_v,j,  M = max w_j,  P_j = 2^(w_j - M),
 //   O = sum P_j v_j,  l = sum P_j / s_v,j,  out = O / l.
 // M follows the weight with which a value enters O, so that f16 holds the
-// leading P whatever the blocks' scales are.  O is rescaled only when M grows by
-// more than 2^4; P_BIAS lifts P to at most 2^15, so that f16's smallest step is
-// 2^-35 of the leading one.
+// leading P whatever the blocks' scales are.  M is kept a whole number (rounded up),
+// so that bringing earlier P to a larger one only moves their exponents, and it
+// is changed only when it grows by more than 3; P_BIAS lifts P to at most 2^15, and
+// the leading one to 2^11 or more: f16's smallest step is 2^-35 of it.
 constexpr int TC_SOFTMAX = 256, TC_CONV = 256, TC_BT = 640;
 constexpr int TC_W_CONV = 8, TC_W_MMA = 16, TC_W_COPY = 17, TC_W_SCALE = 18;
 constexpr int TC_META = 4;                // tiles whose scales are kept
-constexpr float P_BIAS = 11.f, M_SLACK = 4.f;
+constexpr float P_BIAS = 12.f, M_SLACK = 3.f;
 
 template <int D> struct Tc {
     static constexpr int HALVES = D / 64;                 // 128-byte rows of 64 f16
@@ -431,14 +432,13 @@ __device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t (&r)[32]) {
                    "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
                  : "r"(a));
 }
-__device__ __forceinline__ void tc_st32(uint32_t a, const uint32_t (&r)[32]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-                 "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};"
-                 :: "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-                    "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-                    "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-                    "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(a)
-                 : "memory");
+// Sixteen columns, waited for.
+__device__ __forceinline__ void tc_ld16(uint32_t a, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+                 "%15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(a) : "memory");
 }
 __device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t (&r)[16]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
@@ -884,37 +884,39 @@ __device__ __forceinline__ float group_probs(const uint32_t (&r)[32], int u, flo
     }
     return gs.x + gs.y;
 }
-// The largest w of the row's keys.
-template <int MODE>
-__device__ __forceinline__ float tile_max(uint32_t s_col, const float* meta, float rq, const uint32_t (&mk)[4]) {
-    float mx = NEG_INF;
+// A row's running maximum grows to `m2` after `c` of the tile's four groups of 32 keys: what has been summed so far (O, and
+// the P of these groups) is brought to it.  Seldom taken once the first tiles are through.
+template <int D>
+__device__ __forceinline__ void rescale(uint32_t s_col, uint32_t o_col, int c, bool has_o, float f) {
+    tc_wait_st();                        // the P that are read back
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-        uint32_t r[32];
-        tc_ld32(s_col + 32 * c, r);
-        tc_wait_ld(r);
-        if (MODE > 0) {
-            const uint32_t bits = mk[c];
+    for (int i = 0; i < c; ++i) {
+        uint32_t p[16];
+        tc_ld16(s_col + 16 * i, p);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (!((bits >> j) & 1)) r[j] = 0xff800000u;
+        for (int j = 0; j < 16; ++j) {   // in f32: f may be too small for f16 where P f is not
+            float x, y;
+            asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(x), "=f"(y) : "r"(p[j]));
+            p[j] = pack_f16(x * f, y * f);
         }
-        if (MODE < 2) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-                mx = fmaxf(mx, fmaf(group_max(r, u), fmaxf(meta[2 * c + u] * rq, 1.2e-38f), meta[TILE + 2 * c + u]));
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                mx = fmaxf(mx, fmaf(__uint_as_float(r[j]), fmaxf(meta[32 * c + j] * rq, 1.2e-38f), meta[TILE + 32 * c + j]));
-        }
+        tc_st16(s_col + 16 * i, p);
     }
-    return mx;
+    if (!has_o) return;
+#pragma unroll 1
+    for (int i = 0; i < D; i += 16) {
+        uint32_t o[16];
+        tc_ld16(o_col + i, o);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+        tc_st16(o_col + i, o);
+    }
 }
-// P = 2^(w + sub) in f16 over the scores; returns the row's sum of P / s_v.
-template <int MODE>
-__device__ __forceinline__ float tile_probs(uint32_t s_col, const float* meta, float rq, const uint32_t (&mk)[4], float sub) {
-    float l = 0.f;
+
+// One pass over a tile's scores, 32 keys at a time: P = 2^(w - m + P_BIAS) in f16 over the scores, with m the largest w up
+// to M_SLACK ago.
+template <int D, int MODE>
+__device__ __forceinline__ void tile_softmax(uint32_t s_col, uint32_t o_col, const float* meta, float rq, const uint32_t (&mk)[4],
+                                             bool has_o, float& m, float& l) {
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
         uint32_t r[32], p[16];
@@ -926,28 +928,44 @@ __device__ __forceinline__ float tile_probs(uint32_t s_col, const float* meta, f
             for (int j = 0; j < 32; ++j)
                 if (!((bits >> j) & 1)) r[j] = 0xff800000u;
         }
+        float mx = NEG_INF, a[2], b[2];
         if (MODE < 2) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-                l = fmaf(group_probs(r, u, fmaxf(meta[2 * c + u] * rq, 1.2e-38f), meta[TILE + 2 * c + u] + sub, p),
-                         meta[2 * TILE + 2 * c + u], l);
+            for (int u = 0; u < 2; ++u) {
+                a[u] = fmaxf(meta[2 * c + u] * rq, 1.2e-38f);
+                b[u] = meta[TILE + 2 * c + u];
+                mx = fmaxf(mx, fmaf(group_max(r, u), a[u], b[u]));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                r[j] = __float_as_uint(fmaf(__uint_as_float(r[j]), fmaxf(meta[32 * c + j] * rq, 1.2e-38f), meta[TILE + 32 * c + j]));
+                mx = fmaxf(mx, __uint_as_float(r[j]));
+            }
+        }
+        if (__any_sync(FULL, mx > m + M_SLACK)) {
+            const float m2 = fmaxf(m, ceilf(mx)), f = m2 == NEG_INF ? 1.f : ex2(m - m2);
+            m = m2;
+            l *= f;
+            if (c > 0 || has_o) rescale<D>(s_col, o_col, c, has_o, f);
+        }
+        const float sub = P_BIAS - (m == NEG_INF ? 0.f : m);
+        if (MODE < 2) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) l = fmaf(group_probs(r, u, a[u], b[u] + sub, p), meta[2 * TILE + 2 * c + u], l);
         } else {
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
-                const int i = 32 * c + j;
-                const float x = ex2(fmaf(__uint_as_float(r[j]), fmaxf(meta[i] * rq, 1.2e-38f), meta[TILE + i] + sub));
-                const float y = ex2(fmaf(__uint_as_float(r[j + 1]), fmaxf(meta[i + 1] * rq, 1.2e-38f), meta[TILE + i + 1] + sub));
-                l = fmaf(x, meta[2 * TILE + i], l);
-                l = fmaf(y, meta[2 * TILE + i + 1], l);
+                const float x = ex2(__uint_as_float(r[j]) + sub), y = ex2(__uint_as_float(r[j + 1]) + sub);
+                l = fmaf(x, meta[2 * TILE + 32 * c + j], l);
+                l = fmaf(y, meta[2 * TILE + 32 * c + j + 1], l);
                 p[j / 2] = pack_f16(x, y);
             }
         }
         tc_st16(s_col + 16 * c, p);      // columns that have been read
     }
-    return l;
 }
 
-// What a CTA leaves of an item that it does not hold whole.
 // A partial result: the output rows, then the rows' maxima and sums; a multiple of 16 bytes.
 __host__ __device__ constexpr size_t partial_floats(size_t rows, int D) { return (rows * (D + 2) + 3) / 4 * 4; }
 template <int D>
@@ -1117,34 +1135,14 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
                 }
                 const int mode = t >= g.q.nct ? 2 : (t + 1) * TILE > g.q.full ? 1 : 0;
                 uint32_t mk[4] = {};
-                float mx;
+                // with this tile's scores the product before them has ended: O can be rescaled
                 if (mode == 0) {
-                    mx = tile_max<0>(s_col, meta, rq, mk);
+                    tile_softmax<D, 0>(s_col, o_col + i * D, meta, rq, mk, !begins, m, l);
                 } else {
                     tile_mask(P, g, t, n, mk);
-                    mx = mode == 1 ? tile_max<1>(s_col, meta, rq, mk) : tile_max<2>(s_col, meta, rq, mk);
+                    if (mode == 1) tile_softmax<D, 1>(s_col, o_col + i * D, meta, rq, mk, !begins, m, l);
+                    else tile_softmax<D, 2>(s_col, o_col + i * D, meta, rq, mk, !begins, m, l);
                 }
-                if (begins) {
-                    m = mx;
-                } else if (__any_sync(FULL, mx > m + M_SLACK)) {
-                    // the product before this tile's scores has ended: O can be rescaled
-                    const float m2 = fmaxf(m, mx);
-                    const float f = m2 == NEG_INF ? 1.f : ex2(m - m2);
-                    l *= f;
-                    m = m2;
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tc_ld32(o_col + i * D + c, o);
-                        tc_wait_ld(o);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                        tc_st32(o_col + i * D + c, o);
-                    }
-                }
-                const float sub = P_BIAS - (m == NEG_INF ? 0.f : m);
-                l += mode == 0 ? tile_probs<0>(s_col, meta, rq, mk, sub)
-                     : mode == 1 ? tile_probs<1>(s_col, meta, rq, mk, sub) : tile_probs<2>(s_col, meta, rq, mk, sub);
                 tc_wait_st();
                 tc_before();
                 bar_arrive(&sh.pf[i]);
