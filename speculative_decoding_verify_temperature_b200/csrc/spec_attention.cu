@@ -377,14 +377,18 @@ __device__ __noinline__ bool bar_wait_slow(uint64_t* b, uint32_t parity, volatil
     const unsigned long long t0 = global_ns();
     for (unsigned i = 0; i < WAIT_TRIES; ++i) {
         if (bar_try(b, parity)) return true;
-        if (abort && *abort) return false;
-        if (global_ns() - t0 > WAIT_NS) break;
+        if ((i & 63) == 63) {
+            if (abort && *abort) return false;
+            if (global_ns() - t0 > WAIT_NS) break;
+        }
     }
     return false;
 }
+// Whole warps call it: lanes may leave the polls one after the other, and what follows (tensor memory accesses, elected
+// issue) wants them together.
 __device__ __forceinline__ void bar_wait(uint64_t* b, uint32_t parity, TcShared& sh) {
-    if (bar_try(b, parity)) return;
-    if (!bar_wait_slow(b, parity, &sh.abort)) *reinterpret_cast<volatile int*>(&sh.abort) = 1;
+    if (!bar_try(b, parity) && !bar_wait_slow(b, parity, &sh.abort)) *reinterpret_cast<volatile int*>(&sh.abort) = 1;
+    __syncwarp();
 }
 
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -508,9 +512,13 @@ __device__ void tc_copy_pages(const Att& P, const CUtensorMap* kmap, TcShared& s
     int nk = 0, nv = 0, ahead = -2, ahead_t = -1, ahead_b = -1;
     while (u.next(P)) {
         // The tail does not lie in pages; it takes two units of keys, which this warp sees pass: a barrier's parity
-        // says nothing to a waiter that is two phases behind or ahead.
+        // says nothing to a waiter that is two phases behind or ahead.  So it also arrives at the units, which cannot be
+        // used, and their barriers cannot go on, before it has.
         if (!u.cached()) {
-            for (int i = 0; i < 2; ++i, ++nk) bar_wait(&sh.ke[nk % KR], ((nk / KR) & 1) ^ 1, sh);
+            for (int i = 0; i < 2; ++i, ++nk) {
+                bar_wait(&sh.ke[nk % KR], ((nk / KR) & 1) ^ 1, sh);
+                if (lane == 0) bar_arrive(&sh.kf[nk % KR]);
+            }
             continue;
         }
         const int page = ahead_b == u.g.b && ahead_t == u.t ? ahead : page_entry(P, u.g, u.t, lane);
@@ -523,7 +531,10 @@ __device__ void tc_copy_pages(const Att& P, const CUtensorMap* kmap, TcShared& s
         const int ks = nk % KR, vs = nv % VR;
         const int64_t ph = (int64_t)page * P.Hkv + u.g.h;
         bar_wait(&sh.ke[ks], ((nk / KR) & 1) ^ 1, sh);
-        if (lane == 0) bar_expect(&sh.kf[ks], all);
+        if (lane == 0) {
+            bar_arrive(&sh.kf[ks]);                       // in the place of the operand warps
+            bar_expect(&sh.kf[ks], all);
+        }
         __syncwarp();
         if (ok) tensor_copy(base + Tc<D>::K + ks * Tc<D>::RAW_B + lane * bytes, kmap, (int)(ph << P.pshift), &sh.kf[ks]);
         bar_wait(&sh.re[vs], ((nv / VR) & 1) ^ 1, sh);
@@ -598,14 +609,15 @@ __device__ __forceinline__ void tc_scales(const Att& P, TcShared& sh, const Stre
         if (more) fetch(u.g, u.t, ks, vs);
         if (more && u.first()) prefetch_segment<D>(P, u, lane);
         bar_wait(&sh.me[m], par, sh);
-        if (!cached) continue;                            // the operand warps write the tail's
-        if (lane < 8) {
+        // the operand warps write the tail's; they arrive once and this warp once (for the reason given at the copies)
+        if (cached && lane < 8) {
             sh.meta[m][0][lane] = k0;
             sh.meta[m][1][lane] = log2f(v0);
             sh.meta[m][2][lane] = 1.f / v0;
         }
         __syncwarp();
         if (lane == 0) bar_arrive(&sh.mf[m]);
+        if (lane == 0 && cached) bar_arrive(&sh.mf[m]);
     }
 }
 
@@ -987,13 +999,13 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
     if (st.lo >= st.hi) return;
     if (tid == 0) {
         for (int i = 0; i < 6; ++i) {
-            bar_init(&sh.kf[i], 1);
+            bar_init(&sh.kf[i], 2);
             bar_init(&sh.ke[i], 1);
         }
         for (int i = 0; i < 4; ++i) {
             bar_init(&sh.rf[i], 1);
             bar_init(&sh.re[i], TC_CONV / 32);
-            bar_init(&sh.mf[i], 1);
+            bar_init(&sh.mf[i], 2);
             bar_init(&sh.me[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
