@@ -1339,9 +1339,9 @@ __global__ void __launch_bounds__(MERGE_BT) k_attention_merge(const Att P) {
 // ----------------------------------------------------------------------------- few rows (mma.sync)
 
 // At most 16 rows of a kv head (single tokens, short chains): bound by the bytes
-// of the cache.  A warp takes 16 keys at a time; tensor copies bring their 2 D
-// bytes to a ring of three in shared memory that is the warp's own, so that two of
-// them are on their way while one is computed (three warps per scheduler, 8 KB each at D = 128).
+// of the cache.  A warp takes 32 keys of each tile (two chunks of 16); tensor
+// copies bring their bytes to a ring of two tiles in shared memory that is the warp's own, so
+// that the next tile's are on their way while one is computed (8 KB for each of 12 warps at D = 128).
 // From there they go straight into the fragments of m16n8k16 products: the
 // dimensions that are summed over, and the columns of the result, may stand in
 // any order as long as both sides agree, so each lane reads 16 bytes where it needs them
@@ -1353,7 +1353,7 @@ __global__ void __launch_bounds__(MERGE_BT) k_attention_merge(const Att P) {
 //           makes the pair that the step for column block j wants.
 // Each warp has its own running maximum, sum and output (in registers); the four
 // are joined through shared memory at the end of an item.
-constexpr int MM_BT = 128, MM_WARPS = MM_BT / 32, MM_ROWS = 16, MM_RING = 3, MM_CTAS_SM = 3;
+constexpr int MM_BT = 128, MM_WARPS = MM_BT / 32, MM_ROWS = 16, MM_CTAS_SM = 3;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -1383,10 +1383,10 @@ __device__ __forceinline__ uint32_t bf16_amax(uint32_t (&w)[N], bool& bad, bool 
 __device__ __forceinline__ int bits_exp(uint32_t m) { return m ? max(min((int)(m >> 7), 253), 1) - 127 : 0; }
 __device__ __forceinline__ uint32_t bf16_f16(uint32_t w, float s) { return pack_f16(bf_lo(w) * s, bf_hi(w) * s); }
 
-// 16 keys as a warp sees them.
-struct Chunk {
-    int tok, is;                          // first key; kind (0 none left, 1 cached, 2 tail, 3 nothing to do), kv head, segment's parity
-    __device__ __forceinline__ int kind() const { return is & 3; }
+// A warp's part of a tile.
+struct Part {
+    int tok, is;                          // the tile's first key; what it is, kv head, segment's parity
+    __device__ __forceinline__ int kind() const { return is & 3; }       // 0 none left, 1 cached, 2 tail, 3 nothing to do
     __device__ __forceinline__ int h() const { return is >> 2 & 0xfff; }
     __device__ __forceinline__ int parity() const { return is >> 14; }
 };
@@ -1396,13 +1396,13 @@ struct MmAhead {
     int more;
 };
 
-// A warp's ring: its slots of 16 keys and values; their page's scales.
+// A warp's ring: two tiles' 2 x 16 keys and values; their pages' scales.
 template <int D> struct MmRing {
-    unsigned char k[MM_RING][16 * D], v[MM_RING][16 * D];
+    unsigned char k[2][2][16 * D], v[2][2][16 * D];
 };
 struct MmSlots {
-    float scale[MM_RING][2];
-    uint64_t full[MM_RING];
+    float scale[2][2][2];                                 // [slot][chunk][keys, values]
+    uint64_t full[2];
 };
 
 template <int D>
@@ -1413,7 +1413,7 @@ struct MmWarp {
     const Att& P;
     const int lane, warp, g, c;
     MmAhead& a;                                           // the segment of the chunk after, kept by lane 0
-    int t, sub, parity;
+    int t, parity;
     float o[NT][4], m[2], l[2];
 
     __device__ __forceinline__ MmWarp(const Att& P_, int warp_, MmAhead& a_)
@@ -1427,69 +1427,69 @@ struct MmWarp {
         __syncwarp();
         parity = 1;
         t = 0;
-        sub = TILE / 16;
     }
-    // The chunk after, and (cached) its page.
-    __device__ __forceinline__ Chunk next(int& page) {
-        Chunk x{};
-        page = 0;
-        sub += MM_WARPS;
-        if (sub >= TILE / 16) {
-            sub = warp;
-            if (++t >= a.s.t1) {
-                __syncwarp();
-                if (lane == 0) a.more = a.it.next(P, a.s);
-                __syncwarp();
-                if (!a.more) return x;
-                parity ^= 1;
-                t = a.s.t0;
-            }
+    // The warp's part of the tile after, and in lanes 0 and 1 the pages of its two chunks (-2: none).
+    __device__ __forceinline__ Part next(int& page) {
+        Part x{};
+        page = -2;
+        if (++t >= a.s.t1) {
+            __syncwarp();
+            if (lane == 0) a.more = a.it.next(P, a.s);
+            __syncwarp();
+            if (!a.more) return x;
+            parity ^= 1;
+            t = a.s.t0;
         }
         const Seg& s = a.s;
-        x.tok = (t < s.q.nct ? t : t - s.q.nct) * TILE + sub * 16;
-        const int keys = s.q.len >= 0 && !s.q.bad ? s.q.open + P.N : 0;
-        const int kind = t < s.q.nct ? (x.tok < s.q.full ? 1 : 3) : x.tok < keys ? 2 : 3;
-        x.is = kind | s.h << 2 | parity << 14;
-        if (kind == 1) page = __ldg(P.c.page_table + s.b * P.c.page_table_stride + (x.tok >> P.pshift));
+        const bool cached = t < s.q.nct;
+        x.tok = (cached ? t : t - s.q.nct) * TILE;
+        x.is = (cached ? 1 : s.q.len >= 0 && !s.q.bad ? 2 : 3) | s.h << 2 | parity << 14;
+        const int tok = x.tok + first_key(lane);
+        if (cached && lane < 2 && tok < s.q.full) page = __ldg(P.c.page_table + s.b * P.c.page_table_stride + (tok >> P.pshift));
         return x;
     }
-    // A cached chunk's bytes and scales on their way to slot s of the ring (every chunk passes through a slot).
-    __device__ __forceinline__ void fetch(const Chunk& x, int id, int s, MmRing<D>& ring, MmSlots& slots, const CUtensorMap* kmap,
+    __device__ __forceinline__ int first_key(int chunk) const { return 16 * (warp + MM_WARPS * chunk); }
+    // A cached part's bytes and scales on their way to slot s of the ring: chunk h by lane h.  A chunk behind the last key,
+    // or of a page that is not there, brings nothing.
+    __device__ __forceinline__ void fetch(const Part& x, int id, int s, MmRing<D>& ring, MmSlots& slots, const CUtensorMap* kmap,
                                           const CUtensorMap* vmap) const {
-        if (x.kind() == 0) return;
-        const bool there = x.kind() == 1 && id >= 0 && id < P.c.num_pages;
-        const int64_t ph = (int64_t)id * P.Hkv + x.h();
+        if (x.kind() != 1) return;
         __syncwarp();                                     // the slot has been read
         if (lane < 2) {
-            if (there) {
-                copy4(&slots.scale[s][lane], (lane ? P.c.v_scale : P.c.k_scale) + ph);
-                if (lane == 0) {
-                    const int row = (int)((ph << P.pshift) + (x.tok & (P.page - 1)));
-                    bar_expect(&slots.full[s], 2 * 16 * D);
-                    tensor_copy(smem_u32(ring.k[s]), kmap, row, &slots.full[s]);
-                    tensor_copy(smem_u32(ring.v[s]), vmap, row, &slots.full[s]);
-                }
-            } else if (lane == 0) {
+            if (id >= 0 && id < P.c.num_pages) {
+                const int64_t ph = (int64_t)id * P.Hkv + x.h();
+                const int row = (int)((ph << P.pshift) + ((x.tok + first_key(lane)) & (P.page - 1)));
+                copy4(&slots.scale[s][lane][0], P.c.k_scale + ph);
+                copy4(&slots.scale[s][lane][1], P.c.v_scale + ph);
+                bar_expect(&slots.full[s], 2 * 16 * D);
+                tensor_copy(smem_u32(ring.k[s][lane]), kmap, row, &slots.full[s]);
+                tensor_copy(smem_u32(ring.v[s][lane]), vmap, row, &slots.full[s]);
+            } else {
                 bar_arrive(&slots.full[s]);
             }
             copy4_arrive(&slots.full[s]);
         }
     }
-    // Scores of two key blocks to probabilities (f16 fragments of the second product).  a: per column the key's scale
-    // (rows' factors rq come on top), b: log2 of its value's, inv: 1 / that.
-    __device__ __forceinline__ void softmax(const float (&s)[2][4], const float (&rq)[2], const float (&a)[4], const float (&b)[4],
-                                            const float (&inv)[4], const uint32_t (&mask)[2], uint32_t (&p)[4]) {
-        float w[2][4];                                    // [row g, g + 8][keys 2c, 2c + 1, 2c + 8, 2c + 9]
+    // Scores of NB blocks of 8 keys to probabilities (f16 fragments of the second product).  a: per column the key's scale
+    // (the rows' factors rq come on top), b: log2 of its value's, inv: 1 / that; both per pair of blocks or (EACH) per key.
+    template <int NB, bool EACH>
+    __device__ __forceinline__ void softmax(float (&s)[NB][4], const float (&rq)[2], const float (&a)[2 * NB], const float (&b)[2 * NB],
+                                            const float (&inv)[2 * NB], const uint32_t (&mask)[2], uint32_t (&p)[NB / 2][4]) {
         bool grow = false;
         float top[2];
+        auto at = [](int j, int e) { return EACH ? 2 * j + e : j >> 1; };
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
+            float mx = NEG_INF;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float x = fmaf(s[j >> 1][2 * r + (j & 1)], fmaxf(a[j] * rq[r], 1.2e-38f), b[j]);
-                w[r][j] = (mask[r] >> (2 * c + (j & 1) + (j >> 1) * 8)) & 1 ? x : NEG_INF;
-            }
-            float mx = fmaxf(fmaxf(w[r][0], w[r][1]), fmaxf(w[r][2], w[r][3]));
+            for (int j = 0; j < NB; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float& x = s[j][2 * r + e];
+                    x = fmaf(x, fmaxf(a[at(j, e)] * rq[r], 1.2e-38f), b[at(j, e)]);
+                    if (EACH && !((mask[r] >> (2 * c + e + 8 * j)) & 1)) x = NEG_INF;
+                    mx = fmaxf(mx, x);
+                }
             mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
             top[r] = fmaxf(m[r], mx);
@@ -1512,62 +1512,76 @@ struct MmWarp {
         for (int r = 0; r < 2; ++r) {
             const float sub = P_BIAS - (m[r] == NEG_INF ? 0.f : m[r]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                w[r][j] = ex2(w[r][j] + sub);
-                l[r] = fmaf(w[r][j], inv[j], l[r]);
+            for (int j = 0; j < NB; ++j) {
+                const float x = ex2(s[j][2 * r] + sub), y = ex2(s[j][2 * r + 1] + sub);
+                if (EACH) {
+                    l[r] = fmaf(x, inv[at(j, 0)], l[r]);
+                    l[r] = fmaf(y, inv[at(j, 1)], l[r]);
+                } else {
+                    l[r] = fmaf(x + y, inv[at(j, 0)], l[r]);
+                }
+                p[j >> 1][r + 2 * (j & 1)] = pack_f16(x, y);
             }
-            p[r] = pack_f16(w[r][0], w[r][1]);
-            p[2 + r] = pack_f16(w[r][2], w[r][3]);
         }
     }
     // 16-byte piece q of row r of a slot, as the tensor copy swizzles it.
     static __device__ __forceinline__ uint32_t piece(uint32_t at, int r, int q) {
         return at + r * D + ((D == 128 ? q ^ (r & 7) : q ^ (r >> 1 & 3)) << 4);
     }
+    // The first NC chunks of a slot.
+    template <int NC>
     __device__ __forceinline__ void cached(const MmRing<D>& ring, const MmSlots& slots, int sl, const uint4* qf, const float (&rq)[2]) {
-        const uint32_t kp = smem_u32(ring.k[sl]), vp = smem_u32(ring.v[sl]);
-        float s[2][4] = {};
+        float s[2 * NC][4] = {};
 #pragma unroll
         for (int j = 0; j < KH; ++j) {
-            uint4 k[2];
+            uint4 k[2 * NC];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) k[i] = lds128(piece(kp, g + 8 * i, KH * c + j));
+            for (int i = 0; i < 2 * NC; ++i) k[i] = lds128(piece(smem_u32(ring.k[sl][i >> 1]), g + 8 * (i & 1), KH * c + j));
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const uint4 a = qf[(j * 4 + u) * 32 + lane];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < 2 * NC; ++i) {
                     const uint2 b = e4m3_f16(u == 0 ? k[i].x : u == 1 ? k[i].y : u == 2 ? k[i].z : k[i].w);
                     mma16816(s[i], a.x, a.y, a.z, a.w, b.x, b.y);
                 }
             }
         }
-        uint32_t v[4][VW];
+        float aa[4 * NC], bb[4 * NC], ii[4 * NC];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 2 * c + (i & 1) + (i >> 1) * 8;
-            if constexpr (VW == 4) {
-                const uint4 w = lds128(piece(vp, r, g));
-                v[i][0] = w.x; v[i][1] = w.y; v[i][2] = w.z; v[i][3] = w.w;
-            } else {
-                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[i][0]), "=r"(v[i][1]) : "r"(piece(vp, r, g >> 1) + (g & 1) * 8));
-            }
+        for (int n = 0; n < NC; ++n) {
+            const float vs = slots.scale[sl][n][1];
+            aa[n] = slots.scale[sl][n][0];
+            bb[n] = __log2f(vs);
+            ii[n] = __frcp_rn(vs);
         }
-        const float ks = slots.scale[sl][0], vs = slots.scale[sl][1];
-        const float lv = __log2f(vs), iv = __frcp_rn(vs);
-        const float aa[4] = {ks, ks, ks, ks}, bb[4] = {lv, lv, lv, lv}, ii[4] = {iv, iv, iv, iv};
-        const uint32_t all[2] = {0xffffu, 0xffffu};
-        uint32_t p[4];
-        softmax(s, rq, aa, bb, ii, all, p);
+        const uint32_t none[2] = {};
+        uint32_t p[NC][4];
+        softmax<2 * NC, false>(s, rq, aa, bb, ii, none, p);
 #pragma unroll
-        for (int u = 0; u < VW; ++u)
+        for (int n = 0; n < NC; ++n) {
+            uint32_t v[4][VW];
+            const uint32_t vp = smem_u32(ring.v[sl][n]);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {                 // bytes 2h, 2h + 1 of word u, of two keys side by side
-                const uint2 x = e4m3_f16(__byte_perm(v[0][u], v[1][u], h ? 0x7362 : 0x5140));
-                const uint2 y = e4m3_f16(__byte_perm(v[2][u], v[3][u], h ? 0x7362 : 0x5140));
-                mma16816(o[4 * u + 2 * h], p[0], p[1], p[2], p[3], x.x, y.x);
-                mma16816(o[4 * u + 2 * h + 1], p[0], p[1], p[2], p[3], x.y, y.y);
+            for (int i = 0; i < 4; ++i) {
+                const int r = 2 * c + (i & 1) + (i >> 1) * 8;
+                if constexpr (VW == 4) {
+                    const uint4 w = lds128(piece(vp, r, g));
+                    v[i][0] = w.x; v[i][1] = w.y; v[i][2] = w.z; v[i][3] = w.w;
+                } else {
+                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[i][0]), "=r"(v[i][1]) : "r"(piece(vp, r, g >> 1) + (g & 1) * 8));
+                }
             }
+#pragma unroll
+            for (int u = 0; u < VW; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {             // bytes 2h, 2h + 1 of word u, of two keys side by side
+                    const uint2 x = e4m3_f16(__byte_perm(v[0][u], v[1][u], h ? 0x7362 : 0x5140));
+                    const uint2 y = e4m3_f16(__byte_perm(v[2][u], v[3][u], h ? 0x7362 : 0x5140));
+                    mma16816(o[4 * u + 2 * h], p[n][0], p[n][1], p[n][2], p[n][3], x.x, y.x);
+                    mma16816(o[4 * u + 2 * h + 1], p[n][0], p[n][1], p[n][2], p[n][3], x.y, y.y);
+                }
+        }
     }
     // 16 keys of the tail, from bf16 rows.  bad_v: the item's keys whose value is not finite.
     __device__ __forceinline__ void tail(int tok, const Seg& sg, const uint4* qf, const float (&rq)[2], uint32_t* bad_v) {
@@ -1633,18 +1647,18 @@ struct MmWarp {
 #pragma unroll
             for (int u = 0; u < VW * 2; ++u) vw[j][u] = bf16_f16(vw[j][u], exp2i(-ex));
         }
-        uint32_t mask[2], p[4];
+        uint32_t mask[2], p[1][4];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int n = min(g + 8 * r, P.R - 1) / P.G;
             mask[r] = tail_bits(P, sg.b, n, q.open, tok) & 0xffffu;
         }
-        softmax(s, rq, aa, bb, ii, mask, p);
+        softmax<2, true>(s, rq, aa, bb, ii, mask, p);
 #pragma unroll
         for (int u = 0; u < VW * 2; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                mma16816(o[2 * u + h], p[0], p[1], p[2], p[3], __byte_perm(vw[0][u], vw[1][u], h ? 0x7632 : 0x5410),
+                mma16816(o[2 * u + h], p[0][0], p[0][1], p[0][2], p[0][3], __byte_perm(vw[0][u], vw[1][u], h ? 0x7632 : 0x5410),
                          __byte_perm(vw[2][u], vw[3][u], h ? 0x7632 : 0x5410));
     }
     // The item's queries as fragments, and the factors of rows g and g + 8.
@@ -1691,7 +1705,7 @@ template <int D> struct alignas(16) MmShared {
     MmRing<D> ring[MM_WARPS];                             // 1024-byte aligned, as the swizzle wants
     MmSlots slots[MM_WARPS];
     uint4 q[D / 16][32];                                  // the query fragments: every warp writes the same
-    float4 o[MM_WARPS / 2][D / 8][32];                    // a warp's output fragments, for another one
+    float4 o[2][4][32];                                   // output fragments of two warps, four blocks at a time
     float m[MM_WARPS][MM_ROWS], l[MM_WARPS][MM_ROWS];
     uint32_t bad_v[12];
     int bad, late;
@@ -1730,18 +1744,26 @@ __device__ __forceinline__ void mm_finish(const Att& P, MmWarp<D>& w, MmShared<D
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
         w.o[j][0] *= f[0]; w.o[j][1] *= f[0]; w.o[j][2] *= f[1]; w.o[j][3] *= f[1];
-        if (w.warp >= 2) sh.o[w.warp - 2][j][w.lane] = make_float4(w.o[j][0], w.o[j][1], w.o[j][2], w.o[j][3]);
     }
-    __syncthreads();
-    if (w.warp < 2) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const float4 x = sh.o[w.warp][j][w.lane];
-            w.o[j][0] += x.x; w.o[j][1] += x.y; w.o[j][2] += x.z; w.o[j][3] += x.w;
-            if (w.warp == 1) sh.o[1][j][w.lane] = make_float4(w.o[j][0], w.o[j][1], w.o[j][2], w.o[j][3]);
+    for (int half = 2; half >= 1; half /= 2)
+#pragma unroll
+        for (int j0 = 0; j0 < NT; j0 += 4) {
+            if (w.warp >= half && w.warp < 2 * half) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    sh.o[w.warp - half][j][w.lane] = make_float4(w.o[j0 + j][0], w.o[j0 + j][1], w.o[j0 + j][2], w.o[j0 + j][3]);
+            }
+            __syncthreads();
+            if (w.warp < half) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 x = sh.o[w.warp][j][w.lane];
+                    w.o[j0 + j][0] += x.x; w.o[j0 + j][1] += x.y; w.o[j0 + j][2] += x.z; w.o[j0 + j][3] += x.w;
+                }
+            }
+            __syncthreads();
         }
-    }
-    __syncthreads();
     const bool whole = g.whole();
     const bool nan = g.q.bad || sh.bad;
     const float quiet = __int_as_float(0x7fffffff);
@@ -1750,11 +1772,6 @@ __device__ __forceinline__ void mm_finish(const Att& P, MmWarp<D>& w, MmShared<D
         uint32_t any_bad = 0;
         if (g.t1 > g.q.nct)
             for (int i = 0; i < 12; ++i) any_bad |= sh.bad_v[i];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const float4 x = sh.o[1][j][w.lane];
-            w.o[j][0] += x.x; w.o[j][1] += x.y; w.o[j][2] += x.z; w.o[j][3] += x.w;
-        }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int row = w.g + 8 * r, n = row / P.G;
@@ -1835,7 +1852,7 @@ __global__ void __launch_bounds__(MM_BT, MM_CTAS_SM) k_attention_mma(const Att P
         sh.now.more = sh.now.it.next(P, sh.now.s);
     }
     if (threadIdx.x == 64) {
-        for (int i = 0; i < MM_WARPS * MM_RING; ++i) bar_init(&sh.slots[i / MM_RING].full[i % MM_RING], 3);
+        for (int i = 0; i < MM_WARPS * 2; ++i) bar_init(&sh.slots[i >> 1].full[i & 1], 4);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         proxy_fence();
     }
@@ -1847,48 +1864,51 @@ __global__ void __launch_bounds__(MM_BT, MM_CTAS_SM) k_attention_mma(const Att P
     w.begin(st);
     uint4* qf = &sh.q[0][0];
     float rq[2];
-    int id, idy, idz, parity = -1;
-    // chunk x is computed, y and z are on their way, and the page id of the chunk after
-    Chunk x = w.next(id);
+    int id, idy, parity = -1;
+    // part x is computed, y's bytes are on their way, and the page ids of the part after
+    Part x = w.next(id);
     w.fetch(x, id, 0, ring, slots, &kmap, &vmap);
-    Chunk y = w.next(idy);
-    w.fetch(y, idy, 1, ring, slots, &kmap, &vmap);
-    Chunk z = y;
-    idz = 0;
-    if (y.kind()) z = w.next(idz);
+    Part y{};
+    idy = -2;
+    if (x.kind()) y = w.next(idy);
     bool bad = false;
     unsigned full = 0;                                    // parity of each slot's next phase
-    for (int s = 0; x.kind(); s = s == MM_RING - 1 ? 0 : s + 1) {
-        w.fetch(z, idz, s == 0 ? MM_RING - 1 : s - 1, ring, slots, &kmap, &vmap);
+    for (int s = 0; x.kind(); s ^= 1) {
+        w.fetch(y, idy, s ^ 1, ring, slots, &kmap, &vmap);
         if (x.parity() != parity) {
             parity = x.parity();
             w.load_q(sh.now.s, qf, rq);
         }
-        Chunk u = z;
-        int idu = 0;
-        if (z.kind()) u = w.next(idu);
-        if (!bar_try(&slots.full[s], full >> s & 1) && !bar_wait_slow(&slots.full[s], full >> s & 1, nullptr)) {
-            bad = true;
-            if (w.lane == 0) {                            // let it land (bounded), whatever becomes of the result
-                atomicOr(P.status, 1u << SPEC_ERR_TIMEOUT);
+        Part z{};
+        int idz = -2;
+        if (y.kind()) z = w.next(idz);
+        if (x.kind() == 1) {
+            if (!bar_try(&slots.full[s], full >> s & 1) && !bar_wait_slow(&slots.full[s], full >> s & 1, nullptr)) {
+                bad = true;
+                atomicOr(P.status, 1u << SPEC_ERR_TIMEOUT);   // let it land (bounded), whatever becomes of the result
                 if (!bar_wait_slow(&slots.full[s], full >> s & 1, nullptr)) atomicOr(P.status, 1u << SPEC_ERR_COPY_IN_FLIGHT);
             }
             __syncwarp();
+            full ^= 1u << s;
+            const unsigned there = __ballot_sync(FULL, id >= 0 && id < P.c.num_pages) & 3u, none = __ballot_sync(FULL, id == -2) & 3u;
+            bad |= (there | none) != 3u;
+            if (there == 3u) w.template cached<2>(ring, slots, s, qf, rq);
+            else if (there == 1u) w.template cached<1>(ring, slots, s, qf, rq);
+        } else if (x.kind() == 2) {
+#pragma unroll 1
+            for (int n = 0; n < 2; ++n) {
+                const int tok = x.tok + w.first_key(n);
+                if (tok < sh.now.s.q.open + P.N) w.tail(tok, sh.now.s, qf, rq, sh.bad_v);
+            }
         }
-        full ^= 1u << s;
-        if (x.kind() == 1 && id >= 0 && id < P.c.num_pages) w.cached(ring, slots, s, qf, rq);
-        else if (x.kind() == 2) w.tail(x.tok, sh.now.s, qf, rq, sh.bad_v);
-        bad |= x.kind() == 1 && (id < 0 || id >= P.c.num_pages);
         if (y.kind() == 0 || y.parity() != x.parity()) {
             mm_finish<D>(P, w, sh, bad);
             bad = false;
         }
         x = y;
         y = z;
-        z = u;
         id = idy;
         idy = idz;
-        idz = idu;
     }
 }
 
