@@ -1342,18 +1342,26 @@ __global__ void __launch_bounds__(MERGE_BT) k_attention_merge(const Att P) {
 // of the cache.  A warp takes 32 keys of each tile (two chunks of 16); tensor
 // copies bring their bytes to a ring of two tiles in shared memory that is the warp's own, so
 // that the next tile's are on their way while one is computed (8 KB for each of 12 warps at D = 128).
-// From there they go straight into the fragments of m16n8k16 products: the
-// dimensions that are summed over, and the columns of the result, may stand in
-// any order as long as both sides agree, so each lane reads 16 bytes where it needs them
-// (the swizzle keeps the lanes on different banks).
-//   scores  B column n = key n: lane (g, c) holds, of keys g and g + 8, the bytes
-//           [c D/4, (c + 1) D/4); four of them feed one 16-wide step.
-//   values  B row k = key k, column g: lane (g, c) holds, of keys 2c, 2c + 1,
-//           2c + 8, 2c + 9, the dims [g D/8, (g + 1) D/8): byte j of two keys
-//           makes the pair that the step for column block j wants.
+// From there they go straight into the fragments of m16n8k16 products, with the
+// keys (scores) and the dims (output) as rows and 8 queries as columns: NQ = 1 for up
+// to 8 rows of a kv head, 2 for up to 16.  The dimensions that are summed over, and the rows of the
+// output, may stand in any order as long as both sides agree, so each lane reads 16 bytes where it
+// needs them (the swizzle keeps the lanes on different banks).
+//   scores  rows: lane (g, c) holds, of keys g and g + 8, the bytes [c D/4, (c + 1) D/4);
+//           four of them feed one 16-wide step.  Columns: queries.
+//   output  lane (g, c) holds, of keys 2c, 2c + 1, 2c + 8, 2c + 9, the dims [g D/8, (g + 1) D/8):
+//           bytes 2t and 2t + 1 of two keys make the pairs that row block t wants in its rows g and g + 8.
+// Probabilities leave the first product with a key per row and enter the second with a query per column:
+// 8 x 8 transposes between registers.
 // Each warp has its own running maximum, sum and output (in registers); the four
 // are joined through shared memory at the end of an item.
 constexpr int MM_BT = 128, MM_WARPS = MM_BT / 32, MM_ROWS = 16, MM_CTAS_SM = 3;
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -1405,16 +1413,17 @@ struct MmSlots {
     uint64_t full[2];
 };
 
-template <int D>
+template <int D, int NQ>
 struct MmWarp {
     static constexpr int KH = D / 64;                     // 16-byte pieces of a key per lane
     static constexpr int VW = D / 32;                     // 4-byte words of a value per lane
-    static constexpr int NT = D / 8;                      // column blocks of the output
+    static constexpr int NT = D / 16;                     // row blocks of the output
     const Att& P;
     const int lane, warp, g, c;
     MmAhead& a;                                           // the segment of the chunk after, kept by lane 0
     int t, parity;
-    float o[NT][4], m[2], l[2];
+    // [column block][..]: dims g D/8 + 2t (0, 1) and + 1 (2, 3) of queries 2c and 2c + 1; their maxima and this lane's sums
+    float o[NQ][NT][4], m[NQ][2], l[NQ][2];
 
     __device__ __forceinline__ MmWarp(const Att& P_, int warp_, MmAhead& a_)
         : P(P_), lane(threadIdx.x & 31), warp(warp_), g(lane >> 2), c(lane & 3), a(a_) {}
@@ -1470,68 +1479,83 @@ struct MmWarp {
             copy4_arrive(&slots.full[s]);
         }
     }
-    // Scores of NB blocks of 8 keys to probabilities (f16 fragments of the second product).  a: per column the key's scale
-    // (the rows' factors rq come on top), b: log2 of its value's, inv: 1 / that; both per pair of blocks or (EACH) per key.
-    template <int NB, bool EACH>
-    __device__ __forceinline__ void softmax(float (&s)[NB][4], const float (&rq)[2], const float (&a)[2 * NB], const float (&b)[2 * NB],
-                                            const float (&inv)[2 * NB], const uint32_t (&mask)[2], uint32_t (&p)[NB / 2][4]) {
+    // Scores of NC x 16 keys to probabilities (the second product's columns).  Of keys g (0) and g + 8 (1) of each chunk: a the
+    // scale (the queries' factors rq come on top), b log2 of the value's, inv 1 / that.  EACH: these differ from key to key,
+    // and mask bit 8 i says whether the query sees key g + 8 i.
+    template <int NC, bool EACH>
+    __device__ __forceinline__ void softmax(float (&s)[NC][NQ][4], const float (&rq)[NQ][2], const float (&a)[NC][2], const float (&b)[NC][2],
+                                            const float (&inv)[NC][2], const uint32_t (&mask)[NQ][2], uint32_t (&p)[NC][NQ][2]) {
         bool grow = false;
-        float top[2];
-        auto at = [](int j, int e) { return EACH ? 2 * j + e : j >> 1; };
+        float top[NQ][2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float mx = NEG_INF;
+        for (int q = 0; q < NQ; ++q)
 #pragma unroll
-            for (int j = 0; j < NB; ++j)
+            for (int e = 0; e < 2; ++e) {
+                float mx = NEG_INF;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float& x = s[j][2 * r + e];
-                    x = fmaf(x, fmaxf(a[at(j, e)] * rq[r], 1.2e-38f), b[at(j, e)]);
-                    if (EACH && !((mask[r] >> (2 * c + e + 8 * j)) & 1)) x = NEG_INF;
-                    mx = fmaxf(mx, x);
-                }
-            mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
-            top[r] = fmaxf(m[r], mx);
-            grow |= mx > m[r] + M_SLACK;
-        }
+                for (int n = 0; n < NC; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float& x = s[n][q][2 * i + e];
+                        x = fmaf(x, fmaxf(a[n][i] * rq[q][e], 1.2e-38f), b[n][i]);
+                        if (EACH && !((mask[q][e] >> (g + 8 * i)) & 1)) x = NEG_INF;
+                        mx = fmaxf(mx, x);
+                    }
+                top[q][e] = mx;
+                grow |= mx > m[q][e] + M_SLACK;
+            }
         if (__any_sync(FULL, grow)) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float f = top[r] == NEG_INF ? 1.f : ex2(m[r] - top[r]);
-                m[r] = top[r];
-                l[r] *= f;
+            for (int q = 0; q < NQ; ++q)
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    o[j][2 * r] *= f;
-                    o[j][2 * r + 1] *= f;
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(m[q][e], top[q][e]);
+#pragma unroll
+                    for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, d));
+                    const float f = mx == NEG_INF ? 1.f : ex2(m[q][e] - mx);
+                    m[q][e] = mx;
+                    l[q][e] *= f;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        o[q][j][e] *= f;
+                        o[q][j][2 + e] *= f;
+                    }
                 }
-            }
         }
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const float sub = P_BIAS - (m[r] == NEG_INF ? 0.f : m[r]);
+        for (int q = 0; q < NQ; ++q) {
+            float sub[2];
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                const float x = ex2(s[j][2 * r] + sub), y = ex2(s[j][2 * r + 1] + sub);
-                if (EACH) {
-                    l[r] = fmaf(x, inv[at(j, 0)], l[r]);
-                    l[r] = fmaf(y, inv[at(j, 1)], l[r]);
-                } else {
-                    l[r] = fmaf(x + y, inv[at(j, 0)], l[r]);
+            for (int e = 0; e < 2; ++e) sub[e] = P_BIAS - (m[q][e] == NEG_INF ? 0.f : m[q][e]);
+#pragma unroll
+            for (int n = 0; n < NC; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float x = ex2(s[n][q][2 * i] + sub[0]), y = ex2(s[n][q][2 * i + 1] + sub[1]);
+                    l[q][0] = fmaf(x, inv[n][i], l[q][0]);
+                    l[q][1] = fmaf(y, inv[n][i], l[q][1]);
+                    p[n][q][i] = transpose8(pack_f16(x, y));
                 }
-                p[j >> 1][r + 2 * (j & 1)] = pack_f16(x, y);
-            }
         }
     }
     // 16-byte piece q of row r of a slot, as the tensor copy swizzles it.
     static __device__ __forceinline__ uint32_t piece(uint32_t at, int r, int q) {
         return at + r * D + ((D == 128 ? q ^ (r & 7) : q ^ (r >> 1 & 3)) << 4);
     }
+    // The queries of 16 dims: fragments of NQ columns.
+    static __device__ __forceinline__ void columns(const uint32_t* qf, int u, int lane, uint32_t (&b)[NQ][2]) {
+        if constexpr (NQ == 1) {
+            const uint2 x = reinterpret_cast<const uint2*>(qf)[u * 32 + lane];
+            b[0][0] = x.x; b[0][1] = x.y;
+        } else {
+            const uint4 x = reinterpret_cast<const uint4*>(qf)[u * 32 + lane];
+            b[0][0] = x.x; b[0][1] = x.y; b[1][0] = x.z; b[1][1] = x.w;
+        }
+    }
     // The first NC chunks of a slot.
     template <int NC>
-    __device__ __forceinline__ void cached(const MmRing<D>& ring, const MmSlots& slots, int sl, const uint4* qf, const float (&rq)[2]) {
-        float s[2 * NC][4] = {};
+    __device__ __forceinline__ void cached(const MmRing<D>& ring, const MmSlots& slots, int sl, const uint32_t* qf, const float (&rq)[NQ][2]) {
+        float s[NC][NQ][4] = {};
 #pragma unroll
         for (int j = 0; j < KH; ++j) {
             uint4 k[2 * NC];
@@ -1539,25 +1563,29 @@ struct MmWarp {
             for (int i = 0; i < 2 * NC; ++i) k[i] = lds128(piece(smem_u32(ring.k[sl][i >> 1]), g + 8 * (i & 1), KH * c + j));
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const uint4 a = qf[(j * 4 + u) * 32 + lane];
+                uint32_t b[NQ][2];
+                columns(qf, j * 4 + u, lane, b);
 #pragma unroll
-                for (int i = 0; i < 2 * NC; ++i) {
-                    const uint2 b = e4m3_f16(u == 0 ? k[i].x : u == 1 ? k[i].y : u == 2 ? k[i].z : k[i].w);
-                    mma16816(s[i], a.x, a.y, a.z, a.w, b.x, b.y);
+                for (int n = 0; n < NC; ++n) {
+                    const uint4 &k0 = k[2 * n], &k1 = k[2 * n + 1];
+                    const uint2 x = e4m3_f16(u == 0 ? k0.x : u == 1 ? k0.y : u == 2 ? k0.z : k0.w);
+                    const uint2 y = e4m3_f16(u == 0 ? k1.x : u == 1 ? k1.y : u == 2 ? k1.z : k1.w);
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) mma16816(s[n][q], x.x, y.x, x.y, y.y, b[q][0], b[q][1]);
                 }
             }
         }
-        float aa[4 * NC], bb[4 * NC], ii[4 * NC];
+        float aa[NC][2], bb[NC][2], ii[NC][2];
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
             const float vs = slots.scale[sl][n][1];
-            aa[n] = slots.scale[sl][n][0];
-            bb[n] = __log2f(vs);
-            ii[n] = __frcp_rn(vs);
+            aa[n][0] = aa[n][1] = slots.scale[sl][n][0];
+            bb[n][0] = bb[n][1] = __log2f(vs);
+            ii[n][0] = ii[n][1] = __frcp_rn(vs);
         }
-        const uint32_t none[2] = {};
-        uint32_t p[NC][4];
-        softmax<2 * NC, false>(s, rq, aa, bb, ii, none, p);
+        const uint32_t none[NQ][2] = {};
+        uint32_t p[NC][NQ][2];
+        softmax<NC, false>(s, rq, aa, bb, ii, none, p);
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
             uint32_t v[4][VW];
@@ -1578,13 +1606,13 @@ struct MmWarp {
                 for (int h = 0; h < 2; ++h) {             // bytes 2h, 2h + 1 of word u, of two keys side by side
                     const uint2 x = e4m3_f16(__byte_perm(v[0][u], v[1][u], h ? 0x7362 : 0x5140));
                     const uint2 y = e4m3_f16(__byte_perm(v[2][u], v[3][u], h ? 0x7362 : 0x5140));
-                    mma16816(o[4 * u + 2 * h], p[n][0], p[n][1], p[n][2], p[n][3], x.x, y.x);
-                    mma16816(o[4 * u + 2 * h + 1], p[n][0], p[n][1], p[n][2], p[n][3], x.y, y.y);
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) mma16816(o[q][2 * u + h], x.x, x.y, y.x, y.y, p[n][q][0], p[n][q][1]);
                 }
         }
     }
     // 16 keys of the tail, from bf16 rows.  bad_v: the item's keys whose value is not finite.
-    __device__ __forceinline__ void tail(int tok, const Seg& sg, const uint4* qf, const float (&rq)[2], uint32_t* bad_v) {
+    __device__ __forceinline__ void tail(int tok, const Seg& sg, const uint32_t* qf, const float (&rq)[NQ][2], uint32_t* bad_v) {
         const Seq& q = sg.q;
         const int64_t ring = ((int64_t)q.slot * P.Hkv + sg.h) * 2 * P.page;
         auto row = [&](int e, int which) -> const char* {                // a place that is there for every row
@@ -1595,7 +1623,7 @@ struct MmWarp {
             return e < q.open + P.N ? p : P.q.p;
         };
         const int keys = q.open + P.N;
-        float s[2][4] = {}, ka[2];
+        float s[1][NQ][4] = {}, aa[1][2], bb[1][2], ii[1][2], ks[2];
         uint32_t kw[2][KH * 8];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -1616,16 +1644,19 @@ struct MmWarp {
             mx = max(mx, __shfl_xor_sync(FULL, mx, 1));
             mx = max(mx, __shfl_xor_sync(FULL, mx, 2));
             const int e = bits_exp(mx);
-            ka[i] = exp2i(e);
-#pragma unroll
-            for (int u = 0; u < KH * 4; ++u) {
-                const uint4 a = qf[u * 32 + lane];
-                mma16816(s[i], a.x, a.y, a.z, a.w, bf16_f16(kw[i][2 * u], exp2i(-e)), bf16_f16(kw[i][2 * u + 1], exp2i(-e)));
-            }
+            aa[0][i] = exp2i(e);
+            ks[i] = exp2i(-e);
         }
-        float aa[4], bb[4], ii[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) aa[j] = __shfl_sync(FULL, ka[j >> 1], (2 * c + (j & 1)) * 4);
+        for (int u = 0; u < KH * 4; ++u) {
+            uint32_t b[NQ][2];
+            columns(qf, u, lane, b);
+#pragma unroll
+            for (int q = 0; q < NQ; ++q)
+                mma16816(s[0][q], bf16_f16(kw[0][2 * u], ks[0]), bf16_f16(kw[1][2 * u], ks[1]), bf16_f16(kw[0][2 * u + 1], ks[0]),
+                         bf16_f16(kw[1][2 * u + 1], ks[1]), b[q][0], b[q][1]);
+        }
+        int vx[4];                                        // exponents of keys 2c, 2c + 1, 2c + 8, 2c + 9
         uint32_t vw[4][VW * 2];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -1642,128 +1673,146 @@ struct MmWarp {
 #pragma unroll
             for (int d = 4; d < 32; d *= 2) mx = max(mx, __shfl_xor_sync(FULL, mx, d));
             const int ex = bits_exp(mx);
-            bb[j] = (float)ex;
-            ii[j] = exp2i(-ex);
+            vx[j] = ex;
 #pragma unroll
             for (int u = 0; u < VW * 2; ++u) vw[j][u] = bf16_f16(vw[j][u], exp2i(-ex));
         }
-        uint32_t mask[2], p[1][4];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int n = min(g + 8 * r, P.R - 1) / P.G;
-            mask[r] = tail_bits(P, sg.b, n, q.open, tok) & 0xffffu;
+        for (int i = 0; i < 2; ++i) {                     // of keys g and g + 8
+            const int even = __shfl_sync(FULL, vx[2 * i], g >> 1), odd = __shfl_sync(FULL, vx[2 * i + 1], g >> 1);
+            const int ex = g & 1 ? odd : even;
+            bb[0][i] = (float)ex;
+            ii[0][i] = exp2i(-ex);
         }
-        softmax<2, true>(s, rq, aa, bb, ii, mask, p);
+        uint32_t mask[NQ][2], p[1][NQ][2];
 #pragma unroll
-        for (int u = 0; u < VW * 2; ++u)
+        for (int q = 0; q < NQ; ++q)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                mma16816(o[2 * u + h], p[0][0], p[0][1], p[0][2], p[0][3], __byte_perm(vw[0][u], vw[1][u], h ? 0x7632 : 0x5410),
-                         __byte_perm(vw[2][u], vw[3][u], h ? 0x7632 : 0x5410));
+            for (int e = 0; e < 2; ++e) mask[q][e] = tail_bits(P, sg.b, min(8 * q + 2 * c + e, P.R - 1) / P.G, sg.q.open, tok) & 0xffffu;
+        softmax<1, true>(s, rq, aa, bb, ii, mask, p);
+#pragma unroll
+        for (int u = 0; u < VW * 2; ++u) {
+            uint32_t x[2], y[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                x[h] = __byte_perm(vw[0][u], vw[1][u], h ? 0x7632 : 0x5410);
+                y[h] = __byte_perm(vw[2][u], vw[3][u], h ? 0x7632 : 0x5410);
+            }
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) mma16816(o[q][u], x[0], x[1], y[0], y[1], p[0][q][0], p[0][q][1]);
+        }
     }
-    // The item's queries as fragments, and the factors of rows g and g + 8.
-    __device__ __forceinline__ void load_q(const Seg& sg, uint4* qf, float (&rq)[2]) {
-        uint32_t w[2][KH * 8];
+    // The item's queries as fragments, and the factors of this lane's columns.
+    __device__ __forceinline__ void load_q(const Seg& sg, uint32_t* qf, float (&rq)[NQ][2]) {
+        uint32_t w[NQ][KH * 8];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = min(g + 8 * r, P.R - 1), n = row / P.G;
+        for (int q = 0; q < NQ; ++q) {
+            const int row = min(g + 8 * q, P.R - 1), n = row / P.G;
             const char* p = P.q.p + sg.b * P.q.b + n * P.q.n + (sg.h * P.G + row - n * P.G) * P.q.h + c * (D / 2);
 #pragma unroll
             for (int j = 0; j < KH; ++j)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const uint4 v = *reinterpret_cast<const uint4*>(p + 32 * j + 16 * u);
-                    w[r][8 * j + 4 * u] = v.x; w[r][8 * j + 4 * u + 1] = v.y;
-                    w[r][8 * j + 4 * u + 2] = v.z; w[r][8 * j + 4 * u + 3] = v.w;
+                    w[q][8 * j + 4 * u] = v.x; w[q][8 * j + 4 * u + 1] = v.y;
+                    w[q][8 * j + 4 * u + 2] = v.z; w[q][8 * j + 4 * u + 3] = v.w;
                 }
         }
-        float sc[2];
+        __syncwarp();
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int q = 0; q < NQ; ++q) {
             bool bad;
-            uint32_t mx = bf16_amax(w[r], bad, true);
+            uint32_t mx = bf16_amax(w[q], bad, true);
             mx = max(mx, __shfl_xor_sync(FULL, mx, 1));
             mx = max(mx, __shfl_xor_sync(FULL, mx, 2));
-            const int e = bits_exp(mx);
-            sc[r] = exp2i(-e);
-            rq[r] = exp2i(e) * P.scale;
+            const int ex = bits_exp(mx);                  // of query 8q + g
+            const float sc = exp2i(-ex);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) rq[q][e] = exp2i(__shfl_sync(FULL, ex, 4 * (2 * c + e))) * P.scale;
+#pragma unroll
+            for (int u = 0; u < KH * 4; ++u) {
+                qf[(u * 32 + lane) * 2 * NQ + 2 * q] = bf16_f16(w[q][2 * u], sc);
+                qf[(u * 32 + lane) * 2 * NQ + 2 * q + 1] = bf16_f16(w[q][2 * u + 1], sc);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) o[q][j][0] = o[q][j][1] = o[q][j][2] = o[q][j][3] = 0.f;
+            m[q][0] = m[q][1] = NEG_INF;
+            l[q][0] = l[q][1] = 0.f;
         }
         __syncwarp();
-#pragma unroll
-        for (int u = 0; u < KH * 4; ++u)
-            qf[u * 32 + lane] = make_uint4(bf16_f16(w[0][2 * u], sc[0]), bf16_f16(w[1][2 * u], sc[1]), bf16_f16(w[0][2 * u + 1], sc[0]),
-                                           bf16_f16(w[1][2 * u + 1], sc[1]));
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-        m[0] = m[1] = NEG_INF;
-        l[0] = l[1] = 0.f;
     }
 };
 
-template <int D> struct alignas(16) MmShared {
+template <int D, int NQ> struct alignas(16) MmShared {
     MmRing<D> ring[MM_WARPS];                             // 1024-byte aligned, as the swizzle wants
     MmSlots slots[MM_WARPS];
-    uint4 q[D / 16][32];                                  // the query fragments: every warp writes the same
+    alignas(16) uint32_t q[D / 16 * 32 * 2 * NQ];         // the query fragments: every warp writes the same
     float4 o[2][4][32];                                   // output fragments of two warps, four blocks at a time
-    float m[MM_WARPS][MM_ROWS], l[MM_WARPS][MM_ROWS];
+    float m[MM_WARPS][8 * NQ], l[MM_WARPS][8 * NQ];
     uint32_t bad_v[12];
     int bad, late;
     MmAhead now, ahead[MM_WARPS];                         // the segment being computed; of each warp's next chunk
 };
 
 // The end of a segment: the warps' results put together and written out, or left as a part.
-template <int D>
-__device__ __forceinline__ void mm_finish(const Att& P, MmWarp<D>& w, MmShared<D>& sh, bool bad) {
+template <int D, int NQ>
+__device__ __forceinline__ void mm_finish(const Att& P, MmWarp<D, NQ>& w, MmShared<D, NQ>& sh, bool bad) {
     const int tid = threadIdx.x;
     const Seg& g = sh.now.s;
-    constexpr int NT = D / 8;
+    constexpr int NT = D / 16;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        w.l[r] += __shfl_xor_sync(FULL, w.l[r], 1);
-        w.l[r] += __shfl_xor_sync(FULL, w.l[r], 2);
-        if (w.c == 0) {
-            sh.m[w.warp][w.g + 8 * r] = w.m[r];
-            sh.l[w.warp][w.g + 8 * r] = w.l[r];
+    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) w.l[q][e] += __shfl_xor_sync(FULL, w.l[q][e], d);
+            if (w.g == 0) {
+                sh.m[w.warp][8 * q + 2 * w.c + e] = w.m[q][e];
+                sh.l[w.warp][8 * q + 2 * w.c + e] = w.l[q][e];
+            }
         }
-    }
     if (bad) sh.bad = 1;
     __syncthreads();
     // every warp's output on the common maximum, then warps 2 and 3 to 0 and 1, and 1 to 0
-    float mm[2], l[2], f[2];
+    float mm[NQ][2], l[NQ][2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int row = w.g + 8 * r;
-        mm[r] = fmaxf(fmaxf(sh.m[0][row], sh.m[1][row]), fmaxf(sh.m[2][row], sh.m[3][row]));
-        const float base = mm[r] == NEG_INF ? 0.f : mm[r];
-        f[r] = ex2(w.m[r] - base);
-        l[r] = 0.f;
+    for (int q = 0; q < NQ; ++q)
 #pragma unroll
-        for (int i = 0; i < MM_WARPS; ++i) l[r] = fmaf(ex2(sh.m[i][row] - base), sh.l[i][row], l[r]);
-    }
+        for (int e = 0; e < 2; ++e) {
+            const int row = 8 * q + 2 * w.c + e;
+            mm[q][e] = fmaxf(fmaxf(sh.m[0][row], sh.m[1][row]), fmaxf(sh.m[2][row], sh.m[3][row]));
+            const float base = mm[q][e] == NEG_INF ? 0.f : mm[q][e], f = ex2(w.m[q][e] - base);
+            l[q][e] = 0.f;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        w.o[j][0] *= f[0]; w.o[j][1] *= f[0]; w.o[j][2] *= f[1]; w.o[j][3] *= f[1];
-    }
+            for (int i = 0; i < MM_WARPS; ++i) l[q][e] = fmaf(ex2(sh.m[i][row] - base), sh.l[i][row], l[q][e]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                w.o[q][j][e] *= f;
+                w.o[q][j][2 + e] *= f;
+            }
+        }
 #pragma unroll
     for (int half = 2; half >= 1; half /= 2)
 #pragma unroll
-        for (int j0 = 0; j0 < NT; j0 += 4) {
-            if (w.warp >= half && w.warp < 2 * half) {
+        for (int q = 0; q < NQ; ++q)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    sh.o[w.warp - half][j][w.lane] = make_float4(w.o[j0 + j][0], w.o[j0 + j][1], w.o[j0 + j][2], w.o[j0 + j][3]);
-            }
-            __syncthreads();
-            if (w.warp < half) {
+            for (int j0 = 0; j0 < NT; j0 += 4) {
+                if (w.warp >= half && w.warp < 2 * half) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 x = sh.o[w.warp][j][w.lane];
-                    w.o[j0 + j][0] += x.x; w.o[j0 + j][1] += x.y; w.o[j0 + j][2] += x.z; w.o[j0 + j][3] += x.w;
+                    for (int j = 0; j < 4; ++j)
+                        sh.o[w.warp - half][j][w.lane] =
+                            make_float4(w.o[q][j0 + j][0], w.o[q][j0 + j][1], w.o[q][j0 + j][2], w.o[q][j0 + j][3]);
                 }
+                __syncthreads();
+                if (w.warp < half) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 x = sh.o[w.warp][j][w.lane];
+                        w.o[q][j0 + j][0] += x.x; w.o[q][j0 + j][1] += x.y; w.o[q][j0 + j][2] += x.z; w.o[q][j0 + j][3] += x.w;
+                    }
+                }
+                __syncthreads();
             }
-            __syncthreads();
-        }
     const bool whole = g.whole();
     const bool nan = g.q.bad || sh.bad;
     const float quiet = __int_as_float(0x7fffffff);
@@ -1773,54 +1822,52 @@ __device__ __forceinline__ void mm_finish(const Att& P, MmWarp<D>& w, MmShared<D
         if (g.t1 > g.q.nct)
             for (int i = 0; i < 12; ++i) any_bad |= sh.bad_v[i];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = w.g + 8 * r, n = row / P.G;
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int row = 8 * q + 2 * w.c + e, n = row / P.G;
             if (row >= P.R) continue;
-            // this lane's dims: blocks of D / 8 from 2c and 2c + 1 on
+            float x[2 * NT];                              // dims from g D / 8 on
+#pragma unroll
+            for (int j = 0; j < 2 * NT; ++j) x[j] = w.o[q][j >> 1][2 * (j & 1) + e];
             if (any_bad) {                                // values that could not enter the product
                 for (int i = 0; i < 12; ++i) {
                     uint32_t hit = sh.bad_v[i];
                     if (hit) hit &= tail_bits(P, g.b, n, g.q.open, 32 * i);
                     for (; hit; hit &= hit - 1) {
-                        const int e = 32 * i + __ffs(hit) - 1;
-                        const char* src = e < g.q.open
+                        const int k = 32 * i + __ffs(hit) - 1;
+                        const char* src = k < g.q.open
                             ? static_cast<const char*>(P.c.v_open) +
-                                  (((int64_t)g.q.slot * P.Hkv + g.h) * 2 * P.page + (g.q.full + e) % (2 * P.page)) * D * 2
-                            : P.v.p + g.b * P.v.b + (e - g.q.open) * P.v.n + g.h * P.v.h;
-                        const __nv_bfloat16* vv = reinterpret_cast<const __nv_bfloat16*>(src) + 2 * w.c * NT;
+                                  (((int64_t)g.q.slot * P.Hkv + g.h) * 2 * P.page + (g.q.full + k) % (2 * P.page)) * D * 2
+                            : P.v.p + g.b * P.v.b + (k - g.q.open) * P.v.n + g.h * P.v.h;
+                        const __nv_bfloat16* vv = reinterpret_cast<const __nv_bfloat16*>(src) + 2 * w.g * NT;
 #pragma unroll
                         for (int j = 0; j < 2 * NT; ++j) {
                             const float y = __bfloat162float(vv[j]);
-                            if (!(fabsf(y) <= 3.402823466e38f)) w.o[j % NT][2 * r + j / NT] += y;
+                            if (!(fabsf(y) <= 3.402823466e38f)) x[j] += y;
                         }
                     }
                 }
             }
             const int64_t at = ((int64_t)g.b * P.N + n) * P.Hq + g.h * P.G + row - n * P.G;
-            const float inv = nan ? quiet : l[r] == 0.f ? 0.f : 1.f / l[r];
+            const float m = mm[q][e], sum = l[q][e], inv = nan ? quiet : sum == 0.f ? 0.f : 1.f / sum;
             if (whole) {
-                char* dst = P.out + (at * D + 2 * w.c * NT) * 2;
+                char* dst = P.out + (at * D + 2 * w.g * NT) * 2;
 #pragma unroll
-                for (int j = 0; j < 2 * NT; j += 8) {
-                    float x[8];
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) x[u] = w.o[(j + u) % NT][2 * r + (j + u) / NT] * inv;
+                for (int j = 0; j < 2 * NT; j += 8)
                     *reinterpret_cast<uint4*>(dst + 2 * j) =
-                        make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-                }
-                if (w.c == 0 && P.lse) P.lse[at] = nan ? quiet : l[r] == 0.f ? NEG_INF : (mm[r] - P_BIAS + log2f(l[r])) * LN2;
+                        make_uint4(pack_bf16(x[j] * inv, x[j + 1] * inv), pack_bf16(x[j + 2] * inv, x[j + 3] * inv),
+                                   pack_bf16(x[j + 4] * inv, x[j + 5] * inv), pack_bf16(x[j + 6] * inv, x[j + 7] * inv));
+                if (w.g == 0 && P.lse) P.lse[at] = nan ? quiet : sum == 0.f ? NEG_INF : (m - P_BIAS + log2f(sum)) * LN2;
             } else {
-                float* dst = part + (int64_t)row * D + 2 * w.c * NT;
+                float* dst = part + (int64_t)row * D + 2 * w.g * NT;
 #pragma unroll
-                for (int j = 0; j < 2 * NT; j += 4) {
-                    float x[4];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) x[u] = nan ? quiet : w.o[(j + u) % NT][2 * r + (j + u) / NT];
-                    *reinterpret_cast<float4*>(dst + j) = make_float4(x[0], x[1], x[2], x[3]);
-                }
-                if (w.c == 0) {
-                    part[(int64_t)P.R * D + row] = mm[r] == NEG_INF ? NEG_INF : mm[r] - P_BIAS;
-                    part[(int64_t)P.R * D + P.R + row] = nan ? quiet : l[r];
+                for (int j = 0; j < 2 * NT; j += 4)
+                    *reinterpret_cast<float4*>(dst + j) =
+                        nan ? make_float4(quiet, quiet, quiet, quiet) : make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+                if (w.g == 0) {
+                    part[(int64_t)P.R * D + row] = m == NEG_INF ? NEG_INF : m - P_BIAS;
+                    part[(int64_t)P.R * D + P.R + row] = nan ? quiet : sum;
                 }
             }
         }
@@ -1836,11 +1883,11 @@ __device__ __forceinline__ void mm_finish(const Att& P, MmWarp<D>& w, MmShared<D
     __syncthreads();
 }
 
-template <int D>
+template <int D, int NQ>
 __global__ void __launch_bounds__(MM_BT, MM_CTAS_SM) k_attention_mma(const Att P, const __grid_constant__ CUtensorMap kmap,
                                                                      const __grid_constant__ CUtensorMap vmap) {
     extern __shared__ unsigned char mm_smem[];
-    MmShared<D>& sh = *reinterpret_cast<MmShared<D>*>(mm_smem + (-smem_u32(mm_smem) & 1023u));
+    MmShared<D, NQ>& sh = *reinterpret_cast<MmShared<D, NQ>*>(mm_smem + (-smem_u32(mm_smem) & 1023u));
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Stretch st = find_stretch<MM_BT>(P);
     if (threadIdx.x == 0) P.cut[blockIdx.x].parts = 0;
@@ -1857,13 +1904,12 @@ __global__ void __launch_bounds__(MM_BT, MM_CTAS_SM) k_attention_mma(const Att P
         proxy_fence();
     }
     __syncthreads();
-    using W = MmWarp<D>;
-    W w(P, threadIdx.x >> 5, sh.ahead[threadIdx.x >> 5]);
+    MmWarp<D, NQ> w(P, threadIdx.x >> 5, sh.ahead[threadIdx.x >> 5]);
     MmRing<D>& ring = sh.ring[w.warp];
     MmSlots& slots = sh.slots[w.warp];
     w.begin(st);
-    uint4* qf = &sh.q[0][0];
-    float rq[2];
+    uint32_t* qf = sh.q;
+    float rq[NQ][2];
     int id, idy, parity = -1;
     // part x is computed, y's bytes are on their way, and the page ids of the part after
     Part x = w.next(id);
@@ -1902,7 +1948,7 @@ __global__ void __launch_bounds__(MM_BT, MM_CTAS_SM) k_attention_mma(const Att P
             }
         }
         if (y.kind() == 0 || y.parity() != x.parity()) {
-            mm_finish<D>(P, w, sh, bad);
+            mm_finish<D, NQ>(P, w, sh, bad);
             bad = false;
         }
         x = y;
@@ -1918,13 +1964,10 @@ using sv_host::fail;
 
 namespace {
 
-#ifndef TC_OVER_N
-#define TC_OVER_N 4
-#endif
-#ifndef MM_OVER_N
-#define MM_OVER_N 2
-#endif
-constexpr int TC_OVER = TC_OVER_N, MM_OVER = MM_OVER_N;
+// What an item costs on the line of work beside its tiles, in tiles (its start, its end, its cut).  64 chains of 6 over ragged
+// lengths up to 4096 took 313, 265, 268 us at 0, 4, 8; 32 trees of 64 over 8192: 753, 622, 635; 64 single tokens over 8192:
+// 121, 117, 121 at 2, 4, 6.
+constexpr int OVER = 4;
 constexpr int TC_CTAS = 148, MM_CTAS = MM_CTAS_SM * 148;      // CTAs at most
 
 template <int D>
@@ -1972,7 +2015,7 @@ spec_status page_map(const Att& P, void* pages, int rows, CUtensorMap* map) {
 template <int D>
 spec_status launch_tc(Att P, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
-    P.over = TC_OVER;
+    P.over = OVER;
     if (const spec_status s = sv_host::allow_smem(reinterpret_cast<const void*>(k_attention_tc<D>), "k_attention_tc", tc_smem<D>(), done)) return s;
     const int ctas = sv_host::num_sms() < TC_CTAS ? sv_host::num_sms() : TC_CTAS;
     CUtensorMap kmap;
@@ -1982,19 +2025,25 @@ spec_status launch_tc(Att P, cudaStream_t st) {
     return s == SPEC_OK ? launch_merge<D>(P, ctas, st) : s;
 }
 
-template <int D>
+template <int D, int NQ>
 spec_status launch_mma(Att P, cudaStream_t st) {
-    const size_t smem = sizeof(MmShared<D>) + 1024;
+    const size_t smem = sizeof(MmShared<D, NQ>) + 1024;
     static std::atomic<uint64_t> done{0};
-    P.over = MM_OVER;
-    if (const spec_status s = sv_host::allow_smem(reinterpret_cast<const void*>(k_attention_mma<D>), "k_attention_mma", smem, done)) return s;
+    P.over = OVER;
+    if (const spec_status s = sv_host::allow_smem(reinterpret_cast<const void*>(k_attention_mma<D, NQ>), "k_attention_mma", smem, done)) return s;
     CUtensorMap kmap, vmap;
     if (const spec_status s = page_map<D>(P, P.c.k_pages, 16, &kmap)) return s;
     if (const spec_status s = page_map<D>(P, P.c.v_pages, 16, &vmap)) return s;
     const int want = MM_CTAS_SM * sv_host::num_sms(), ctas = want < MM_CTAS ? want : MM_CTAS;
-    k_attention_mma<D><<<ctas, MM_BT, smem, st>>>(P, kmap, vmap);
+    k_attention_mma<D, NQ><<<ctas, MM_BT, smem, st>>>(P, kmap, vmap);
     const spec_status s = sv_host::launched("k_attention_mma");
     return s == SPEC_OK ? launch_merge<D>(P, ctas, st) : s;
+}
+
+template <int D>
+spec_status launch(const Att& P, cudaStream_t st) {
+    if (P.R > MM_ROWS) return launch_tc<D>(P, st);
+    return P.R > 8 ? launch_mma<D, 2>(P, st) : launch_mma<D, 1>(P, st);
 }
 
 }  // namespace
@@ -2051,8 +2100,7 @@ spec_status spec_tree_attention(int B, int N, int q_heads, const spec_kv_cache* 
     P.cut = reinterpret_cast<Cut*>(ws + sv_host::CACHE_WS_CUT);
     P.partial = reinterpret_cast<float*>(ws + sv_host::CACHE_WS_PARTIAL);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (P.R > MM_ROWS) return D == 64 ? launch_tc<64>(P, st) : launch_tc<128>(P, st);
-    return D == 64 ? launch_mma<64>(P, st) : launch_mma<128>(P, st);
+    return D == 64 ? launch<64>(P, st) : launch<128>(P, st);
 }
 
 }  // extern "C"
