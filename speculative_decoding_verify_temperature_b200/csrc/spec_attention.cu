@@ -152,36 +152,36 @@ struct Seg {
 
 struct SegIter {
     Stretch s;
-    long long at, b_lo;
-    int b;
+    long long at, item_lo;
+    int b, item;
     Seq q;
     __device__ __forceinline__ void begin(const Att& P, const Stretch& st) {
         s = st;
         at = st.lo;
         b = st.b;
-        b_lo = st.b_lo;
-        if (at < s.hi) q = seq_of(P, b);
+        if (at < s.hi) {
+            q = seq_of(P, b);
+            item = (int)((at - st.b_lo) / (q.ntiles + P.over));
+            item_lo = st.b_lo + (long long)item * (q.ntiles + P.over);
+        }
     }
     __device__ __forceinline__ bool next(const Att& P, Seg& g) {
-        const int items = P.Hkv * P.mtiles;
         while (at < s.hi) {
-            while (at >= b_lo + (long long)(q.ntiles + P.over) * items) {
-                b_lo += (long long)(q.ntiles + P.over) * items;
+            if (item == P.Hkv * P.mtiles) {
+                item = 0;
                 q = seq_of(P, ++b);
             }
             const int units = q.ntiles + P.over;
-            const int item = (int)((at - b_lo) / units);
             g.q = q;
             g.b = b;
             g.h = item / P.mtiles;
             g.mt = item - g.h * P.mtiles;
-            g.item_lo = b_lo + (long long)item * units;
-            g.t0 = max((int)(at - g.item_lo) - P.over, 0);
-            g.t1 = (int)min((long long)units, s.hi - g.item_lo) - P.over;
-            at = g.item_lo + P.over + max(g.t1, 0);
-            if (g.t1 > g.t0) return true;
-            if (at < s.hi) continue;
-            return false;                 // the stretch ends before the item's first tile
+            g.item_lo = item_lo;
+            g.t0 = max((int)(at - item_lo) - P.over, 0);
+            g.t1 = (int)min((long long)units, s.hi - item_lo) - P.over;
+            ++item;
+            at = item_lo += units;
+            if (g.t1 > g.t0) return true;                 // else the stretch ends before the item's first tile
         }
         return false;
     }
@@ -436,6 +436,14 @@ __device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t (&r)[32]) {
                    "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
                  : "r"(a));
 }
+__device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+                 "%14, %15};"
+                 :: "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                    "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(a)
+                 : "memory");
+}
+
 // Sixteen columns, waited for.
 __device__ __forceinline__ void tc_ld16(uint32_t a, uint32_t (&r)[16]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -444,12 +452,23 @@ __device__ __forceinline__ void tc_ld16(uint32_t a, uint32_t (&r)[16]) {
                    "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
                  : "r"(a) : "memory");
 }
-__device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t (&r)[16]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-                 "%14, %15};"
-                 :: "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-                    "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(a)
-                 : "memory");
+// Eight columns, waited for.
+__device__ __forceinline__ void tc_ld8(uint32_t a, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(a) : "memory");
+}
+__device__ __forceinline__ void tc_ld4(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void tc_st8(uint32_t a, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};"
+                 :: "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(a) : "memory");
+}
+__device__ __forceinline__ void tc_st4(uint32_t a, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%4], {%0, %1, %2, %3};"
+                 :: "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(a) : "memory");
 }
 
 // Shared-memory operand descriptor: rows of ROW bytes swizzled over ROW bytes (128
@@ -621,6 +640,29 @@ __device__ __forceinline__ void tc_scales(const Att& P, TcShared& sh, const Stre
     }
 }
 
+// Largest finite magnitude of bf16 words, as bits; elements that are not finite become 0 or (keep_nan) NaN.
+template <int N>
+__device__ __forceinline__ uint32_t bf16_amax(uint32_t (&w)[N], bool& bad, bool keep_nan) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+    m = max(m & 0xffffu, m >> 16);
+    bad = m >= 0x7f80u;
+    if (bad) {
+        m = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int s = 0; s < 32; s += 16) {
+                const uint32_t a = (w[i] >> s) & 0x7fffu;
+                if (a >= 0x7f80u) w[i] = (w[i] & ~(0xffffu << s)) | (keep_nan ? 0x7fffu << s : 0u);
+                else m = max(m, a);
+            }
+    }
+    return m;
+}
+__device__ __forceinline__ int bits_exp(uint32_t m) { return m ? max(min((int)(m >> 7), 253), 1) - 127 : 0; }
+
 // The warps that make operands.
 template <int D>
 struct TcConv {
@@ -708,39 +750,52 @@ struct TcConv {
         hi = make_uint2(a[0] | a[1] << 16, a[2] | a[3] << 16);
         lo = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
     }
-    // Rows are loaded two passes ahead of their use, in a loop that stays small: this code runs once per item, and
-    // unrolled it cost more in instruction fetches (30000 cycles a tail tile) than all it computes.
-    __device__ __forceinline__ void load_q(const Seg& g, int rows, int p, Vec8<SPEC_BF16>& w) {
-        const int r = min(tid / LPR + p * RP, rows - 1);  // rows behind the last repeat it
+    // The item's queries: QL lanes to a row, each with four (D = 64: two) pieces of 16 bytes, the next pass's on their way.
+    // A loop that stays small: its code runs once per item and is never in the instruction caches.  (16 lanes to a row
+    // and a piece each: 1100 cycles for 16 rows, nearly all of it waiting for shuffles.)
+    static constexpr int QV = D / 32, QP = TC_CONV / 4;
+    __device__ __forceinline__ void load_q(const Seg& g, int rows, int p, Vec8<SPEC_BF16> (&w)[QV]) {
+        const int r = min(tid / 4 + p * QP, rows - 1);    // rows behind the last repeat it
         const int row = g.mt * 256 + r, n = row / P.G, h = g.h * P.G + row - n * P.G;
-        w.load_plain(P.q.p + g.b * P.q.b + n * P.q.n + h * P.q.h + 16 * (tid % LPR));
+        const char* src = P.q.p + g.b * P.q.b + n * P.q.n + h * P.q.h + 16 * (tid % 4);
+#pragma unroll
+        for (int i = 0; i < QV; ++i) w[i].load_plain(src + 64 * i);
     }
-    __device__ __forceinline__ void put_q_row(Vec8<SPEC_BF16> w, int p, float* rq) {
-        const int l = tid % LPR, r = tid / LPR + p * RP;
+    __device__ __forceinline__ void put_q_rows(Vec8<SPEC_BF16> (&w)[QV], int p, float* rq) {
+        const int r = tid / 4 + p * QP;
+        uint32_t all[QV * 4];
+#pragma unroll
+        for (int i = 0; i < QV * 4; ++i) all[i] = (&w[i / 4].a.x)[i % 4];
         bool bad;
-        const int e = scale_row(w.a, bad, true);
-        uint2 hi, lo;
-        split_row(w.a, e, hi, lo);
+        uint32_t mx = bf16_amax(all, bad, true);
+        mx = max(mx, __shfl_xor_sync(FULL, mx, 1));
+        mx = max(mx, __shfl_xor_sync(FULL, mx, 2));
+        const int e = mx ? max((int)(mx >> 7), 7) - 127 : 0;  // -120 to 127
         const uint32_t dst = base + Tc<D>::Q + (r / 128) * Tc<D>::Q_B;
-        // D = 128: two tiles of 128-byte rows; 64: side by side
-        sts64(swz(dst, r % 128, l / 2) + (l & 1) * 8, hi);
-        sts64((D == 128 ? swz(dst + Tc<D>::RAW_B, r % 128, l / 2) : swz(dst, r % 128, 4 + l / 2)) + (l & 1) * 8, lo);
-        if (l == 0) rq[r] = exp2i(e) * (P.scale * 0.0078125f);
+#pragma unroll
+        for (int i = 0; i < QV; ++i) {
+            const int l = tid % 4 + 4 * i;                // piece of the row
+            uint2 hi, lo;
+            split_row(make_uint4(all[4 * i], all[4 * i + 1], all[4 * i + 2], all[4 * i + 3]), e, hi, lo);
+            // D = 128: two tiles of 128-byte rows; 64: side by side
+            sts64(swz(dst, r % 128, l / 2) + (l & 1) * 8, hi);
+            sts64((D == 128 ? swz(dst + Tc<D>::RAW_B, r % 128, l / 2) : swz(dst, r % 128, 4 + l / 2)) + (l & 1) * 8, lo);
+        }
+        if (tid % 4 == 0) rq[r] = exp2i(e) * (P.scale * 0.0078125f);
     }
     __device__ __forceinline__ void put_q(const Seg& g, int seg) {
         // the rows behind the last are whatever they are: their results are not looked at
-        const int rows = min(256, P.R - g.mt * 256), np = (rows + 2 * RP - 1) / (2 * RP) * 2;
+        const int rows = min(256, P.R - g.mt * 256), np = (rows + QP - 1) / QP;
         float* rq = sh.rq[seg & 3];
-        Vec8<SPEC_BF16> a, b;
-        load_q(g, rows, 0, a);
-        load_q(g, rows, 1, b);
+        Vec8<SPEC_BF16> w[QV];
+        load_q(g, rows, 0, w);
 #pragma unroll 1
-        for (int p = 0; p < np; p += 2) {
-            const Vec8<SPEC_BF16> a0 = a, b0 = b;
-            load_q(g, rows, p + 2, a);                    // behind the last pass: the last row again
-            load_q(g, rows, p + 3, b);
-            put_q_row(a0, p, rq);
-            put_q_row(b0, p + 1, rq);
+        for (int p = 0; p < np; ++p) {
+            Vec8<SPEC_BF16> x[QV];
+#pragma unroll
+            for (int i = 0; i < QV; ++i) x[i] = w[i];
+            load_q(g, rows, p + 1, w);                    // behind the last pass: the last row again
+            put_q_rows(x, p, rq);
         }
     }
     // Row e of the tail: open tokens from the ring, then the nodes.  One load for every row, from a place that is
@@ -788,9 +843,7 @@ struct TcConv {
         constexpr int KR = Tc<D>::KR;
         const int m = u.gt & (TC_META - 1);
         const int k0 = nk % KR, k1 = (nk + 1) % KR;
-        Vec8<SPEC_BF16> ka, va, kb, vb;
-        load_tail(u, 0, ka, va);
-        load_tail(u, 1, kb, vb);
+        Vec8<SPEC_BF16> ka{}, va{}, kb{}, vb{};
         bar_wait(&sh.me[m], ((u.gt / TC_META) & 1) ^ 1, sh);
         bar_wait(&sh.ke[k0], ((nk / KR) & 1) ^ 1, sh);
         bar_wait(&sh.ke[k1], (((nk + 1) / KR) & 1) ^ 1, sh);
@@ -800,17 +853,17 @@ struct TcConv {
         float* meta = sh.meta[m][0];
         // rows behind the last key: their scores are masked, their values have to be finite
         const int keys = u.g.q.len >= 0 && !u.g.q.bad ? min(TILE, u.g.q.open + P.N - (u.t - u.g.q.nct) * TILE) : 0;
-        const int np = (keys + 2 * RP - 1) / (2 * RP) * 2;
+        const int np = (keys + RP - 1) / RP;
         for (int i = np * RP * (D / 8) + tid; i < TILE * (D / 8); i += TC_CONV)
             sts128(swz(vd + (i % (D / 8) / 8) * Tc<D>::HALF, i / (D / 8), i % 8), make_uint4(0, 0, 0, 0));
         for (int r = np * RP + tid; r < TILE; r += TC_CONV) meta[r] = meta[TILE + r] = meta[2 * TILE + r] = 1.f;
 #pragma unroll 1
-        for (int p = 0; p < np; p += 2) {
-            const Vec8<SPEC_BF16> k2 = ka, v2 = va, k3 = kb, v3 = vb;
-            load_tail(u, p + 2, ka, va);
-            load_tail(u, p + 3, kb, vb);
-            put_tail_row(u, k2, v2, p, khi, klo, vd, meta);
-            put_tail_row(u, k3, v3, p + 1, khi, klo, vd, meta);
+        for (int p = -2; p < np; ++p) {
+            const Vec8<SPEC_BF16> k = ka, v = va;
+            ka = kb;
+            va = vb;
+            load_tail(u, p + 2, kb, vb);
+            if (p >= 0) put_tail_row(u, k, v, p, khi, klo, vd, meta);
         }
         proxy_fence();
         asm volatile("bar.sync 2, %0;" :: "n"(TC_CONV) : "memory");
@@ -857,20 +910,13 @@ struct TcConv {
     }
 };
 
-// A row's bits of a tile's keys, 32 per word.
-__device__ __forceinline__ void tile_mask(const Att& P, const Seg& g, int t, int n, uint32_t (&mk)[4]) {
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        if (t < g.q.nct) {
-            const int left = g.q.full - t * TILE - 32 * w;
-            mk[w] = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
-        } else {
-            mk[w] = g.q.len < 0 || g.q.bad ? 0u : tail_bits(P, g.b, n, g.q.open, (t - g.q.nct) * TILE + 32 * w);
-        }
-    }
+// A row's bits of 32 of a tile's keys.
+__device__ __forceinline__ uint32_t tile_mask(const Att& P, const Seg& g, int t, int n, int w) {
+    if (t >= g.q.nct) return g.q.len < 0 || g.q.bad ? 0u : tail_bits(P, g.b, n, g.q.open, (t - g.q.nct) * TILE + 32 * w);
+    const int left = g.q.full - t * TILE - 32 * w;
+    return left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
 }
 
-// MODE 0: cached tile, all keys; 1: cached tile, masked; 2: tail (masked, scales per key).
 // The column loops stay rolled: unrolled (and with the scores of 32 columns loaded ahead) the code no longer fits the
 // instruction caches beside that of the other roles, and a round of 64-node trees took 800 us instead of 630.
 __device__ __forceinline__ float group_max(const uint32_t (&r)[32], int u) {
@@ -896,85 +942,95 @@ __device__ __forceinline__ float group_probs(const uint32_t (&r)[32], int u, flo
     }
     return gs.x + gs.y;
 }
-// A row's running maximum grows to `m2` after `c` of the tile's four groups of 32 keys: what has been summed so far (O, and
-// the P of these groups) is brought to it.  Seldom taken once the first tiles are through.
+// A row's running maximum grows after `cols` of the tile's P have been written, four columns at a time: what has been summed so
+// far (O, and these P) is brought to it.  Seldom taken once the first tiles are through.
 template <int D>
-__device__ __forceinline__ void rescale(uint32_t s_col, uint32_t o_col, int c, bool has_o, float f) {
+__device__ __noinline__ void rescale(uint32_t s_col, uint32_t o_col, int cols, bool has_o, float f) {
     tc_wait_st();                        // the P that are read back
 #pragma unroll 1
-    for (int i = 0; i < c; ++i) {
-        uint32_t p[16];
-        tc_ld16(s_col + 16 * i, p);
+    for (int i = 0; i < cols; i += 4) {
+        uint32_t p[4];
+        tc_ld4(s_col + i, p);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {   // in f32: f may be too small for f16 where P f is not
+        for (int j = 0; j < 4; ++j) {    // in f32: f may be too small for f16 where P f is not
             float x, y;
             asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(x), "=f"(y) : "r"(p[j]));
             p[j] = pack_f16(x * f, y * f);
         }
-        tc_st16(s_col + 16 * i, p);
+        tc_st4(s_col + i, p);
     }
     if (!has_o) return;
 #pragma unroll 1
-    for (int i = 0; i < D; i += 16) {
-        uint32_t o[16];
-        tc_ld16(o_col + i, o);
+    for (int i = 0; i < D; i += 8) {
+        uint32_t o[8];
+        tc_ld8(o_col + i, o);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-        tc_st16(o_col + i, o);
+        for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+        tc_st8(o_col + i, o);
     }
 }
+template <int D>
+__device__ __forceinline__ void grow(uint32_t s_col, uint32_t o_col, int cols, bool has_o, float mx, float& m, float& l) {
+    if (!__any_sync(FULL, mx > m + M_SLACK)) return;
+    const float m2 = fmaxf(m, ceilf(mx)), f = m2 == NEG_INF ? 1.f : ex2(m - m2);
+    m = m2;
+    l *= f;
+    if (cols > 0 || has_o) rescale<D>(s_col, o_col, cols, has_o, f);
+}
 
-// One pass over a tile's scores, 32 keys at a time: P = 2^(w - m + P_BIAS) in f16 over the scores, with m the largest w up
-// to M_SLACK ago.
-template <int D, int MODE>
-__device__ __forceinline__ void tile_softmax(uint32_t s_col, uint32_t o_col, const float* meta, float rq, const uint32_t (&mk)[4],
-                                             bool has_o, float& m, float& l) {
+// One pass over a tile's scores: P = 2^(w - m + P_BIAS) in f16 over the scores, with m the largest w up to M_SLACK ago.
+// A cached tile that has all of its keys, 32 at a time.
+template <int D>
+__device__ __forceinline__ void tile_softmax(uint32_t s_col, uint32_t o_col, const float* meta, float rq, bool has_o, float& m, float& l) {
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
         uint32_t r[32], p[16];
         tc_ld32(s_col + 32 * c, r);
         tc_wait_ld(r);
-        if (MODE > 0) {
-            const uint32_t bits = mk[c];
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (!((bits >> j) & 1)) r[j] = 0xff800000u;
-        }
         float mx = NEG_INF, a[2], b[2];
-        if (MODE < 2) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                a[u] = fmaxf(meta[2 * c + u] * rq, 1.2e-38f);
-                b[u] = meta[TILE + 2 * c + u];
-                mx = fmaxf(mx, fmaf(group_max(r, u), a[u], b[u]));
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                r[j] = __float_as_uint(fmaf(__uint_as_float(r[j]), fmaxf(meta[32 * c + j] * rq, 1.2e-38f), meta[TILE + 32 * c + j]));
-                mx = fmaxf(mx, __uint_as_float(r[j]));
-            }
+        for (int u = 0; u < 2; ++u) {
+            a[u] = fmaxf(meta[2 * c + u] * rq, 1.2e-38f);
+            b[u] = meta[TILE + 2 * c + u];
+            mx = fmaxf(mx, fmaf(group_max(r, u), a[u], b[u]));
         }
-        if (__any_sync(FULL, mx > m + M_SLACK)) {
-            const float m2 = fmaxf(m, ceilf(mx)), f = m2 == NEG_INF ? 1.f : ex2(m - m2);
-            m = m2;
-            l *= f;
-            if (c > 0 || has_o) rescale<D>(s_col, o_col, c, has_o, f);
-        }
+        grow<D>(s_col, o_col, 16 * c, has_o, mx, m, l);
         const float sub = P_BIAS - (m == NEG_INF ? 0.f : m);
-        if (MODE < 2) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) l = fmaf(group_probs(r, u, a[u], b[u] + sub, p), meta[2 * TILE + 2 * c + u], l);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-                const float x = ex2(__uint_as_float(r[j]) + sub), y = ex2(__uint_as_float(r[j + 1]) + sub);
-                l = fmaf(x, meta[2 * TILE + 32 * c + j], l);
-                l = fmaf(y, meta[2 * TILE + 32 * c + j + 1], l);
-                p[j / 2] = pack_f16(x, y);
-            }
-        }
+        for (int u = 0; u < 2; ++u) l = fmaf(group_probs(r, u, a[u], b[u] + sub, p), meta[2 * TILE + 2 * c + u], l);
         tc_st16(s_col + 16 * c, p);      // columns that have been read
+    }
+}
+// A masked one: the last of the cached tiles (a scale per 16 keys), and the tail (a scale per key).  Once or twice per item, so
+// its instructions are never in the caches: it is kept small.
+template <int D>
+__device__ __forceinline__ void tile_softmax_masked(uint32_t s_col, uint32_t o_col, const uint32_t (&mk)[4], bool per_key,
+                                                    const float* meta, float rq, bool has_o, float& m, float& l) {
+    const int per = per_key ? 0 : 4;
+    uint32_t bits = 0;
+#pragma unroll 1
+    for (int c = 0; c < TILE; c += 16, bits >>= 16) {
+        if ((c & 16) == 0) bits = c == 0 ? mk[0] : c == 32 ? mk[1] : c == 64 ? mk[2] : mk[3];
+        uint32_t r[16], p[8];
+        tc_ld16(s_col + c, r);
+        float mx = NEG_INF;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float* s = meta + ((c + j) >> per);
+            const float x = fmaf(__uint_as_float(r[j]), fmaxf(s[0] * rq, 1.2e-38f), s[TILE]);
+            r[j] = (bits >> j) & 1 ? __float_as_uint(x) : 0xff800000u;
+            mx = fmaxf(mx, __uint_as_float(r[j]));
+        }
+        grow<D>(s_col, o_col, c / 2, has_o, mx, m, l);
+        const float sub = P_BIAS - (m == NEG_INF ? 0.f : m);
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+            const float x = ex2(__uint_as_float(r[j]) + sub), y = ex2(__uint_as_float(r[j + 1]) + sub);
+            l = fmaf(x, meta[2 * TILE + ((c + j) >> per)], l);
+            l = fmaf(y, meta[2 * TILE + ((c + j + 1) >> per)], l);
+            p[j / 2] = pack_f16(x, y);
+        }
+        tc_st8(s_col + c / 2, p);
     }
 }
 
@@ -1133,6 +1189,18 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
             for (int tl = dual ? 0 : i; tl < nt; tl += dual ? 1 : 2) {
                 const int gt = g0 + tl, t = g.t0 + tl;
                 const float* meta = sh.meta[gt & (TC_META - 1)][0];
+                const bool masked = t >= g.q.nct || (t + 1) * TILE > g.q.full;
+                uint32_t mk[4] = {};
+                if (masked && !idle) {                                    // while the scores are made
+#pragma unroll 1
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t bits = tile_mask(P, g, t, n, w);
+                        mk[0] = w == 0 ? bits : mk[0];
+                        mk[1] = w == 1 ? bits : mk[1];
+                        mk[2] = w == 2 ? bits : mk[2];
+                        mk[3] = w == 3 ? bits : mk[3];
+                    }
+                }
                 bar_wait(&sh.sf[i], cnt & 1, sh);          // first: with it, the scales' barrier is in this phase or the next
                 bar_wait(&sh.mf[gt & (TC_META - 1)], (gt / TC_META) & 1, sh);
                 tc_after();
@@ -1145,16 +1213,9 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
                     bar_arrive(&sh.pf[i]);
                     continue;
                 }
-                const int mode = t >= g.q.nct ? 2 : (t + 1) * TILE > g.q.full ? 1 : 0;
-                uint32_t mk[4] = {};
                 // with this tile's scores the product before them has ended: O can be rescaled
-                if (mode == 0) {
-                    tile_softmax<D, 0>(s_col, o_col + i * D, meta, rq, mk, !begins, m, l);
-                } else {
-                    tile_mask(P, g, t, n, mk);
-                    if (mode == 1) tile_softmax<D, 1>(s_col, o_col + i * D, meta, rq, mk, !begins, m, l);
-                    else tile_softmax<D, 2>(s_col, o_col + i * D, meta, rq, mk, !begins, m, l);
-                }
+                if (!masked) tile_softmax<D>(s_col, o_col + i * D, meta, rq, !begins, m, l);
+                else tile_softmax_masked<D>(s_col, o_col + i * D, mk, t >= g.q.nct, meta, rq, !begins, m, l);
                 tc_wait_st();
                 tc_before();
                 bar_arrive(&sh.pf[i]);
@@ -1193,17 +1254,15 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
             float* part = partial_of<D>(P, blockIdx.x, g.t0 == 0 ? 1 : 0);
             const float quiet = __int_as_float(0x7fffffff);
 #pragma unroll 1
-            for (int c = c_lo; c < (idle ? c_lo : c_hi); c += 32) {
-                uint32_t o[32];
-                tc_ld32(o_col + (dual ? i * D : 0) + c, o);
-                tc_wait_ld(o);
+            for (int c = c_lo; c < (idle ? c_lo : c_hi); c += 8) {
+                uint32_t o[8];
+                tc_ld8(o_col + (dual ? i * D : 0) + c, o);
                 if (!dual) {
                     if (nt > 1) {
-                        uint32_t o2[32];
-                        tc_ld32(o_col + D + c, o2);
-                        tc_wait_ld(o2);
+                        uint32_t o2[8];
+                        tc_ld8(o_col + D + c, o2);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
+                        for (int j = 0; j < 8; ++j)
                             o[j] = __float_as_uint(__uint_as_float(o[j]) * f[0] + __uint_as_float(o2[j]) * f[1]);
                     }
                 }
@@ -1219,7 +1278,7 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
                                 : P.v.p + g.b * P.v.b + (e - g.q.open) * P.v.n + g.h * P.v.h;
                             const __nv_bfloat16* vv = reinterpret_cast<const __nv_bfloat16*>(src) + c;
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) {
+                            for (int j = 0; j < 8; ++j) {
                                 const float x = __bfloat162float(vv[j]);
                                 if (!(fabsf(x) <= 3.402823466e38f)) o[j] = __float_as_uint(__uint_as_float(o[j]) + x);
                             }
@@ -1228,19 +1287,15 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
                 }
                 if (ri < rows) {
                     if (whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(P.out + (orow * D + c) * 2);
+                        uint32_t w[4];
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            float x[8];
-#pragma unroll
-                            for (int u = 0; u < 8; ++u) x[u] = nan ? quiet : __uint_as_float(o[j + u]) * inv;
-                            dst[j / 8] = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                                                    pack_bf16(x[6], x[7]));
-                        }
+                        for (int j = 0; j < 4; ++j)
+                            w[j] = nan ? 0x7fff7fffu : pack_bf16(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                        *reinterpret_cast<uint4*>(P.out + (orow * D + c) * 2) = make_uint4(w[0], w[1], w[2], w[3]);
                     } else {
                         float4* dst = reinterpret_cast<float4*>(part + (int64_t)ri * D + c);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4)
+                        for (int j = 0; j < 8; j += 4)
                             dst[j / 4] = nan ? make_float4(quiet, quiet, quiet, quiet)
                                              : make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]),
                                                            __uint_as_float(o[j + 2]), __uint_as_float(o[j + 3]));
@@ -1367,28 +1422,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// Largest finite magnitude of bf16 words, as bits; elements that are not finite become 0 or (keep_nan) NaN.
-template <int N>
-__device__ __forceinline__ uint32_t bf16_amax(uint32_t (&w)[N], bool& bad, bool keep_nan) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
-    m = max(m & 0xffffu, m >> 16);
-    bad = m >= 0x7f80u;
-    if (bad) {
-        m = 0;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-#pragma unroll
-            for (int s = 0; s < 32; s += 16) {
-                const uint32_t a = (w[i] >> s) & 0x7fffu;
-                if (a >= 0x7f80u) w[i] = (w[i] & ~(0xffffu << s)) | (keep_nan ? 0x7fffu << s : 0u);
-                else m = max(m, a);
-            }
-    }
-    return m;
-}
-__device__ __forceinline__ int bits_exp(uint32_t m) { return m ? max(min((int)(m >> 7), 253), 1) - 127 : 0; }
 __device__ __forceinline__ uint32_t bf16_f16(uint32_t w, float s) { return pack_f16(bf_lo(w) * s, bf_hi(w) * s); }
 
 // A warp's part of a tile.
