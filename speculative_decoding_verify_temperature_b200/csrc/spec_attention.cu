@@ -1998,9 +1998,9 @@ using sv_host::fail;
 namespace {
 
 // What an item costs on the line of work beside its tiles, in tiles (its start, its end, its cut).  64 chains of 6 over ragged
-// lengths up to 4096 took 313, 265, 268 us at 0, 4, 8; 32 trees of 64 over 8192: 753, 622, 635; 64 single tokens over 8192:
-// 121, 117, 121 at 2, 4, 6.
-constexpr int OVER = 4;
+// lengths up to 4096 took 217, 209, 203 us at 2, 3, 4 (an earlier form 268 at 8), 32 trees of 64 over 8192 575, 553, 543 (635);
+// 64 single tokens over 8192 118, 117, 122.
+constexpr int TC_OVER = 4, MM_OVER = 3;
 constexpr int TC_CTAS = 148, MM_CTAS = MM_CTAS_SM * 148;      // CTAs at most
 
 template <int D>
@@ -2048,7 +2048,7 @@ spec_status page_map(const Att& P, void* pages, int rows, CUtensorMap* map) {
 template <int D>
 spec_status launch_tc(Att P, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
-    P.over = OVER;
+    P.over = TC_OVER;
     if (const spec_status s = sv_host::allow_smem(reinterpret_cast<const void*>(k_attention_tc<D>), "k_attention_tc", tc_smem<D>(), done)) return s;
     const int ctas = sv_host::num_sms() < TC_CTAS ? sv_host::num_sms() : TC_CTAS;
     CUtensorMap kmap;
@@ -2062,7 +2062,7 @@ template <int D, int NQ>
 spec_status launch_mma(Att P, cudaStream_t st) {
     const size_t smem = sizeof(MmShared<D, NQ>) + 1024;
     static std::atomic<uint64_t> done{0};
-    P.over = OVER;
+    P.over = MM_OVER;
     if (const spec_status s = sv_host::allow_smem(reinterpret_cast<const void*>(k_attention_mma<D, NQ>), "k_attention_mma", smem, done)) return s;
     CUtensorMap kmap, vmap;
     if (const spec_status s = page_map<D>(P, P.c.k_pages, 16, &kmap)) return s;

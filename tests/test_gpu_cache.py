@@ -402,6 +402,21 @@ def test_attention(spec, B, N, Hq, Hkv, D, page, lengths):
     assert torch.equal(out, again) and torch.equal(lse, lse2)      # the same bits every time
 
 
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,page,lengths", [
+    (48, 6, 64, 8, 128, 16, [(i * 397) % 701 for i in range(48)]), (100, 20, 8, 4, 64, 16, [i % 40 - 1 for i in range(100)]),
+    (12, 256, 4, 2, 128, 32, [(i * 37) % 300 for i in range(12)]), (40, 3, 8, 1, 128, 128, [(i * 131) % 1200 for i in range(40)]),
+    (1, 40, 32, 4, 128, 64, [9000]), (150, 1, 8, 2, 128, 16, [(i * 29) % 90 for i in range(150)])])
+def test_attention_waits_end(spec, B, N, Hq, Hkv, D, page, lengths):
+    """Many short items, tails only, items cut over many blocks: no wait gives up (the status word stays 0), call after call."""
+    c, r, q, k, v, mask = attention_inputs(spec, B, N, Hq, Hkv, D, page, lengths, 7 * B + N)
+    ws = workspace(spec, B, N, Hq, D)
+    args = (q.cuda(), k.cuda(), v.cuda(), c, ref.pack(mask).cuda())
+    outs = [spec.spec_tree_attention(*args, return_lse=True, workspace=ws) for _ in range(20)]
+    assert spec.spec_read_device_status(ws) == 0
+    check_attention(r, lengths, q, k, v, mask, *outs[0], 1 / math.sqrt(D))
+    assert all(torch.equal(o, outs[0][0]) and torch.equal(e, outs[0][1]) for o, e in outs)
+
+
 @pytest.mark.parametrize("N,Hq,Hkv,D", [(1, 8, 2, 128), (6, 4, 2, 64), (40, 8, 2, 128), (130, 2, 1, 128)])
 def test_attention_any_mask(spec, N, Hq, Hkv, D):
     """Arbitrary masks, rows without any key among them, chains without a mask, slots in another order."""
