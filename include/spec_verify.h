@@ -566,7 +566,8 @@ spec_status spec_vp_chain_finish(int B, int gamma, int V_shard, const int32_t* t
  * lengths        [B] int32: tokens in the cache; negative = no sequence in this
  *                row (its outputs are zeros, nothing is appended).
  * head_dim 64 or 128; page_size 16, 32, 64 or 128; lengths up to
- * max_pages * page_size + page_size - 1 and below 2^30.
+ * max_pages * page_size + page_size - 1 and below 2^30; at most 2^31 - 1 rows
+ * (num_pages * kv_heads * page_size).
  *
  * Sequences whose device-side inputs are invalid (a page id outside
  * [0, num_pages) where it is read, a slot outside [0, num_slots), a length above
@@ -686,7 +687,7 @@ spec_status spec_tree_attention(int B, int N, int q_heads, const spec_kv_cache* 
  * Row i becomes token lengths[b] + i.  With k_weight and / or rot_dim > 0 its key
  * is normed and rotated to that position on the way as by spec_qk_norm_rope.
  * Keys and values are rounded to bf16; when a block fills, each head's block is
- * scaled by the least power of two that brings its largest finite magnitude
+ * scaled by the least power of two (2^-126 or more) that brings its largest finite magnitude
  * within 448 (1 for a block of zeros) and rounded to e4m3 (nearest, ties to
  * even); NaN and infinities become NaN.
  * out_lengths    [B] int32: lengths[b] + rows; may be the lengths themselves.

@@ -480,6 +480,9 @@ spec_status check_cache(const spec_kv_cache* c, int B) {
                     (long long)c->page_table_stride);
     if (c->num_pages < 0 || c->num_pages > INT32_MAX)
         return fail(SPEC_ERR_INVALID_ARG, "cache: num_pages %lld", (long long)c->num_pages);
+    if (c->num_pages * c->kv_heads * c->page_size > INT32_MAX)       // a row is a 32-bit coordinate of the tensor copies
+        return fail(SPEC_ERR_INVALID_ARG, "cache: %lld pages of %d heads x %d tokens are more than 2^31 - 1 rows",
+                    (long long)c->num_pages, c->kv_heads, c->page_size);
     if (c->num_slots < 0 || (!c->slots && c->num_slots < B))
         return fail(SPEC_ERR_INVALID_ARG, "cache: %d slots for %d sequences", c->num_slots, B);
     if (B > 0 && !c->lengths) return fail(SPEC_ERR_INVALID_ARG, "cache: lengths are NULL");

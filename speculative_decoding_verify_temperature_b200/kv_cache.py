@@ -69,12 +69,20 @@ def _rows4(t, name, shape, dtype, device):
     s = t.stride()
     if s[3] != 1 and shape[3] > 1:
         raise ValueError(f"{name} must have unit stride in its last dim")
-    c = _strides.get(s)
-    if c is None:
-        if len(_strides) > 4096:
-            _strides.clear()
-        c = _strides[s] = (ctypes.c_int64 * 3)(s[0], s[1], s[2])
-    return t.data_ptr(), c
+    return t.data_ptr(), _strides.get(s) or _new_strides(s)
+
+
+def _new_strides(s):
+    if len(_strides) > 4096:
+        _strides.clear()
+    c = _strides[s] = (ctypes.c_int64 * 3)(s[0], s[1], s[2])
+    return c
+
+
+def _packed(N, H, D):
+    """The strides of a contiguous [B, N, H, D] tensor for the library."""
+    s = (N * H * D, H * D, D, 1)
+    return _strides.get(s) or _new_strides(s)
 
 
 class KvCache:
@@ -235,6 +243,8 @@ def _weights(pairs, D, device):
         if w is None:
             ptrs.append(None)
             continue
+        if not isinstance(w, torch.Tensor):
+            raise TypeError(f"{name} must be a tensor")
         if dt is not None and w.dtype != dt:
             raise TypeError("q_weight and k_weight must have the same dtype")
         dt = w.dtype
@@ -248,10 +258,11 @@ def _weights(pairs, D, device):
 def _frequencies(inv_freq, device):
     if inv_freq is None:
         return None, 0
-    if inv_freq.dim() != 1:
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
         raise ValueError("inv_freq must be a [rot_dim / 2] tensor")
-    _need(inv_freq, "inv_freq", _F32, inv_freq.shape, device)
-    return inv_freq.data_ptr(), 2 * inv_freq.shape[0]
+    n = inv_freq.shape[0]
+    _need(inv_freq, "inv_freq", _F32, (n,), device)
+    return inv_freq.data_ptr(), 2 * n
 
 
 def spec_qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -274,10 +285,14 @@ def spec_qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None
     with current:
         if q_out is None:
             q_out = q.new_empty((B, N, Hq, D))
+            qop, qos = q_out.data_ptr(), _packed(N, Hq, D)
+        else:
+            qop, qos = _rows4(q_out, "q_out", (B, N, Hq, D), q.dtype, dev)
         if k_out is None:
             k_out = q.new_empty((B, N, Hk, D))
-        qop, qos = _rows4(q_out, "q_out", (B, N, Hq, D), q.dtype, dev)
-        kop, kos = _rows4(k_out, "k_out", (B, N, Hk, D), q.dtype, dev)
+            kop, kos = k_out.data_ptr(), _packed(N, Hk, D)
+        else:
+            kop, kos = _rows4(k_out, "k_out", (B, N, Hk, D), q.dtype, dev)
         _check(lib().spec_qk_norm_rope(B, N, Hq, Hk, D, qp, qs, kp, ks, dt, positions.data_ptr(), freq, rot,
                                        int(bool(interleaved)), qw, kw, wdt, eps, qop, qos, kop, kos, s),
                "spec_qk_norm_rope")

@@ -138,6 +138,24 @@ def _tensors(B=2, P=8, H=2, page=16, D=64, M=4, S=2):
                 page_table=torch.zeros(B, M, dtype=torch.int32), lengths=torch.zeros(B, dtype=torch.int32))
 
 
+@pytest.mark.parametrize("pages,heads,page,ok", [((1 << 26) - 1, 2, 16, True), (1 << 26, 2, 16, False),
+                                                 (1 << 24, 1, 128, False), ((1 << 31) - 1, 1, 16, False)])
+def test_rows_of_the_cache_have_a_limit(L, pages, heads, page, ok):
+    """A row of the pages is a 32-bit coordinate: more are refused by both calls that reach them."""
+    from speculative_decoding_verify_temperature_b200 import spec_verify as sv
+    c = cache(num_pages=pages, kv_heads=heads, page_size=page)
+    s = strides(1024, 128 * heads, 128)
+    def detail(status):                                   # no output: what is refused next
+        assert status == sv.SPEC_ERR_INVALID_ARG
+        return L.spec_last_error_detail().decode()
+
+    texts = [detail(L.spec_kv_append(1, 1, 1, c, FAKE, s, FAKE, s, 1, None, None, None, 0, 0, None, 1, 1e-6, None,
+                                     WS, 1 << 20, None)),
+             detail(L.spec_tree_attention(1, 1, heads, c, FAKE, s, FAKE, s, FAKE, s, None, 1.0, None, None, WS,
+                                          1 << 30, None))]
+    assert all(("rows" in t) == (not ok) for t in texts), texts
+
+
 def test_binding_refusals():
     import speculative_decoding_verify_temperature_b200 as spec
     good = spec.KvCache(**_tensors())
