@@ -200,7 +200,7 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t m) {
 // rows before lengths[b] come from the ring, the others from k and v.  A full
 // block is reduced to its largest magnitude, scaled and written as a page; else
 // the new rows go to the ring.  Bound by latency for a round's few rows (11 us a call, the host's
-// part of it), by instructions for prompts: 8 x 2048 tokens (8 heads of 128, normed and rotated) take 44 us, 1.7 TB/s, with 59% of
+// part of it), by instructions for prompts: 8 x 2048 tokens (8 heads of 128, normed and rotated) take 39 us, 1.9 TB/s, with about 59% of
 // the issue slots filled and a barrier in the middle for the block's maximum.
 template <int DT, int R>
 __global__ void __launch_bounds__(AP_BT, R <= 4 ? 3 : 2) k_append(const Append P) {
@@ -607,9 +607,10 @@ spec_status spec_kv_append(int B, int T, int width, const spec_kv_cache* cache,
     P.status = reinterpret_cast<unsigned*>(ws + sv_host::CACHE_WS_STATUS);
     P.cnt = reinterpret_cast<unsigned*>(ws + sv_host::CACHE_WS_SEQ);
     const int blocks = (page - 1 + width - 1) / page + 1;          // touched at most
-    // a CTA takes several heads (they share the angles) once there are CTAs enough for eight per SM
+    // a CTA takes several heads (they share the angles) once there are CTAs enough for four per SM: 8 x 2048 tokens took 43 us
+    // with eight, 39 with four, 45 with three; 1 x 2048 13.3 us with each of them, 15 with two heads to a CTA
     const long long units = (long long)blocks * B * Hkv;
-    long long per = (units + 8LL * sv_host::num_sms() - 1) / (8LL * sv_host::num_sms());
+    long long per = (units + 4LL * sv_host::num_sms() - 1) / (4LL * sv_host::num_sms());
     P.heads_per_cta = (int)(per < 1 ? 1 : per > Hkv ? Hkv : per);
     const long long ys = (long long)B * ((Hkv + P.heads_per_cta - 1) / P.heads_per_cta);
     if (ys > 65535) return fail(SPEC_ERR_INVALID_ARG, "B * kv_heads = %lld is above 65535 rows of CTAs", ys);
