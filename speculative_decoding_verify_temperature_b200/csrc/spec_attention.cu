@@ -253,7 +253,7 @@ __device__ __forceinline__ uint32_t tail_bits(const Att& P, int b, int n, int op
 // the leading one to 2^11 or more: f16's smallest step is 2^-35 of it.
 //
 // Measured (B200, D = 128, 64 query on 8 kv heads): 32 trees of 64 nodes over ragged lengths up to 8192 550 us, 630 TFLOP/s;
-// one tree of 32 over 131072 tokens 120 us, 285 TFLOP/s; 64 chains of 6 over ragged lengths up to 4096 204 us.  Bound by the
+// 64 chains of 6 over ragged lengths up to 4096 204 us; one tree of 32 over 131072 tokens (32 query heads of 64) 120 us.  Bound by the
 // chain of one stream's steps, about 5400 cycles a tile: softmax 3100 (its own warp's latencies: MUFU a third busy), the
 // product with values 700, the scores of the next tile 850, barriers the rest; the two streams run side by side and tensor
 // memory (S0 S1 O0 O1 fill it at D = 128) has no room for a third.  An item costs another 25000 cycles or so.  Tried and slower:
@@ -1420,10 +1420,11 @@ __global__ void __launch_bounds__(MERGE_BT) k_attention_merge(const Att P) {
 // Each warp has its own running maximum, sum and output (in registers); the four
 // are joined through shared memory at the end of an item.
 //
-// Measured (D = 128, 64 query on 8 kv heads): 64 single tokens over ragged lengths up to 8192 124 us, 5.4 TB/s, 0.83 of the copy
+// Measured (D = 128, 32 query on 8 kv heads): 64 single tokens over ragged lengths up to 8192 125 us, 5.4 TB/s, 0.83 of the copy
 // rate.  Bound by the bytes, near the end by latency: three warps per scheduler issue in 37% of the cycles.  With queries as
 // rows (16, half of them empty for 8) it took 140 us, with steps of 16 keys 170.
-// Up to 16 rows go this way; the tensor-core kernel takes 128 rows in the time of one.  64 chains of 2, 16 rows: 99 us here.  More rows
+// Up to 16 rows go this way; the tensor-core kernel takes 128 rows in the time of one.  64 chains of 2 with 64 query heads,
+// 16 rows, over 4096: 99 us here.  More rows
 // by more warps on the same ring (queries as rows) were measured against it: 32 rows 223 : 211 us, 48 rows 226 : 219, 64 rows
 // 320 : 229.
 constexpr int MM_BT = 128, MM_WARPS = MM_BT / 32, MM_ROWS = 16, MM_CTAS_SM = 3;
