@@ -253,7 +253,7 @@ __device__ __forceinline__ uint32_t tail_bits(const Att& P, int b, int n, int op
 // the leading one to 2^11 or more: f16's smallest step is 2^-35 of it.
 //
 // Measured (B200, D = 128, 64 query on 8 kv heads): 32 trees of 64 nodes over ragged lengths up to 8192 550 us, 630 TFLOP/s;
-// 64 chains of 6 over ragged lengths up to 4096 204 us; one tree of 32 over 131072 tokens (32 query heads of 64) 120 us.  Bound by the
+// 64 chains of 6 over ragged lengths up to 4096 197 us; one tree of 32 over 131072 tokens (32 query heads of 64) 106 us.  Bound by the
 // chain of one stream's steps, about 5400 cycles a tile: softmax 3100 (its own warp's latencies: MUFU a third busy), the
 // product with values 700, the scores of the next tile 850, barriers the rest; the two streams run side by side and tensor
 // memory (S0 S1 O0 O1 fill it at D = 128) has no room for a third.  An item costs another 25000 cycles or so.  Tried and slower:
@@ -1336,8 +1336,9 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
 
 // Puts the cut items together: block x the item that CTA x began, one warp per
 // row, lane p the maximum and sum of part p.  Bound by latency: the parts lie in L2.
-// Launched beside the kernel before, so that only its own work is left when that ends.
-constexpr int MERGE_BT = 256, MERGE_ROWS = 32;
+// Launched beside the kernel before, so that only its own work is left when that ends.  A row to each warp: with 4, 2, 1 of them
+// one tree of 32 over 131072 tokens (8 items in 148 parts) took 126, 116, 111 us, 64 chains of 6 205, 200, 197.
+constexpr int MERGE_BT = 256, MERGE_ROWS = MERGE_BT / 32;
 
 template <int D>
 __global__ void __launch_bounds__(MERGE_BT) k_attention_merge(const Att P) {
