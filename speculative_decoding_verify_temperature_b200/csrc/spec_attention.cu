@@ -28,7 +28,7 @@ struct Att {
     float* lse;
     unsigned* status;
     struct Cut* cut;                      // [gridDim.x] the item that a CTA begins and does not end
-    float* partial;                       // [gridDim.x][2][rows of an item][D + 2]
+    float* partial;                       // [gridDim.x][2][rows of an item][D + 3]
 };
 
 // An item whose tiles several CTAs share: they leave partial results, the CTA that
@@ -252,6 +252,14 @@ __device__ __forceinline__ uint32_t tail_bits(const Att& P, int b, int n, int op
 // is changed only when it grows by more than 3; P_BIAS lifts P to at most 2^15, and
 // the leading one to 2^11 or more: f16's smallest step is 2^-35 of it.
 //
+// l stands relative to the same M, although it has nothing to do with the values: P_j / s_v,j is 2^(x_j - M + P_BIAS),
+// which leaves the range of f32 where M is more than 100 or so away from the largest x_j.  With every s_v,j within
+// [FAR_LO, FAR_HI] it is at most 43 away, and what f32 drops of l lies 2^-55 below its leading part.  From the first tile with
+// another scale on, a row's l is summed from exponentials of its own, 2^(x_j - r), with r a whole number that
+// follows the largest x_j ("far"; r = M - P_BIAS otherwise), and out = O / l 2^(M - P_BIAS - r).  That costs a second
+// exponential per key, in code that trained values do not reach; the others pay for it in an item's own steps (64 chains of 6
+// over ragged lengths up to 4096 197 -> 203 us; 549 and 105 us, see below, as before).
+//
 // Measured (B200, D = 128, 64 query on 8 kv heads): 32 trees of 64 nodes over ragged lengths up to 8192 550 us, 630 TFLOP/s;
 // 64 chains of 6 over ragged lengths up to 4096 197 us; one tree of 32 over 131072 tokens (32 query heads of 64) 106 us.  Bound by the
 // chain of one stream's steps, about 5400 cycles a tile: softmax 3100 (its own warp's latencies: MUFU a third busy), the
@@ -263,6 +271,9 @@ constexpr int TC_SOFTMAX = 256, TC_CONV = 256, TC_BT = 640;
 constexpr int TC_W_CONV = 8, TC_W_MMA = 16, TC_W_COPY = 17, TC_W_SCALE = 18;
 constexpr int TC_META = 4;                // tiles whose scales are kept
 constexpr float P_BIAS = 12.f, M_SLACK = 3.f;
+constexpr float FAR_LO = 0x1p-40f, FAR_HI = 0x1p40f, R_SLACK = 20.f;
+__device__ __forceinline__ bool is_far(float s) { return !(s >= FAR_LO && s <= FAR_HI); }
+__device__ __forceinline__ bool is_far_exp(int e) { return e < -40 || e > 40; }
 
 template <int D> struct Tc {
     static constexpr int HALVES = D / 64;                 // 128-byte rows of 64 f16
@@ -275,9 +286,12 @@ template <int D> struct Tc {
     static constexpr int O_COL = 256;                     // tensor memory columns: S0 S1 (128 each), O0 O1 (D each)
 };
 struct TcShared {
-    float meta[TC_META][3][TILE];                         // per key (tail) or group of 16 (cached): a, log2 s_v, 1 / s_v
+    // per key (tail) or group of 16 (cached): a, log2 s_v, 1 / s_v; of a far tile: a, +inf, -1, log2 s_v
+    float meta[TC_META][4][TILE];
     float rq[4][256];                                     // per row: its power of two * scale * log2(e)
     float xm[2][TILE], xl[2][TILE];                       // M and l of the streams that are joined
+    float far[3][2][TILE];                                // M, l and r of far rows
+    int far_tail;                                         // 1 + the last tail tile with a far key
     uint32_t bad_v[4][12];                                // tail keys whose value is not finite
     int bad_seg[8];                                       // 1 + segment that met a bad page
     uint64_t kf[6], ke[6], rf[4], re[4], vf[2], ve[2], mf[TC_META], me[TC_META], sf[2], pf[2], pv[2], qf, qe, drain;
@@ -296,6 +310,11 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// What a sum relative to 2^from counts relative to 2^to >= 2^from (-inf: an empty sum, whose NaN stays).
+__device__ __forceinline__ float moved(float from, float to) { return from == NEG_INF ? (to == NEG_INF ? 1.f : 0.f) : ex2(from - to); }
+// What takes O to an output is 1 / l and 2^g, g = M - P_BIAS - r, 0 unless the row is far.  2^(g / 2), twice, stays in f32's range.
+__device__ __forceinline__ float lift_of(float m, float r) { return m == NEG_INF ? 0.f : m - P_BIAS - r; }
+__device__ __forceinline__ float half_exp2(float g) { return ex2(0.5f * g); }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -637,10 +656,13 @@ __device__ __forceinline__ void tc_scales(const Att& P, TcShared& sh, const Stre
         if (more && u.first()) prefetch_segment<D>(P, u, lane);
         bar_wait(&sh.me[m], par, sh);
         // the operand warps write the tail's; they arrive once and this warp once (for the reason given at the copies)
+        const bool far = __any_sync(FULL, is_far(v0));    // lanes without a key hold 1
         if (cached && lane < 8) {
+            const float b = log2f(v0);
             sh.meta[m][0][lane] = k0;
-            sh.meta[m][1][lane] = log2f(v0);
-            sh.meta[m][2][lane] = 1.f / v0;
+            sh.meta[m][1][lane] = far ? -NEG_INF : b;
+            sh.meta[m][2][lane] = far ? -1.f : 1.f / v0;
+            if (far) sh.meta[m][3][lane] = b;
         }
         __syncwarp();
         if (lane == 0) bar_arrive(&sh.mf[m]);
@@ -844,6 +866,7 @@ struct TcConv {
             meta[r] = exp2i(ke) * 0.0078125f;
             meta[TILE + r] = (float)ve;
             meta[2 * TILE + r] = exp2i(-ve);
+            if (is_far_exp(ve)) *reinterpret_cast<volatile int*>(&sh.far_tail) = u.gt + 1;
         }
     }
     // A tile of the tail: its two units of keys, its values and all of its scales.
@@ -875,6 +898,14 @@ struct TcConv {
         }
         proxy_fence();
         asm volatile("bar.sync 2, %0;" :: "n"(TC_CONV) : "memory");
+        if (tid < 32 && *reinterpret_cast<volatile int*>(&sh.far_tail) == u.gt + 1) {
+            for (int r = tid; r < TILE; r += 32) {
+                meta[3 * TILE + r] = meta[TILE + r];
+                meta[TILE + r] = -NEG_INF;
+                meta[2 * TILE + r] = -1.f;
+            }
+            __syncwarp();
+        }
         if (tid == 0) {
             bar_arrive(&sh.mf[m]);
             bar_arrive(&sh.kf[k0]);
@@ -977,19 +1008,100 @@ __device__ __noinline__ void rescale(uint32_t s_col, uint32_t o_col, int cols, b
         tc_st8(o_col + i, o);
     }
 }
+constexpr float FAR_M = -3e38f;           // M of a far row, outside of this function
+// Brings M up to mx where a row of the warp asks for it.
 template <int D>
-__device__ __forceinline__ void grow(uint32_t s_col, uint32_t o_col, int cols, bool has_o, float mx, float& m, float& l) {
-    if (!__any_sync(FULL, mx > m + M_SLACK)) return;
+__device__ __forceinline__ void raise_m(uint32_t s_col, uint32_t o_col, int cols, bool has_o, float mx, float& m, float& l) {
     const float m2 = fmaxf(m, ceilf(mx)), f = m2 == NEG_INF ? 1.f : ex2(m - m2);
     m = m2;
     l *= f;
     if (cols > 0 || has_o) rescale<D>(s_col, o_col, cols, has_o, f);
 }
+// The rest of a tile, from column c on, for a warp whose rows are far: l is summed on its own, relative to 2^r.  What stands
+// before column c weighs nothing (masked) or is NaN.  The thread's M, l and r are at x[0], x[2 TILE] and x[4 TILE] in shared memory.
+template <int D>
+__device__ __noinline__ void far_tile(uint32_t s_col, uint32_t o_col, int c, uint4 mk, int per, const float* meta, float rq, bool has_o,
+                                      float* x) {
+    float m = x[0], l = x[2 * TILE], r = x[4 * TILE];
+    const float* b = meta + (meta[2 * TILE] < 0.f ? 3 * TILE : TILE);
+#pragma unroll 1
+    for (; c < TILE; c += 16) {
+        const uint32_t bits = (c < 32 ? mk.x : c < 64 ? mk.y : c < 96 ? mk.z : mk.w) >> (c & 16);
+        uint32_t v[16], p[8];
+        tc_ld16(s_col + c, v);
+        float mx = NEG_INF, top = NEG_INF, none = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float y = (bits >> j) & 1 ? __uint_as_float(v[j]) * fmaxf(meta[(c + j) >> per] * rq, 1.2e-38f) : NEG_INF;
+            v[j] = __float_as_uint(y);
+            top = fmaxf(top, y);
+            mx = fmaxf(mx, y + b[(c + j) >> per]);
+        }
+        if (__any_sync(FULL, mx > m + M_SLACK)) raise_m<D>(s_col, o_col, c / 2, has_o, mx, m, none);
+        if (top > r + R_SLACK) {
+            const float up = ceilf(top);
+            l *= moved(r, up);
+            r = up;
+        }
+        const float sub = P_BIAS - (m == NEG_INF ? 0.f : m), ref = r == NEG_INF ? 0.f : r;
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+            const float y = __uint_as_float(v[j]), z = __uint_as_float(v[j + 1]);
+            l += ex2(y - ref) + ex2(z - ref);
+            p[j / 2] = pack_f16(ex2(y + (b[(c + j) >> per] + sub)), ex2(z + (b[(c + j + 1) >> per] + sub)));
+        }
+        tc_st8(s_col + c / 2, p);
+    }
+    x[0] = m;
+    x[2 * TILE] = l;
+    x[4 * TILE] = r;
+}
+// Seldom taken once the first tiles are through: a row's largest w passes M + M_SLACK.  The weights of a far tile pass every M, and
+// everything passes that of a far row: true then, and the tile from column c on has been dealt with.  So
+// what is far costs the other rows nothing.
+template <int D>
+__device__ __forceinline__ bool grow(uint32_t s_col, uint32_t o_col, int c, const uint32_t (&mk)[4], int per, const float* meta, float rq,
+                                     bool has_o, TcShared& sh, float mx, float& m, float& l) {
+    if (!__any_sync(FULL, mx > m + M_SLACK)) return false;
+    if (meta[2 * TILE] < 0.f || m == FAR_M) {             // the same for all rows of the warp
+        float* const x = &sh.far[0][0][threadIdx.x];      // the softmax warps' threads are 0 to 255
+        if (m != FAR_M) {
+            x[0] = m;
+            x[2 * TILE] = l;
+            x[4 * TILE] = m == NEG_INF ? NEG_INF : m - P_BIAS;
+            m = FAR_M;
+        }
+        far_tile<D>(s_col, o_col, c, make_uint4(mk[0], mk[1], mk[2], mk[3]), per, meta, rq, has_o, x);
+        return true;
+    }
+    raise_m<D>(s_col, o_col, c / 2, has_o, mx, m, l);
+    return false;
+}
+
+// A row of the streams joined where it is far in one of them: the factors of O, M, l, M - P_BIAS - r.
+struct Joined {
+    float f0, f1, m, l, lift;
+};
+__device__ __noinline__ Joined join_far(const TcShared& sh, int row, int nt) {
+    float mi[2], li[2], ri[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool far = sh.xm[i][row] == FAR_M;
+        mi[i] = far ? sh.far[0][i][row] : sh.xm[i][row];
+        li[i] = far ? sh.far[1][i][row] : sh.xl[i][row];
+        ri[i] = far ? sh.far[2][i][row] : mi[i] == NEG_INF ? NEG_INF : mi[i] - P_BIAS;
+    }
+    const float m = fmaxf(mi[0], mi[1]), r = fmaxf(ri[0], ri[1]);
+    return Joined{moved(mi[0], m), nt < 2 ? 0.f : moved(mi[1], m), m,
+                  li[0] * moved(ri[0], r) + (nt < 2 ? 0.f : li[1] * moved(ri[1], r)), lift_of(m, r)};
+}
 
 // One pass over a tile's scores: P = 2^(w - m + P_BIAS) in f16 over the scores, with m the largest w up to M_SLACK ago.
 // A cached tile that has all of its keys, 32 at a time.
 template <int D>
-__device__ __forceinline__ void tile_softmax(uint32_t s_col, uint32_t o_col, const float* meta, float rq, bool has_o, float& m, float& l) {
+__device__ __forceinline__ void tile_softmax(uint32_t s_col, uint32_t o_col, const float* meta, float rq, bool has_o, TcShared& sh, float& m,
+                                             float& l) {
+    const uint32_t all[4] = {~0u, ~0u, ~0u, ~0u};
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
         uint32_t r[32], p[16];
@@ -1002,7 +1114,7 @@ __device__ __forceinline__ void tile_softmax(uint32_t s_col, uint32_t o_col, con
             b[u] = meta[TILE + 2 * c + u];
             mx = fmaxf(mx, fmaf(group_max(r, u), a[u], b[u]));
         }
-        grow<D>(s_col, o_col, 16 * c, has_o, mx, m, l);
+        if (grow<D>(s_col, o_col, 32 * c, all, 4, meta, rq, has_o, sh, mx, m, l)) return;
         const float sub = P_BIAS - (m == NEG_INF ? 0.f : m);
 #pragma unroll
         for (int u = 0; u < 2; ++u) l = fmaf(group_probs(r, u, a[u], b[u] + sub, p), meta[2 * TILE + 2 * c + u], l);
@@ -1013,7 +1125,7 @@ __device__ __forceinline__ void tile_softmax(uint32_t s_col, uint32_t o_col, con
 // its instructions are never in the caches: it is kept small.
 template <int D>
 __device__ __forceinline__ void tile_softmax_masked(uint32_t s_col, uint32_t o_col, const uint32_t (&mk)[4], bool per_key,
-                                                    const float* meta, float rq, bool has_o, float& m, float& l) {
+                                                    const float* meta, float rq, bool has_o, TcShared& sh, float& m, float& l) {
     const int per = per_key ? 0 : 4;
     uint32_t bits = 0;
 #pragma unroll 1
@@ -1029,7 +1141,7 @@ __device__ __forceinline__ void tile_softmax_masked(uint32_t s_col, uint32_t o_c
             r[j] = (bits >> j) & 1 ? __float_as_uint(x) : 0xff800000u;
             mx = fmaxf(mx, __uint_as_float(r[j]));
         }
-        grow<D>(s_col, o_col, c / 2, has_o, mx, m, l);
+        if (grow<D>(s_col, o_col, c, mk, per, meta, rq, has_o, sh, mx, m, l)) return;
         const float sub = P_BIAS - (m == NEG_INF ? 0.f : m);
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
@@ -1042,8 +1154,9 @@ __device__ __forceinline__ void tile_softmax_masked(uint32_t s_col, uint32_t o_c
     }
 }
 
-// A partial result: the output rows, then the rows' maxima and sums; a multiple of 16 bytes.
-__host__ __device__ constexpr size_t partial_floats(size_t rows, int D) { return (rows * (D + 2) + 3) / 4 * 4; }
+// A partial result: the output rows, then the rows' M - P_BIAS, l and r; a multiple of 16 bytes.  r is only there where it is not
+// M - P_BIAS, and l is negative then.
+__host__ __device__ constexpr size_t partial_floats(size_t rows, int D) { return (rows * (D + 3) + 3) / 4 * 4; }
 template <int D>
 __device__ __forceinline__ float* partial_of(const Att& P, int cta, int slot) {
     return P.partial + ((int64_t)cta * 2 + slot) * partial_floats(min(P.R, 256), D);
@@ -1083,7 +1196,7 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
         bar_init(&sh.qf, TC_CONV / 32);
         bar_init(&sh.qe, 1);
         bar_init(&sh.drain, 1);
-        sh.abort = 0;
+        sh.abort = sh.far_tail = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         proxy_fence();
     }
@@ -1222,8 +1335,8 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
                     continue;
                 }
                 // with this tile's scores the product before them has ended: O can be rescaled
-                if (!masked) tile_softmax<D>(s_col, o_col + i * D, meta, rq, !begins, m, l);
-                else tile_softmax_masked<D>(s_col, o_col + i * D, mk, t >= g.q.nct, meta, rq, !begins, m, l);
+                if (!masked) tile_softmax<D>(s_col, o_col + i * D, meta, rq, !begins, sh, m, l);
+                else tile_softmax_masked<D>(s_col, o_col + i * D, mk, t >= g.q.nct, meta, rq, !begins, sh, m, l);
                 tc_wait_st();
                 tc_before();
                 bar_arrive(&sh.pf[i]);
@@ -1235,6 +1348,7 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
             // ---- the segment's rows: whole items are written out, parts go to the workspace
             float f[2] = {1.f, 0.f};                                      // factors of the streams' sums
             int c_lo = 0, c_hi = D;
+            float lift = 0.f;                                             // M - P_BIAS - r
             if (!dual) {
                 sh.xm[i][r] = m;
                 sh.xl[i][r] = l;
@@ -1246,8 +1360,16 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
                 f[1] = nt < 2 ? 0.f : m1 == NEG_INF ? (mm == NEG_INF ? 1.f : 0.f) : ex2(m1 - mm);
                 l = sh.xl[0][r] * f[0] + (nt < 2 ? 0.f : sh.xl[1][r] * f[1]);
                 m = mm;
+                if (m0 == FAR_M || m1 == FAR_M) {
+                    const Joined j = join_far(sh, r, nt);
+                    f[0] = j.f0, f[1] = j.f1, m = j.m, l = j.l, lift = j.lift;
+                }
                 c_lo = i * (D / 2);
                 c_hi = c_lo + D / 2;
+            } else if (m == FAR_M) {
+                m = sh.far[0][i][r];
+                l = sh.far[1][i][r];
+                lift = lift_of(m, sh.far[2][i][r]);
             }
             const bool whole = g.whole();
             const bool nan = g.q.bad || *reinterpret_cast<volatile int*>(&sh.bad_seg[seg & 7]) == seg + 1;
@@ -1257,7 +1379,7 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
 #pragma unroll
                 for (int w = 0; w < 12; ++w) bad_v |= sh.bad_v[seg & 3][w];
             }
-            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const float inv = (l == 0.f ? 0.f : 1.f / l) * (lift == 0.f ? 1.f : half_exp2(lift));
             const int64_t orow = ((int64_t)g.b * P.N + n) * P.Hq + head;
             float* part = partial_of<D>(P, blockIdx.x, g.t0 == 0 ? 1 : 0);
             const float quiet = __int_as_float(0x7fffffff);
@@ -1296,6 +1418,11 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
                 if (ri < rows) {
                     if (whole) {
                         uint32_t w[4];
+                        if (lift != 0.f) {
+                            const float up = half_exp2(lift);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * up);
+                        }
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             w[j] = nan ? 0x7fff7fffu : pack_bf16(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
@@ -1312,11 +1439,13 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
             }
             const bool speaks = ri < rows && (dual || i == 0);
             if (whole) {
-                if (speaks && P.lse) P.lse[orow] = nan ? quiet : l == 0.f ? NEG_INF : (m - P_BIAS + log2f(l)) * LN2;
+                if (speaks && P.lse) P.lse[orow] = nan ? quiet : l == 0.f ? NEG_INF : (m - P_BIAS - lift + log2f(l)) * LN2;
             } else {
                 if (speaks) {
-                    part[(int64_t)rows_of(P) * D + ri] = m == NEG_INF ? NEG_INF : m - P_BIAS;
-                    part[(int64_t)rows_of(P) * D + rows_of(P) + ri] = nan ? quiet : l;
+                    float* stat = part + (int64_t)rows_of(P) * D + ri;
+                    stat[0] = m == NEG_INF ? NEG_INF : m - P_BIAS;
+                    stat[rows_of(P)] = nan ? quiet : lift == 0.f ? l : -l;
+                    if (lift != 0.f) stat[2 * rows_of(P)] = m - P_BIAS - lift;
                 }
                 if (g.t0 == 0 && tid == 0) P.cut[blockIdx.x] = Cut{g.b, g.h, g.mt, parts_of(P, g, st, blockIdx.x)};
             }
@@ -1335,7 +1464,7 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
 }
 
 // Puts the cut items together: block x the item that CTA x began, one warp per
-// row, lane p the maximum and sum of part p.  Bound by latency: the parts lie in L2.
+// row, lane p the references and the sum of part p.  Bound by latency: the parts lie in L2.
 // Launched beside the kernel before, so that only its own work is left when that ends.  A row to each warp: with 4, 2, 1 of them
 // one tree of 32 over 131072 tokens (8 items in 148 parts) took 126, 116, 111 us, 64 chains of 6 205, 200, 197.
 constexpr int MERGE_BT = 256, MERGE_ROWS = MERGE_BT / 32;
@@ -1350,28 +1479,33 @@ __global__ void __launch_bounds__(MERGE_BT) k_attention_merge(const Att P) {
     constexpr int E = D / 32;
     for (int r = blockIdx.y * MERGE_ROWS + (threadIdx.x >> 5); r < upto; r += MERGE_BT / 32) {
         auto part = [&](int i) { return partial_of<D>(P, blockIdx.x + i, i == 0 ? 1 : 0); };
-        float M = NEG_INF, m0 = NEG_INF, l0 = 0.f;
+        float M = NEG_INF, R = NEG_INF, m0 = NEG_INF, r0 = NEG_INF, l0 = 0.f;
         for (int i = lane; i < cut.parts; i += 32) {
-            const float* p = part(i) + (int64_t)rows * D;
-            const float m = __ldcg(p + r), s = __ldcg(p + rows + r);
-            if (i == lane) m0 = m, l0 = s;
+            const float* p = part(i) + (int64_t)rows * D + r;
+            const float m = __ldcg(p), s = __ldcg(p + rows), x = s < 0.f ? __ldcg(p + 2 * rows) : m;
+            if (i == lane) m0 = m, l0 = s < 0.f ? -s : s, r0 = x;
             M = fmaxf(M, m);
+            R = fmaxf(R, x);
         }
 #pragma unroll
-        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
-        const float base = M == NEG_INF ? 0.f : M;
+        for (int o = 16; o; o >>= 1) {
+            M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+            R = fmaxf(R, __shfl_xor_sync(FULL, R, o));
+        }
+        const float base = M == NEG_INF ? 0.f : M, ref = R == NEG_INF ? 0.f : R;
         float acc[E] = {}, l = 0.f;
         for (int i0 = 0; i0 < cut.parts; i0 += 32) {
             if (i0) {
-                m0 = NEG_INF, l0 = 0.f;
+                m0 = r0 = NEG_INF, l0 = 0.f;
                 if (i0 + lane < cut.parts) {
-                    const float* p = part(i0 + lane) + (int64_t)rows * D;
-                    m0 = __ldcg(p + r);
-                    l0 = __ldcg(p + rows + r);
+                    const float* p = part(i0 + lane) + (int64_t)rows * D + r;
+                    m0 = r0 = __ldcg(p);
+                    l0 = __ldcg(p + rows);
+                    if (l0 < 0.f) l0 = -l0, r0 = __ldcg(p + 2 * rows);
                 }
             }
             const float w = ex2(m0 - base);
-            l = fmaf(w, l0, l);
+            l = fmaf(ex2(r0 - ref), l0, l);
             const int n = min(32, cut.parts - i0);
 #pragma unroll 8
             for (int i = 0; i < n; ++i) {
@@ -1389,15 +1523,17 @@ __global__ void __launch_bounds__(MERGE_BT) k_attention_merge(const Att P) {
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(FULL, l, o);
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float up = half_exp2(M == NEG_INF ? 0.f : M - ref), inv = (l == 0.f ? 0.f : 1.f / l) * up;
+#pragma unroll
+        for (int j = 0; j < E; ++j) acc[j] = acc[j] * up * inv;
         const int row = cut.mt * 256 + r, n = row / P.G;
         const int64_t at = ((int64_t)cut.b * P.N + n) * P.Hq + cut.h * P.G + row - n * P.G;
         char* out = P.out + at * D * 2;
         if constexpr (E == 4)
-            reinterpret_cast<uint2*>(out)[lane] = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+            reinterpret_cast<uint2*>(out)[lane] = make_uint2(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]));
         else
-            reinterpret_cast<uint32_t*>(out)[lane] = pack_bf16(acc[0] * inv, acc[1] * inv);
-        if (P.lse && lane == 0) P.lse[at] = l == 0.f ? NEG_INF : (base + log2f(l)) * LN2;
+            reinterpret_cast<uint32_t*>(out)[lane] = pack_bf16(acc[0], acc[1]);
+        if (P.lse && lane == 0) P.lse[at] = l == 0.f ? NEG_INF : (ref + log2f(l)) * LN2;
     }
 }
 
@@ -1461,6 +1597,7 @@ template <int D> struct MmRing {
 };
 struct MmSlots {
     float scale[2][2][2];                                 // [slot][chunk][keys, values]
+    float ref[16];                                        // r of the rows: once they are far, and at a segment's end
     uint64_t full[2];
 };
 
@@ -1472,12 +1609,14 @@ struct MmWarp {
     const Att& P;
     const int lane, warp, g, c;
     MmAhead& a;                                           // the segment of the chunk after, kept by lane 0
+    float* const ref;                                     // r of the rows, in shared memory
     int t, parity;
+    bool far;                                             // l is relative to 2^r, not to 2^(m - P_BIAS)
     // [column block][..]: dims g D/8 + 2t (0, 1) and + 1 (2, 3) of queries 2c and 2c + 1; their maxima and this lane's sums
     float o[NQ][NT][4], m[NQ][2], l[NQ][2];
 
-    __device__ __forceinline__ MmWarp(const Att& P_, int warp_, MmAhead& a_)
-        : P(P_), lane(threadIdx.x & 31), warp(warp_), g(lane >> 2), c(lane & 3), a(a_) {}
+    __device__ __forceinline__ MmWarp(const Att& P_, int warp_, MmAhead& a_, MmSlots& slots)
+        : P(P_), lane(threadIdx.x & 31), warp(warp_), g(lane >> 2), c(lane & 3), a(a_), ref(slots.ref) {}
 
     __device__ __forceinline__ void begin(const Stretch& st) {
         if (lane == 0) {
@@ -1530,6 +1669,49 @@ struct MmWarp {
             copy4_arrive(&slots.full[s]);
         }
     }
+    __device__ __forceinline__ float own_ref(int q, int e) const { return m[q][e] == NEG_INF ? NEG_INF : m[q][e] - P_BIAS; }
+    // From now on the segment's sums are far.
+    __device__ __forceinline__ void go_far() {
+        far = true;
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (g == 0) ref[8 * q + 2 * c + e] = own_ref(q, e);
+        __syncwarp();
+    }
+    // A far row's sum over NC x 16 keys, relative to 2^r.
+    template <int NC, bool EACH>
+    __device__ __forceinline__ void far_sums(const float (&s)[NC][NQ][4], const float (&rq)[NQ][2], const float (&a)[NC][2],
+                                             const uint32_t (&mask)[NQ][2]) {
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x[2 * NC], top = NEG_INF;
+#pragma unroll
+                for (int n = 0; n < 2 * NC; ++n) {
+                    x[n] = s[n >> 1][q][2 * (n & 1) + e] * fmaxf(a[n >> 1][n & 1] * rq[q][e], 1.2e-38f);
+                    if (EACH && !((mask[q][e] >> (g + 8 * (n & 1))) & 1)) x[n] = NEG_INF;
+                    top = fmaxf(top, x[n]);
+                }
+#pragma unroll
+                for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(FULL, top, d));
+                float& at = ref[8 * q + 2 * c + e];       // the same row in all lanes of column c
+                float r = at;
+                __syncwarp();
+                if (top > r + R_SLACK) {
+                    const float up = ceilf(top);
+                    l[q][e] *= moved(r, up);
+                    r = up;
+                    if (g == 0) at = r;
+                }
+                __syncwarp();
+                const float sub = r == NEG_INF ? 0.f : r;
+#pragma unroll
+                for (int n = 0; n < 2 * NC; ++n) l[q][e] += ex2(x[n] - sub);
+            }
+    }
     // Scores of NC x 16 keys to probabilities (the second product's columns).  Of keys g (0) and g + 8 (1) of each chunk: a the
     // scale (the queries' factors rq come on top), b log2 of the value's, inv 1 / that.  EACH: these differ from key to key,
     // and mask bit 8 i says whether the query sees key g + 8 i.
@@ -1565,7 +1747,7 @@ struct MmWarp {
                     for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, d));
                     const float f = mx == NEG_INF ? 1.f : ex2(m[q][e] - mx);
                     m[q][e] = mx;
-                    l[q][e] *= f;
+                    if (!far) l[q][e] *= f;
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
                         o[q][j][e] *= f;
@@ -1636,6 +1818,15 @@ struct MmWarp {
         }
         const uint32_t none[NQ][2] = {};
         uint32_t p[NC][NQ][2];
+        bool wide = far;
+#pragma unroll
+        for (int n = 0; n < NC; ++n) wide |= is_far(slots.scale[sl][n][1]);
+        if (wide) {                                       // the same in all lanes
+            if (!far) go_far();
+            far_sums<NC, false>(s, rq, aa, none);
+#pragma unroll
+            for (int n = 0; n < NC; ++n) ii[n][0] = ii[n][1] = 0.f;
+        }
         softmax<NC, false>(s, rq, aa, bb, ii, none, p);
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
@@ -1707,6 +1898,7 @@ struct MmWarp {
                 mma16816(s[0][q], bf16_f16(kw[0][2 * u], ks[0]), bf16_f16(kw[1][2 * u], ks[1]), bf16_f16(kw[0][2 * u + 1], ks[0]),
                          bf16_f16(kw[1][2 * u + 1], ks[1]), b[q][0], b[q][1]);
         }
+        bool wide = false;
         int vx[4];                                        // exponents of keys 2c, 2c + 1, 2c + 8, 2c + 9
         uint32_t vw[4][VW * 2];
 #pragma unroll
@@ -1725,6 +1917,7 @@ struct MmWarp {
             for (int d = 4; d < 32; d *= 2) mx = max(mx, __shfl_xor_sync(FULL, mx, d));
             const int ex = bits_exp(mx);
             vx[j] = ex;
+            wide |= e < keys && is_far_exp(ex);
 #pragma unroll
             for (int u = 0; u < VW * 2; ++u) vw[j][u] = bf16_f16(vw[j][u], exp2i(-ex));
         }
@@ -1740,6 +1933,11 @@ struct MmWarp {
         for (int q = 0; q < NQ; ++q)
 #pragma unroll
             for (int e = 0; e < 2; ++e) mask[q][e] = tail_bits(P, sg.b, min(8 * q + 2 * c + e, P.R - 1) / P.G, sg.q.open, tok) & 0xffffu;
+        if (far || __any_sync(FULL, wide)) {
+            if (!far) go_far();
+            far_sums<1, true>(s, rq, aa, mask);
+            ii[0][0] = ii[0][1] = 0.f;
+        }
         softmax<1, true>(s, rq, aa, bb, ii, mask, p);
 #pragma unroll
         for (int u = 0; u < VW * 2; ++u) {
@@ -1790,6 +1988,7 @@ struct MmWarp {
             m[q][0] = m[q][1] = NEG_INF;
             l[q][0] = l[q][1] = 0.f;
         }
+        far = false;
         __syncwarp();
     }
 };
@@ -1820,12 +2019,13 @@ __device__ __forceinline__ void mm_finish(const Att& P, MmWarp<D, NQ>& w, MmShar
             if (w.g == 0) {
                 sh.m[w.warp][8 * q + 2 * w.c + e] = w.m[q][e];
                 sh.l[w.warp][8 * q + 2 * w.c + e] = w.l[q][e];
+                if (!w.far) w.ref[8 * q + 2 * w.c + e] = w.own_ref(q, e);
             }
         }
     if (bad) sh.bad = 1;
     __syncthreads();
     // every warp's output on the common maximum, then warps 2 and 3 to 0 and 1, and 1 to 0
-    float mm[NQ][2], l[NQ][2];
+    float mm[NQ][2], l[NQ][2], rr[NQ][2];
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
 #pragma unroll
@@ -1833,9 +2033,12 @@ __device__ __forceinline__ void mm_finish(const Att& P, MmWarp<D, NQ>& w, MmShar
             const int row = 8 * q + 2 * w.c + e;
             mm[q][e] = fmaxf(fmaxf(sh.m[0][row], sh.m[1][row]), fmaxf(sh.m[2][row], sh.m[3][row]));
             const float base = mm[q][e] == NEG_INF ? 0.f : mm[q][e], f = ex2(w.m[q][e] - base);
+            const float ri[MM_WARPS] = {sh.slots[0].ref[row], sh.slots[1].ref[row], sh.slots[2].ref[row], sh.slots[3].ref[row]};
+            rr[q][e] = fmaxf(fmaxf(ri[0], ri[1]), fmaxf(ri[2], ri[3]));
+            const float ref = rr[q][e] == NEG_INF ? 0.f : rr[q][e];
             l[q][e] = 0.f;
 #pragma unroll
-            for (int i = 0; i < MM_WARPS; ++i) l[q][e] = fmaf(ex2(sh.m[i][row] - base), sh.l[i][row], l[q][e]);
+            for (int i = 0; i < MM_WARPS; ++i) l[q][e] = fmaf(ex2(ri[i] - ref), sh.l[i][row], l[q][e]);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 w.o[q][j][e] *= f;
@@ -1901,15 +2104,18 @@ __device__ __forceinline__ void mm_finish(const Att& P, MmWarp<D, NQ>& w, MmShar
                 }
             }
             const int64_t at = ((int64_t)g.b * P.N + n) * P.Hq + g.h * P.G + row - n * P.G;
-            const float m = mm[q][e], sum = l[q][e], inv = nan ? quiet : sum == 0.f ? 0.f : 1.f / sum;
+            const float m = mm[q][e] == NEG_INF ? NEG_INF : mm[q][e] - P_BIAS, r = rr[q][e], sum = l[q][e];
             if (whole) {
+                const float up = half_exp2(m == NEG_INF ? 0.f : m - r), inv = (nan ? quiet : sum == 0.f ? 0.f : 1.f / sum) * up;
+#pragma unroll
+                for (int j = 0; j < 2 * NT; ++j) x[j] = x[j] * up * inv;
                 char* dst = P.out + (at * D + 2 * w.g * NT) * 2;
 #pragma unroll
                 for (int j = 0; j < 2 * NT; j += 8)
                     *reinterpret_cast<uint4*>(dst + 2 * j) =
-                        make_uint4(pack_bf16(x[j] * inv, x[j + 1] * inv), pack_bf16(x[j + 2] * inv, x[j + 3] * inv),
-                                   pack_bf16(x[j + 4] * inv, x[j + 5] * inv), pack_bf16(x[j + 6] * inv, x[j + 7] * inv));
-                if (w.g == 0 && P.lse) P.lse[at] = nan ? quiet : sum == 0.f ? NEG_INF : (m - P_BIAS + log2f(sum)) * LN2;
+                        make_uint4(pack_bf16(x[j], x[j + 1]), pack_bf16(x[j + 2], x[j + 3]),
+                                   pack_bf16(x[j + 4], x[j + 5]), pack_bf16(x[j + 6], x[j + 7]));
+                if (w.g == 0 && P.lse) P.lse[at] = nan ? quiet : sum == 0.f ? NEG_INF : (r + log2f(sum)) * LN2;
             } else {
                 float* dst = part + (int64_t)row * D + 2 * w.g * NT;
 #pragma unroll
@@ -1917,8 +2123,10 @@ __device__ __forceinline__ void mm_finish(const Att& P, MmWarp<D, NQ>& w, MmShar
                     *reinterpret_cast<float4*>(dst + j) =
                         nan ? make_float4(quiet, quiet, quiet, quiet) : make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
                 if (w.g == 0) {
-                    part[(int64_t)P.R * D + row] = m == NEG_INF ? NEG_INF : m - P_BIAS;
-                    part[(int64_t)P.R * D + P.R + row] = nan ? quiet : sum;
+                    float* stat = part + (int64_t)P.R * D + row;
+                    stat[0] = m;
+                    stat[P.R] = nan ? quiet : m == r ? sum : -sum;
+                    if (m != r) stat[2 * P.R] = r;
                 }
             }
         }
@@ -1955,7 +2163,7 @@ __global__ void __launch_bounds__(MM_BT, MM_CTAS_SM) k_attention_mma(const Att P
         proxy_fence();
     }
     __syncthreads();
-    MmWarp<D, NQ> w(P, threadIdx.x >> 5, sh.ahead[threadIdx.x >> 5]);
+    MmWarp<D, NQ> w(P, threadIdx.x >> 5, sh.ahead[threadIdx.x >> 5], sh.slots[threadIdx.x >> 5]);
     MmRing<D>& ring = sh.ring[w.warp];
     MmSlots& slots = sh.slots[w.warp];
     w.begin(st);

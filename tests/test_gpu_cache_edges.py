@@ -1,0 +1,61 @@
+"""The cache calls at the edges of what their documentation allows.  Tolerances as in test_gpu_cache.py, whose
+inputs and checks are used."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import cache_ref as ref
+from test_gpu_cache import BF, check_attention, make_cache, workspace
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def spec(cuda_device):
+    import speculative_decoding_verify_temperature_b200 as s
+    return s
+
+
+# ----------------------------------------------------------------------------- values of any magnitude
+
+def far_values(spec, N, Hq, Hkv, D, page, length, blocks, tail, nodes, seed=0):
+    """One sequence whose cached values are multiplied by powers of two: 2^blocks[i mod n] in block i, 2^tail in the open
+    block, 2^nodes[i mod n] in node i."""
+    g = torch.Generator().manual_seed(seed)
+    c = make_cache(spec, 1, Hkv, D, page, max(length // page, 1), np.random.RandomState(seed))
+    r = ref.Cache(1, Hkv, D, page)
+    full = length // page * page
+    e = [blocks[t // page % len(blocks)] if t < full else tail for t in range(length)]
+    scale = torch.exp2(torch.tensor(e, dtype=torch.float64))[:, None, None]
+    k = torch.randn((length, Hkv, D), generator=g).to(BF)
+    v = (torch.randn((length, Hkv, D), generator=g).double() * scale).to(BF)
+    if length:
+        spec.spec_kv_append(k[None].cuda(), v[None].cuda(), None, c)
+        r.append(0, k, v)
+    q, nk = torch.randn((1, N, Hq, D), generator=g).to(BF), torch.randn((1, N, Hkv, D), generator=g).to(BF)
+    ne = torch.exp2(torch.tensor([nodes[i % len(nodes)] for i in range(N)], dtype=torch.float64))
+    nv = (torch.randn((1, N, Hkv, D), generator=g).double() * ne[None, :, None, None]).to(BF)
+    return c, r, q, nk, nv
+
+
+FAR = [  # cached, exponents of the full blocks, of the open block, of the nodes
+    (0, [0], 0, [-117]), (0, [0], 0, [-126, -118]), (1, [0], -119, [-119]), (300, [-118], -118, [-118]),
+    (300, [-126, -110], -100, [-122]), (300, [-125, 20], 10, [15, -120]), (300, [20, -125, -125, -125], -125, [-125]),
+    (300, [110, -120], -126, [100, -118]), (300, [118], 118, [118]), (333, [0, -118], -118, [0]), (9000, [-118, 30], 0, [-117]),
+    (9000, [-118], -118, [-118]), (20000, [-60, -120, 60], 3, [1, -1, 90])]
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,D,page", [(1, 8, 2, 128, 16), (3, 8, 2, 64, 32), (5, 6, 2, 128, 64), (20, 8, 2, 128, 128),
+                                             (33, 8, 2, 64, 16), (70, 4, 1, 128, 32)])
+@pytest.mark.parametrize("length,blocks,tail,nodes", FAR)
+def test_attention_of_far_values(spec, N, Hq, Hkv, D, page, length, blocks, tail, nodes):
+    """Values of any magnitude that bf16 and the pages' scales hold, in one row's reach: neither the log-sum-exp, which has
+    nothing to do with the values, nor the outputs lose a key."""
+    c, r, q, k, v = far_values(spec, N, Hq, Hkv, D, page, length, blocks, tail, nodes)
+    mask = torch.tril(torch.ones(N, N, dtype=torch.bool))[None]
+    ws = workspace(spec, 1, N, Hq, D)
+    out, lse = spec.spec_tree_attention(q.cuda(), k.cuda(), v.cuda(), c, ref.pack(mask).cuda(), return_lse=True, workspace=ws)
+    check_attention(r, [length], q, k, v, mask, out, lse, 1 / math.sqrt(D))
+    assert spec.spec_read_device_status(ws) == 0
