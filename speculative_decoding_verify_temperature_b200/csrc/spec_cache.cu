@@ -416,11 +416,9 @@ __global__ void __launch_bounds__(AP_BT, R <= 4 ? 3 : 2) k_append(const Append P
 template <int DT, int R>
 spec_status launch_append_rows(const Append& P, dim3 grid, cudaStream_t st) {
     const size_t smem = (size_t)(P.page + 1 + P.page / 8 + 8) * (P.rot / 2) * sizeof(float2);   // up to 76.5 KB
-    if (smem > 48 * 1024) {
-        static std::atomic<uint64_t> done{0};
-        if (const spec_status s = sv_host::allow_smem(reinterpret_cast<const void*>(k_append<DT, R>), "k_append", 80 * 1024, done))
-            return s;
-    }
+    // asked for whatever this call needs: the kernel's static shared memory counts towards the 48 KB too
+    static std::atomic<uint64_t> done{0};
+    if (const spec_status s = sv_host::allow_smem(reinterpret_cast<const void*>(k_append<DT, R>), "k_append", 80 * 1024, done)) return s;
     k_append<DT, R><<<grid, AP_BT, smem, st>>>(P);
     return sv_host::launched("k_append");
 }

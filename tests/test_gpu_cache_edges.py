@@ -59,3 +59,20 @@ def test_attention_of_far_values(spec, N, Hq, Hkv, D, page, length, blocks, tail
     out, lse = spec.spec_tree_attention(q.cuda(), k.cuda(), v.cuda(), c, ref.pack(mask).cuda(), return_lse=True, workspace=ws)
     check_attention(r, [length], q, k, v, mask, out, lse, 1 / math.sqrt(D))
     assert spec.spec_read_device_status(ws) == 0
+
+
+# ----------------------------------------------------------------------------- append
+
+@pytest.mark.parametrize("rot", range(0, 129, 16))
+@pytest.mark.parametrize("dt", [torch.float32, BF])
+def test_append_every_rotated_width(spec, rot, dt):
+    """Every width of rotation at the largest page and head: what a call needs of shared memory it asks for itself."""
+    D = page = 128
+    k, v = torch.randn(1, page + 3, 1, D).to(dt), torch.randn(1, page + 3, 1, D).to(dt)
+    c = make_cache(spec, 1, 1, D, page, 1, np.random.RandomState(rot))
+    freq = ref.inv_freq(rot) if rot else None
+    spec.spec_kv_append(k.cuda(), v.cuda(), None, c, inv_freq=None if freq is None else freq.cuda())
+    assert c.lengths.tolist() == [page + 3]
+    e, mag = ref.norm_rope(k[0], torch.arange(page + 3), freq, None, 1e-6, False)
+    got = c.k_open[0][:, page:page + 3].transpose(0, 1).cpu().double()
+    assert ((got - e[page:]).abs() <= e[page:].abs() * 2.0 ** -8 + mag[page:] * 2.0 ** -19).all()
