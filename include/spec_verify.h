@@ -611,7 +611,7 @@ size_t spec_cache_workspace_bytes(int B, int N, int q_heads, int head_dim);
  * parents        [B, N] int32 as in spec_verify_tree_*; NULL = chains (the
  *                parent of n is n - 1, max_depth is not looked at).
  * lengths        [B] int32: cached tokens (the root's position); negative =
- *                no sequence in this row.
+ *                no sequence in this row (its parents are not looked at).
  * out_positions  [B, N] int32: lengths[b] + depth(n); -1 in every node of a row
  *                without a sequence or with an invalid one.
  * out_ancestors  [B, N, ceil(N/32)] int32 words: bit (m mod 32) of word m / 32 of

@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(SPEC_MAX_NODES) k_tree_plan(int N, int max_dep
     const int len = lengths[b];
     int p = -1;
     bool bad = len >= SPEC_MAX_CACHE_LEN;
-    if (n < N) {
+    if (n < N && len >= 0) {              // the parents of a row without a sequence are not looked at
         p = parents ? parents[(int64_t)b * N + n] : n - 1;
         bad |= n == 0 ? p != -1 : (p < 0 || p >= n);
         par[n] = p;

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import cache_ref as ref
-from test_gpu_cache import BF, check_attention, make_cache, workspace
+from test_gpu_cache import BF, check_attention, flagged, gpu, make_cache, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +76,15 @@ def test_append_every_rotated_width(spec, rot, dt):
     e, mag = ref.norm_rope(k[0], torch.arange(page + 3), freq, None, 1e-6, False)
     got = c.k_open[0][:, page:page + 3].transpose(0, 1).cpu().double()
     assert ((got - e[page:]).abs() <= e[page:].abs() * 2.0 ** -8 + mag[page:] * 2.0 ** -19).all()
+
+
+# ----------------------------------------------------------------------------- plan
+
+def test_plan_of_a_row_without_a_sequence(spec):
+    """A padded row's parents are not looked at: it gets its -1 and zeros, and nothing is reported."""
+    parents = np.tile(np.arange(-1, 7, dtype=np.int32), (3, 1))
+    parents[1] = 1 << 20
+    ws = workspace(spec)
+    pos, anc = spec.spec_tree_plan(gpu(parents), gpu(np.array([4, -1, 9], dtype=np.int32)), 8, workspace=ws)
+    assert (pos[1] == -1).all() and (anc[1] == 0).all() and not flagged(spec, ws)
+    assert pos[0].tolist() == list(range(4, 12)) and pos[2].tolist() == list(range(9, 17))
