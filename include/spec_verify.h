@@ -574,6 +574,11 @@ spec_status spec_vp_chain_finish(int B, int gamma, int V_shard, const int32_t* t
  * the limit) get NaN in every attention output, or length -1 and no write from
  * an append; the SPEC_ERR_DEVICE_INPUT bit is set in the workspace.
  *
+ * Every wait of spec_tree_attention on the device is bounded (2^24 polls and
+ * 1 s).  One that gives up sets SPEC_ERR_TIMEOUT (and SPEC_ERR_COPY_IN_FLIGHT
+ * if a copy of its own may still be under way) in the workspace; the rows that it
+ * could have reached get NaN in out and lse.
+ *
  * One workspace of spec_cache_workspace_bytes serves all four calls of a round,
  * for one stream at a time; spec_workspace_init clears it once.
  */
@@ -742,7 +747,8 @@ spec_status spec_profile_events(void* start_event, void* stop_event);
  * wait again with the full budget so that the copy lands before the CTA goes
  * on (else also (1 << SPEC_ERR_COPY_IN_FLIGHT)), and then read the staged
  * statistics from global memory instead, or give up on the sequence (-1 in
- * its outputs) when the staged row pair was lost.  tries = 0 makes every first
+ * its outputs) when the staged row pair was lost; spec_tree_attention does the
+ * same for the copies of the cache's pages (NaN in its outputs).  tries = 0 makes every first
  * wait give up at once while the copies land normally, which drives that
  * path without making any copy late; tries < 0 restores the default.
  * Applies to later calls on the calling host thread.  Not for production use.

@@ -17,6 +17,8 @@ SV_HIDDEN spec_status fail(spec_status st, const char* fmt, ...) __attribute__((
 // After a launch: the runtime's verdict, and one more in spec_launch_count().
 SV_HIDDEN spec_status launched(const char* what);
 SV_HIDDEN int num_sms();
+// Polls of the first wait for copied bytes (spec_debug_wait_budget of the calling thread).
+SV_HIDDEN unsigned wait_tries();
 // NVTX range of one C-ABI call.
 SV_HIDDEN void range_push(const char* name);
 SV_HIDDEN void range_pop();

@@ -16,6 +16,7 @@ spec_status fail(spec_status st, const char* fmt, ...) {
 }
 spec_status launched(const char* what) { return ::launched(what); }
 int num_sms() { return ::num_sms(); }
+unsigned wait_tries() { return g_wait_tries; }
 void range_push(const char* name) { nvtxRangePushA(name); }
 void range_pop() { nvtxRangePop(); }
 

@@ -27,6 +27,7 @@ struct Att {
     char* out;
     float* lse;
     unsigned* status;
+    unsigned wait_tries;                  // polls of the first wait for copied bytes
     struct Cut* cut;                      // [gridDim.x] the item that a CTA begins and does not end
     float* partial;                       // [gridDim.x][2][rows of an item][D + 3]
 };
@@ -361,7 +362,10 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
 
 // Barriers.  Every wait is bounded: when one gives up, the CTA's `abort` is set
 // and all waits return at once; every role then runs through its (finite) loops
-// with whatever is there, and the status word says that the results are void.
+// with whatever is there, the rows' results become NaN and the status word says why.  What a role arrives with after such a
+// wait comes after `abort`, so whoever takes it for the real thing finds `abort` set at the rows' end.  Barriers that count
+// arrivals alone stay in order whatever arrives; those that count bytes too (kf, rf) would not, so nobody arrives there and no copy is
+// sent after a failed wait.
 constexpr unsigned WAIT_TRIES = 1u << 24;
 constexpr unsigned long long WAIT_NS = 1000000000ull;
 __device__ __forceinline__ void bar_init(uint64_t* b, unsigned n) {
@@ -395,14 +399,16 @@ __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
                  "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(b)), "r"(parity) : "memory");
     return ok != 0;
 }
+__device__ __forceinline__ bool aborted(const TcShared& sh) { return *reinterpret_cast<const volatile int*>(&sh.abort) != 0; }
 __device__ __forceinline__ unsigned long long global_ns() {
     unsigned long long t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
 }
-__device__ __noinline__ bool bar_wait_slow(uint64_t* b, uint32_t parity, volatile int* abort) {
+__device__ __noinline__ bool bar_wait_slow(uint64_t* b, uint32_t parity, volatile int* abort, unsigned tries = WAIT_TRIES) {
+    if (abort && *abort) return false;
     const unsigned long long t0 = global_ns();
-    for (unsigned i = 0; i < WAIT_TRIES; ++i) {
+    for (unsigned i = 0; i < tries; ++i) {
         if (bar_try(b, parity)) return true;
         if ((i & 63) == 63) {
             if (abort && *abort) return false;
@@ -415,6 +421,11 @@ __device__ __noinline__ bool bar_wait_slow(uint64_t* b, uint32_t parity, volatil
 // issue) wants them together.
 __device__ __forceinline__ void bar_wait(uint64_t* b, uint32_t parity, TcShared& sh) {
     if (!bar_try(b, parity) && !bar_wait_slow(b, parity, &sh.abort)) *reinterpret_cast<volatile int*>(&sh.abort) = 1;
+    __syncwarp();
+}
+// The first wait for bytes that were copied: `tries` polls (a testing hook: 0 gives up at once).
+__device__ __forceinline__ void bar_wait_copy(uint64_t* b, uint32_t parity, TcShared& sh, unsigned tries) {
+    if (tries == 0 || (!bar_try(b, parity) && !bar_wait_slow(b, parity, &sh.abort, tries))) *reinterpret_cast<volatile int*>(&sh.abort) = 1;
     __syncwarp();
 }
 
@@ -556,14 +567,20 @@ __device__ void tc_copy_pages(const Att& P, const CUtensorMap* kmap, TcShared& s
     u.begin(P, st);
     const uint32_t bytes = (uint32_t)D << P.pshift;
     int nk = 0, nv = 0, ahead = -2, ahead_t = -1, ahead_b = -1;
+    unsigned k_sent = 0, v_sent = 0;                      // of the last units, bit 0 the last: whether a copy was sent there
+    bool ok = true;                                       // no wait of the CTA has been given up
+    auto wait = [&](uint64_t* b, uint32_t parity) {
+        bar_wait(b, parity, sh);
+        ok = __all_sync(FULL, ok && !aborted(sh));
+    };
     while (u.next(P)) {
         // The tail does not lie in pages; it takes two units of keys, which this warp sees pass: a barrier's parity
         // says nothing to a waiter that is two phases behind or ahead.  So it also arrives at the units, which cannot be
         // used, and their barriers cannot go on, before it has.
         if (!u.cached()) {
-            for (int i = 0; i < 2; ++i, ++nk) {
-                bar_wait(&sh.ke[nk % KR], ((nk / KR) & 1) ^ 1, sh);
-                if (lane == 0) bar_arrive(&sh.kf[nk % KR]);
+            for (int i = 0; i < 2; ++i, ++nk, k_sent <<= 1) {
+                wait(&sh.ke[nk % KR], ((nk / KR) & 1) ^ 1);
+                if (lane == 0 && ok) bar_arrive(&sh.kf[nk % KR]);
             }
             continue;
         }
@@ -571,32 +588,35 @@ __device__ void tc_copy_pages(const Att& P, const CUtensorMap* kmap, TcShared& s
         ahead = page_entry(P, u.g, u.t + 1, lane);        // on its way for the tile after
         ahead_b = u.g.b;
         ahead_t = u.t + 1;
-        const bool ok = page >= 0 && page < P.c.num_pages;
-        if (page != -2 && !ok) sh.bad_seg[u.seg & 7] = u.seg + 1;
-        const uint32_t all = __popc(__ballot_sync(FULL, ok)) * bytes;
+        const bool there = page >= 0 && page < P.c.num_pages;
+        if (page != -2 && !there) sh.bad_seg[u.seg & 7] = u.seg + 1;
+        const uint32_t all = __popc(__ballot_sync(FULL, there)) * bytes;
         const int ks = nk % KR, vs = nv % VR;
         const int64_t ph = (int64_t)page * P.Hkv + u.g.h;
-        bar_wait(&sh.ke[ks], ((nk / KR) & 1) ^ 1, sh);
-        if (lane == 0) {
+        wait(&sh.ke[ks], ((nk / KR) & 1) ^ 1);
+        k_sent = k_sent << 1 | ok;
+        if (lane == 0 && ok) {
             bar_arrive(&sh.kf[ks]);                       // in the place of the operand warps
             bar_expect(&sh.kf[ks], all);
         }
         __syncwarp();
-        if (ok) tensor_copy(base + Tc<D>::K + ks * Tc<D>::RAW_B + lane * bytes, kmap, (int)(ph << P.pshift), &sh.kf[ks]);
-        bar_wait(&sh.re[vs], ((nv / VR) & 1) ^ 1, sh);
-        if (lane == 0) bar_expect(&sh.rf[vs], all);
+        if (ok && there) tensor_copy(base + Tc<D>::K + ks * Tc<D>::RAW_B + lane * bytes, kmap, (int)(ph << P.pshift), &sh.kf[ks]);
+        wait(&sh.re[vs], ((nv / VR) & 1) ^ 1);
+        v_sent = v_sent << 1 | ok;
+        if (lane == 0 && ok) bar_expect(&sh.rf[vs], all);
         __syncwarp();
-        if (ok) bulk_copy(base + Tc<D>::RAW + vs * Tc<D>::RAW_B + lane * bytes, static_cast<const char*>(P.c.v_pages) + ph * bytes,
+        if (ok && there) bulk_copy(base + Tc<D>::RAW + vs * Tc<D>::RAW_B + lane * bytes, static_cast<const char*>(P.c.v_pages) + ph * bytes,
                           bytes, &sh.rf[vs]);
         ++nk;
         ++nv;
     }
-    // also after a wait that gave up: no copy is in flight when the CTA ends.  (A key unit that the tail filled is
-    // waited for too: its writers arrive as well.)
-    for (int i = max(0, nk - KR); i < nk; ++i)
-        if (!bar_try(&sh.kf[i % KR], (i / KR) & 1)) bar_wait_slow(&sh.kf[i % KR], (i / KR) & 1, nullptr);
-    for (int i = max(0, nv - VR); i < nv; ++i)
-        if (!bar_try(&sh.rf[i % VR], (i / VR) & 1)) bar_wait_slow(&sh.rf[i % VR], (i / VR) & 1, nullptr);
+    // also after a wait that gave up: no copy is in flight when the CTA ends
+    bool landed = true;
+    for (int i = nk - 1; i >= max(0, nk - KR); --i, k_sent >>= 1)
+        if (k_sent & 1) landed &= bar_try(&sh.kf[i % KR], (i / KR) & 1) || bar_wait_slow(&sh.kf[i % KR], (i / KR) & 1, nullptr);
+    for (int i = nv - 1; i >= max(0, nv - VR); --i, v_sent >>= 1)
+        if (v_sent & 1) landed &= bar_try(&sh.rf[i % VR], (i / VR) & 1) || bar_wait_slow(&sh.rf[i % VR], (i / VR) & 1, nullptr);
+    if (!landed) atomicOr(P.status, 1u << SPEC_ERR_COPY_IN_FLIGHT);
 }
 
 __device__ __forceinline__ void prefetch_row(const char* p, int bytes) {
@@ -908,8 +928,10 @@ struct TcConv {
         }
         if (tid == 0) {
             bar_arrive(&sh.mf[m]);
-            bar_arrive(&sh.kf[k0]);
-            bar_arrive(&sh.kf[k1]);
+            if (!aborted(sh)) {                           // else these units may not be free
+                bar_arrive(&sh.kf[k0]);
+                bar_arrive(&sh.kf[k1]);
+            }
         }
         if (lane == 0) bar_arrive(&sh.vf[u.gt & 1]);
     }
@@ -938,7 +960,7 @@ struct TcConv {
             }
             ++nk;
             const int s = nv % VR;
-            bar_wait(&sh.rf[s], (nv / VR) & 1, sh);
+            bar_wait_copy(&sh.rf[s], (nv / VR) & 1, sh, P.wait_tries);
             bar_wait(&sh.ve[u.gt & 1], ((u.gt >> 1) & 1) ^ 1, sh);
             put(base + Tc<D>::V + (u.gt & 1) * Tc<D>::V_B, base + Tc<D>::RAW + s * Tc<D>::RAW_B, u.g.q.full - u.t * TILE);
             __syncwarp();
@@ -1242,7 +1264,7 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
                 const int parts = tl < nc ? 1 : 2, nk = nk0 + tl + max(0, tl - nc);
                 for (int part = 0; part < parts; ++part) {
                     const int s = (nk + part) % KR;
-                    bar_wait(&sh.kf[s], ((nk + part) / KR) & 1, sh);
+                    bar_wait_copy(&sh.kf[s], ((nk + part) / KR) & 1, sh, P.wait_tries);
                     tc_after();
                     const uint64_t k = kd + s * (Tc<D>::RAW_B >> 4);
 #pragma unroll
@@ -1372,10 +1394,11 @@ __global__ void __launch_bounds__(TC_BT, 1) k_attention_tc(const Att P, const __
                 lift = lift_of(m, sh.far[2][i][r]);
             }
             const bool whole = g.whole();
-            const bool nan = g.q.bad || *reinterpret_cast<volatile int*>(&sh.bad_seg[seg & 7]) == seg + 1;
-            if (nan && r == 0) atomicOr(P.status, 1u << SPEC_ERR_DEVICE_INPUT);
+            const bool invalid = g.q.bad || *reinterpret_cast<volatile int*>(&sh.bad_seg[seg & 7]) == seg + 1;
+            if (invalid && r == 0) atomicOr(P.status, 1u << SPEC_ERR_DEVICE_INPUT);
+            const bool nan = invalid || aborted(sh);
             uint32_t bad_v = 0;
-            if (g.t1 > g.q.nct) {
+            if (g.t1 > g.q.nct && !nan) {
 #pragma unroll
                 for (int w = 0; w < 12; ++w) bad_v |= sh.bad_v[seg & 3][w];
             }
@@ -2176,10 +2199,10 @@ __global__ void __launch_bounds__(MM_BT, MM_CTAS_SM) k_attention_mma(const Att P
     Part y{};
     idy = -2;
     if (x.kind()) y = w.next(idy);
-    bool bad = false;
+    bool bad = false, lost = false;                       // lost: a copy that did not land; nothing is sent after it
     unsigned full = 0;                                    // parity of each slot's next phase
     for (int s = 0; x.kind(); s ^= 1) {
-        w.fetch(y, idy, s ^ 1, ring, slots, &kmap, &vmap);
+        if (!lost) w.fetch(y, idy, s ^ 1, ring, slots, &kmap, &vmap);
         if (x.parity() != parity) {
             parity = x.parity();
             w.load_q(sh.now.s, qf, rq);
@@ -2188,12 +2211,17 @@ __global__ void __launch_bounds__(MM_BT, MM_CTAS_SM) k_attention_mma(const Att P
         int idz = -2;
         if (y.kind()) z = w.next(idz);
         if (x.kind() == 1) {
-            if (!bar_try(&slots.full[s], full >> s & 1) && !bar_wait_slow(&slots.full[s], full >> s & 1, nullptr)) {
+            const bool came = !lost && P.wait_tries != 0 &&
+                              (bar_try(&slots.full[s], full >> s & 1) || bar_wait_slow(&slots.full[s], full >> s & 1, nullptr, P.wait_tries));
+            if (!__all_sync(FULL, came)) {
                 bad = true;
-                atomicOr(P.status, 1u << SPEC_ERR_TIMEOUT);   // let it land (bounded), whatever becomes of the result
-                if (!bar_wait_slow(&slots.full[s], full >> s & 1, nullptr)) atomicOr(P.status, 1u << SPEC_ERR_COPY_IN_FLIGHT);
+                if (!lost) {                              // let them land (bounded), whatever becomes of the result
+                    bool landed = bar_wait_slow(&slots.full[s], full >> s & 1, nullptr);
+                    if (y.kind() == 1) landed &= bar_wait_slow(&slots.full[s ^ 1], full >> (s ^ 1) & 1, nullptr);
+                    lost = __any_sync(FULL, !landed);
+                    if (w.lane == 0) atomicOr(P.status, (1u << SPEC_ERR_TIMEOUT) | (lost ? 1u << SPEC_ERR_COPY_IN_FLIGHT : 0u));
+                }
             }
-            __syncwarp();
             full ^= 1u << s;
             const unsigned there = __ballot_sync(FULL, id >= 0 && id < P.c.num_pages) & 3u, none = __ballot_sync(FULL, id == -2) & 3u;
             bad |= (there | none) != 3u;
@@ -2356,6 +2384,7 @@ spec_status spec_tree_attention(int B, int N, int q_heads, const spec_kv_cache* 
     P.lse = lse;
     char* ws = static_cast<char*>(workspace);
     P.status = reinterpret_cast<unsigned*>(ws + sv_host::CACHE_WS_STATUS);
+    P.wait_tries = sv_host::wait_tries();
     P.cut = reinterpret_cast<Cut*>(ws + sv_host::CACHE_WS_CUT);
     P.partial = reinterpret_cast<float*>(ws + sv_host::CACHE_WS_PARTIAL);
     cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -203,7 +203,7 @@ def spec_debug_bounds_hits() -> int | None:
 
 def spec_debug_wait_budget(tries: int = -1) -> None:
     """Testing hook: polls of the first wait for each bulk copy the finalize
-    kernels issue, for later calls on this thread (0 = give up at once and take
+    kernels and the tree attention issue, for later calls on this thread (0 = give up at once and take
     the timeout path; negative = the default budget)."""
     _check(lib().spec_debug_wait_budget(int(tries)), "spec_debug_wait_budget")
 

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import cache_ref as ref
-from test_gpu_cache import BF, check_attention, flagged, gpu, make_cache, workspace
+from test_gpu_cache import BF, attention_inputs, check_attention, flagged, gpu, make_cache, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +88,36 @@ def test_plan_of_a_row_without_a_sequence(spec):
     pos, anc = spec.spec_tree_plan(gpu(parents), gpu(np.array([4, -1, 9], dtype=np.int32)), 8, workspace=ws)
     assert (pos[1] == -1).all() and (anc[1] == 0).all() and not flagged(spec, ws)
     assert pos[0].tolist() == list(range(4, 12)) and pos[2].tolist() == list(range(9, 17))
+
+
+# ----------------------------------------------------------------------------- waits that give up
+
+TIMEOUT, IN_FLIGHT = 1 << 5, 1 << 7
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,D,page,lengths", [
+    (1, 8, 2, 128, 16, [40, 100, 7, 900]), (3, 8, 2, 64, 32, [3000, 65]), (20, 8, 2, 128, 16, [40, 100, 7, 900]),
+    (20, 8, 2, 64, 128, [500, 20000]), (70, 4, 1, 128, 64, [300, 2000]), (24, 8, 2, 128, 32, [(i * 97) % 700 for i in range(90)])])
+def test_attention_says_when_a_wait_gave_up(spec, N, Hq, Hkv, D, page, lengths):
+    """With no patience for a copy (the copies land as ever) the call ends, its rows are NaN, and the status word says so;
+    no copy is left in flight, and the next call on the same workspace is clean."""
+    c, r, q, k, v, mask = attention_inputs(spec, len(lengths), N, Hq, Hkv, D, page, lengths, 11 * N + D)
+    ws = workspace(spec, len(lengths), N, Hq, D)
+    args = (q.cuda(), k.cuda(), v.cuda(), c, ref.pack(mask).cuda())
+    clean, clean_lse = spec.spec_tree_attention(*args, return_lse=True, workspace=ws)
+    assert spec.spec_read_device_status(ws) == 0
+    spec.spec_debug_wait_budget(0)
+    try:
+        out, lse = spec.spec_tree_attention(*args, return_lse=True, workspace=ws)
+    finally:
+        spec.spec_debug_wait_budget(-1)
+    status = spec.spec_read_device_status(ws)
+    assert status & TIMEOUT and not status & IN_FLIGHT, status
+    for b, n in enumerate(lengths):
+        if n >= page:                                     # the row needed a copy
+            assert torch.isnan(out[b]).all() and torch.isnan(lse[b]).all()
+        else:
+            assert torch.isnan(out[b]).all() or torch.equal(out[b], clean[b])
+    again, again_lse = spec.spec_tree_attention(*args, return_lse=True, workspace=ws)
+    assert spec.spec_read_device_status(ws) == 0
+    assert torch.equal(again, clean) and torch.equal(again_lse, clean_lse)
