@@ -7,6 +7,7 @@ round; ``workloads`` makes the seeded synthetic inputs.
 from . import workloads  # noqa: F401
 from .kv_cache import (  # noqa: F401
     KvCache,
+    spec_cache_status,
     spec_cache_workspace_bytes,
     spec_kv_append,
     spec_qk_norm_rope,

@@ -14,8 +14,9 @@ One round of a layer, ``parents`` [B, N] and a ``KvCache`` in hand::
 Argument checks happen before anything is enqueued.  Calls run on
 ``torch.cuda.current_stream`` of the tensors' device unless a stream is given;
 outputs are allocated on that stream.  Without a ``workspace`` each (device,
-stream) has one of its own, and a call that is being captured into a CUDA
-graph gets one that belongs to the graph.
+stream) has one of its own, whose status word ``spec_cache_status`` reads, and a
+call that is being captured into a CUDA graph gets one that belongs to the
+graph (give it a ``workspace`` to read the status of its replays).
 """
 from __future__ import annotations
 
@@ -25,7 +26,7 @@ import math
 
 import torch
 
-from .spec_verify import SPEC_BF16, SPEC_F32, _check, _dtype, lib, spec_workspace_init
+from .spec_verify import SPEC_BF16, SPEC_F32, _check, _dtype, lib, spec_read_device_status, spec_workspace_init
 
 _I32, _F32 = torch.int32, torch.float32
 
@@ -196,10 +197,26 @@ def _workspace(workspace, device, handle, B, N, q_heads, head_dim):
         buf = torch.empty(need, dtype=torch.uint8, device=device)
         spec_workspace_init(buf)
     elif buf is None or buf.numel() < need:
-        buf = torch.empty(need, dtype=torch.uint8, device=device)
+        old, buf = buf, torch.empty(need, dtype=torch.uint8, device=device)
         spec_workspace_init(buf)
+        if old is not None:
+            buf[:4].copy_(old[:4])                 # what earlier calls reported stays readable
         _cache_ws[at] = buf
     return buf
+
+
+def spec_cache_status(device=None, stream=None) -> int:
+    """The status bits (``1 << code``) that cache calls without a ``workspace`` have set on this stream (default: the
+    device's current one) since the last read; clears them and synchronises the stream.  0 if there was no such call."""
+    device = torch.device("cuda" if device is None else device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    handle, current = _on(device, stream)
+    buf = _cache_ws.get((device.index, handle))
+    if buf is None:
+        return 0
+    with current:
+        return spec_read_device_status(buf)
 
 
 def spec_tree_plan(parents, lengths, max_depth: int = 64, *, N: int | None = None, out_positions=None,

@@ -121,3 +121,24 @@ def test_attention_says_when_a_wait_gave_up(spec, N, Hq, Hkv, D, page, lengths):
     again, again_lse = spec.spec_tree_attention(*args, return_lse=True, workspace=ws)
     assert spec.spec_read_device_status(ws) == 0
     assert torch.equal(again, clean) and torch.equal(again_lse, clean_lse)
+
+
+# ----------------------------------------------------------------------------- workspaces and streams
+
+def test_status_of_calls_without_a_workspace(spec):
+    """What a call without a workspace reports can be read, per stream, also after that workspace has grown."""
+    side = torch.cuda.Stream()
+    parents = gpu(np.array([[-1, 5]], dtype=np.int32))
+    lengths = gpu(np.array([3], dtype=np.int32))
+    spec.spec_cache_status(), spec.spec_cache_status(stream=side)        # what other tests left
+    spec.spec_tree_plan(parents, lengths, 4)
+    assert spec.spec_cache_status() == 1 << 4 and spec.spec_cache_status() == 0
+    spec.spec_tree_plan(parents, lengths, 4, stream=side)
+    assert spec.spec_cache_status() == 0
+    c, r, q, k, v, mask = attention_inputs(spec, 1, 200, 8, 1, 128, 16, [40], 1)
+    torch.cuda.synchronize()
+    spec.spec_tree_attention(q.cuda(), k.cuda(), v.cuda(), c, ref.pack(mask).cuda(), stream=side)     # needs a larger one
+    assert spec.spec_cache_status("cuda", side) == 1 << 4 and spec.spec_cache_status("cuda", side) == 0
+    with torch.cuda.stream(side):
+        spec.spec_tree_plan(parents, lengths, 4)
+        assert spec.spec_cache_status() == 1 << 4
