@@ -580,7 +580,8 @@ spec_status spec_vp_chain_finish(int B, int gamma, int V_shard, const int32_t* t
  * could have reached get NaN in out and lse.
  *
  * One workspace of spec_cache_workspace_bytes serves all four calls of a round,
- * for one stream at a time; spec_workspace_init clears it once.
+ * for one stream at a time; spec_workspace_init clears it once.  Only its first
+ * SPEC_CACHE_STATE_BYTES (status word and counters) have to be zero.
  */
 typedef struct spec_kv_cache {
     void* k_pages;
@@ -602,6 +603,7 @@ typedef struct spec_kv_cache {
 } spec_kv_cache;
 
 #define SPEC_MAX_CACHE_LEN (1 << 30)
+#define SPEC_CACHE_STATE_BYTES 65792
 #define SPEC_MAX_HEADS 1024
 
 /*

@@ -71,12 +71,13 @@ inline spec_status make_rows(const char* what, const void* p, const int64_t* str
 // The workspace of the cache calls: the status word (the word that
 // spec_read_device_status reads), an append's arrival counters (one per
 // sequence; zero between calls), the attention's records of items that several CTAs
-// share and their partial results.  The counters lie at the same place for
+// share and their partial results (both written by every call before it reads them).  The counters lie at the same place for
 // every shape, so that a workspace can serve calls of different sizes.
 constexpr int ATT_MAX_CTAS = 1024;
 constexpr int CACHE_MAX_B = 16384;
 constexpr size_t CACHE_WS_STATUS = 0, CACHE_WS_SEQ = 256, CACHE_WS_CUT = CACHE_WS_SEQ + 4 * CACHE_MAX_B,
                  CACHE_WS_PARTIAL = CACHE_WS_CUT + 32 * ATT_MAX_CTAS;
+static_assert(CACHE_WS_CUT == SPEC_CACHE_STATE_BYTES, "what has to be zero comes first");
 SV_HIDDEN spec_status check_cache_ws(void* ws, size_t bytes, size_t need);
 SV_HIDDEN spec_status check_cache(const spec_kv_cache* c, int B);
 

@@ -162,6 +162,7 @@ def spec_cache_workspace_bytes(B: int, N: int, q_heads: int, head_dim: int) -> i
 
 _cache_ws = {}
 _ws_bytes = {}
+_STATE_BYTES = 65792                               # SPEC_CACHE_STATE_BYTES
 
 
 _same = contextlib.nullcontext()
@@ -195,10 +196,10 @@ def _workspace(workspace, device, handle, B, N, q_heads, head_dim):
     buf = _cache_ws.get(at)
     if torch._C._cuda_isCurrentStreamCapturing():  # replays of several graphs may overlap: one each
         buf = torch.empty(need, dtype=torch.uint8, device=device)
-        spec_workspace_init(buf)
+        spec_workspace_init(buf[:_STATE_BYTES])    # part of every replay: no more than has to be zero
     elif buf is None or buf.numel() < need:
         old, buf = buf, torch.empty(need, dtype=torch.uint8, device=device)
-        spec_workspace_init(buf)
+        spec_workspace_init(buf[:_STATE_BYTES])
         if old is not None:
             buf[:4].copy_(old[:4])                 # what earlier calls reported stays readable
         _cache_ws[at] = buf

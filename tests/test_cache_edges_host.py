@@ -1,0 +1,24 @@
+"""The cache calls' host side at the edges of what their documentation allows (no GPU needed)."""
+import os
+import re
+
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.mark.parametrize("capturing", [True, False])
+def test_a_new_workspace_clears_its_state_only(monkeypatch, capturing):
+    """The calls of a captured round clear their workspaces in every replay: status word and counters, not the partial results."""
+    from speculative_decoding_verify_temperature_b200 import build, kv_cache
+    build.build()
+    header = open(os.path.join(ROOT, "include", "spec_verify.h")).read()
+    state = int(re.search(r"#define SPEC_CACHE_STATE_BYTES (\d+)", header).group(1))
+    cleared = []
+    monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: capturing, raising=False)
+    monkeypatch.setattr(kv_cache, "spec_workspace_init", lambda buf: cleared.append((buf.data_ptr(), buf.numel())))
+    monkeypatch.setattr(kv_cache, "_cache_ws", {})
+    ws = kv_cache._workspace(None, torch.device("cpu"), 0, 4, 64, 64, 128)
+    assert ws.numel() >= kv_cache.spec_cache_workspace_bytes(4, 64, 64, 128) > 30 << 20
+    assert cleared == [(ws.data_ptr(), state)]

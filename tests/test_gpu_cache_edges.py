@@ -142,3 +142,18 @@ def test_status_of_calls_without_a_workspace(spec):
     with torch.cuda.stream(side):
         spec.spec_tree_plan(parents, lengths, 4)
         assert spec.spec_cache_status() == 1 << 4
+
+
+def test_only_a_workspaces_state_has_to_be_zero(spec):
+    """Behind the status word and the counters a workspace may hold anything."""
+    B, N, Hq, lengths = 3, 40, 8, [3000, 30, 700]
+    c, r, q, k, v, mask = attention_inputs(spec, B, N, Hq, 2, 128, 16, lengths, 3)
+    args = (q.cuda(), k.cuda(), v.cuda(), c, ref.pack(mask).cuda())
+    for n in (N, 1):
+        args = tuple(x[:, :n] if i < 3 else x for i, x in enumerate(args[:4])) + (None,)
+        want = spec.spec_tree_attention(*args, return_lse=True)
+        ws = torch.full((spec.spec_cache_workspace_bytes(B, n, Hq, 128),), 255, dtype=torch.uint8, device="cuda")
+        spec.spec_workspace_init(ws[:65792])
+        got = spec.spec_tree_attention(*args, return_lse=True, workspace=ws)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert spec.spec_read_device_status(ws) == 0
