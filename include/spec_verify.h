@@ -645,8 +645,8 @@ spec_status spec_tree_plan(int B, int N, int max_depth, const int32_t* parents, 
  * positions      [B, N] int32, contiguous; negative: zeros are written.
  * inv_freq       [rot_dim / 2] f32; rot_dim = 0: no rotation.
  * q_weight, k_weight  [D] of wdt, nullable.
- * q_out, k_out   strides of their own; may be q and k themselves, else must not
- *                overlap them.
+ * q_out, k_out   strides of their own, of D elements or more (rows apart); may be
+ *                q and k themselves, else must not overlap them.
  * D a multiple of 8 up to 256, rot_dim a multiple of 16 up to D.
  */
 spec_status spec_qk_norm_rope(int B, int N, int q_heads, int kv_heads, int D,

@@ -453,6 +453,16 @@ spec_status check_rotation(int D, int rot, int interleaved, const float* inv_fre
     return SPEC_OK;
 }
 
+// An output's rows are apart: a broadcast one would be written by several CTAs at once.
+spec_status check_apart(const char* what, const int64_t* strides, int B, int N, int H, int D) {
+    const int dims[3] = {B, N, H};
+    for (int i = 0; i < 3; ++i)
+        if (dims[i] > 1 && strides[i] < D && strides[i] > -D)
+            return sv_host::fail(SPEC_ERR_INVALID_ARG, "%s: stride %d (%lld elements) is less than a row of %d", what, i,
+                                 (long long)strides[i], D);
+    return SPEC_OK;
+}
+
 spec_status check_weight(const char* what, const void* w) {
     if (w && ((uintptr_t)w & 15u) != 0) return sv_host::fail(SPEC_ERR_INVALID_ARG, "%s not 16-byte aligned", what);
     return SPEC_OK;
@@ -546,9 +556,11 @@ spec_status spec_qk_norm_rope(int B, int N, int q_heads, int kv_heads, int D,
     const int esz = dt == SPEC_F32 ? 4 : 2;
     if (spec_status s = sv_host::make_rows("q", q, q_strides, B, N, q_heads, esz, &P.q)) return s;
     if (spec_status s = sv_host::make_rows("q_out", q_out, q_out_strides, B, N, q_heads, esz, &P.qo)) return s;
+    if (spec_status s = check_apart("q_out", q_out_strides, B, N, q_heads, D)) return s;
     if (kv_heads) {
         if (spec_status s = sv_host::make_rows("k", k, k_strides, B, N, kv_heads, esz, &P.k)) return s;
         if (spec_status s = sv_host::make_rows("k_out", k_out, k_out_strides, B, N, kv_heads, esz, &P.ko)) return s;
+        if (spec_status s = check_apart("k_out", k_out_strides, B, N, kv_heads, D)) return s;
     }
     P.B = B; P.N = N; P.Hq = q_heads; P.Hk = kv_heads; P.D = D; P.rot = rot_dim; P.interleaved = interleaved;
     P.GW = group_width(D);

@@ -1,4 +1,5 @@
 """The cache calls' host side at the edges of what their documentation allows (no GPU needed)."""
+import ctypes
 import os
 import re
 
@@ -22,3 +23,25 @@ def test_a_new_workspace_clears_its_state_only(monkeypatch, capturing):
     ws = kv_cache._workspace(None, torch.device("cpu"), 0, 4, 64, 64, 128)
     assert ws.numel() >= kv_cache.spec_cache_workspace_bytes(4, 64, 64, 128) > 30 << 20
     assert cleared == [(ws.data_ptr(), state)]
+
+
+@pytest.mark.parametrize("axis", range(3))
+@pytest.mark.parametrize("which", ["q_out", "k_out"])
+def test_norm_rope_refuses_outputs_that_overlap_themselves(axis, which):
+    """A broadcast output would be written by several CTAs at once."""
+    from speculative_decoding_verify_temperature_b200 import build, spec_verify as sv
+    build.build()
+    L, fake = sv.lib(), 1 << 20
+
+    def call(strides):
+        rows = {n: [12 * 64, 4 * 64, 64] for n in ("q", "k", "q_out", "k_out")}
+        rows[which] = strides
+        q, k, qo, ko = ((ctypes.c_int64 * 3)(*rows[n]) for n in ("q", "k", "q_out", "k_out"))
+        return L.spec_qk_norm_rope(2, 3, 4, 4, 64, fake, q, fake, k, 1, fake, fake, 64, 0, None, None, 1, 1e-6, fake, qo, fake, ko,
+                                   None)
+
+    for stride in (0, 32, 56):
+        strides = [12 * 64, 4 * 64, 64]
+        strides[axis] = stride
+        assert call(strides) == sv.SPEC_ERR_INVALID_ARG
+        assert which in L.spec_last_error_detail().decode()
