@@ -94,7 +94,7 @@ class KvCache:
     [num_slots, kv_heads, 2 * page_size, head_dim] bf16, ``page_table`` [B, max_pages]
     int32 (rows may be strided), ``lengths`` [B] int32 (negative: no sequence in the row),
     ``slots`` [B] int32 or None (sequence b uses ring b).  Holds the tensors; what they hold
-    may change between calls, the tensors may not.
+    may change between calls, the tensors may not (``batch`` makes a cache with others).
     """
 
     def __init__(self, k_pages, v_pages, k_scale, v_scale, k_open, v_open, page_table, lengths, slots=None):
@@ -137,6 +137,11 @@ class KvCache:
                           page_table.data_ptr() or None, None if slots is None else slots.data_ptr() or None,
                           lengths.data_ptr() or None, P, stride, S, M, H, D, page)
         self._ref = ctypes.byref(self._c)
+
+    def __setattr__(self, name, value):
+        if "_ref" in self.__dict__:                # the library would go on with the old tensor's address
+            raise AttributeError(f"{name}: a KvCache keeps its tensors; use batch() or make another")
+        object.__setattr__(self, name, value)
 
     @classmethod
     def allocate(cls, num_pages, kv_heads, page_size, head_dim, page_table, lengths, slots=None, num_slots=None):

@@ -45,3 +45,17 @@ def test_norm_rope_refuses_outputs_that_overlap_themselves(axis, which):
         strides[axis] = stride
         assert call(strides) == sv.SPEC_ERR_INVALID_ARG
         assert which in L.spec_last_error_detail().decode()
+
+
+def test_a_cache_keeps_its_tensors():
+    """The library holds their addresses: assigning another tensor would leave it with the old one's memory."""
+    import speculative_decoding_verify_temperature_b200 as spec
+    from test_cache_host import _tensors
+    c = spec.KvCache(**_tensors())
+    for name in ("k_pages", "v_scale", "k_open", "page_table", "lengths", "slots", "head_dim"):
+        was = getattr(c, name)
+        with pytest.raises(AttributeError, match="batch"):
+            setattr(c, name, was)
+        assert getattr(c, name) is was
+    d = c.batch(c.page_table[:1], c.lengths[:1].clone())
+    assert d.B == 1 and d.k_pages is c.k_pages and d.lengths is not c.lengths
