@@ -697,7 +697,8 @@ spec_status spec_tree_attention(int B, int N, int q_heads, const spec_kv_cache* 
  * scaled by the least power of two (2^-126 or more) that brings its largest finite magnitude
  * within 448 (1 for a block of zeros) and rounded to e4m3 (nearest, ties to
  * even); NaN and infinities become NaN.
- * out_lengths    [B] int32: lengths[b] + rows; may be the lengths themselves.
+ * out_lengths    [B] int32: lengths[b] + rows; may be the lengths themselves
+ *                (in the last layer's call, where several layers share them).
  *                -1 for an invalid sequence (a bad page, slot or length, a row
  *                outside [0, T), num_accepted >= width or < -1, no room), whose
  *                cache is left as it was; a negative length is passed on.

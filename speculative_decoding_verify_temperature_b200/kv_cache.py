@@ -11,6 +11,10 @@ One round of a layer, ``parents`` [B, N] and a ``KvCache`` in hand::
     ...                                                                            # logits, spec_verify_tree_*
     spec_kv_append(k, v, num_accepted, cache, accept_index=accept_index)
 
+The last call writes the new lengths over ``cache.lengths``.  Layers whose caches share
+that tensor append with ``out_lengths=after`` instead and copy ``after`` to it once
+all of them are through.
+
 Argument checks happen before anything is enqueued.  Calls run on
 ``torch.cuda.current_stream`` of the tensors' device unless a stream is given;
 outputs are allocated on that stream.  Without a ``workspace`` each (device,
@@ -365,7 +369,9 @@ def spec_kv_append(k, v, num_accepted, cache: KvCache, *, accept_index=None, inv
     ``k`` / ``v`` [B, T, kv_heads, D] bf16 or f32; ``num_accepted`` [B] int32 (None: every
     row); ``accept_index`` [B, width] int32 picks the rows (None: rows 0, 1, ...).  With
     ``inv_freq`` / ``k_weight`` keys are rotated / normed on the way.  The new lengths are
-    written to ``out_lengths`` (default: the cache's own ``lengths``) and returned."""
+    written to ``out_lengths`` (default: the cache's own ``lengths``) and returned.  Where several layers'
+    caches share their ``lengths``, the default is for none of them but the last: the others would append
+    behind rows that they do not have."""
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("k must be a [B, T, heads, D] tensor")
     B, T = k.shape[:2]

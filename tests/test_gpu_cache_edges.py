@@ -1,6 +1,9 @@
 """The cache calls at the edges of what their documentation allows.  Tolerances as in test_gpu_cache.py, whose
 inputs and checks are used."""
 import math
+import os
+import re
+import types
 
 import numpy as np
 import pytest
@@ -157,3 +160,54 @@ def test_only_a_workspaces_state_has_to_be_zero(spec):
         got = spec.spec_tree_attention(*args, return_lse=True, workspace=ws)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         assert spec.spec_read_device_status(ws) == 0
+
+
+# ----------------------------------------------------------------------------- several layers
+
+def test_rounds_of_several_layers_as_documented(spec):
+    """The README's program on a model of three layers that share page table and lengths: after a prompt and a round every layer
+    holds its own rows of the same tokens, as caches with lengths of their own do."""
+    B, Hq, Hkv, D, page, dim, V = 3, 4, 2, 64, 16, 96, 64
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    program = re.search(r"### A round over the cache.*?```python\n(.*?)```", text, re.S).group(1)
+    g = torch.Generator("cuda").manual_seed(0)
+    r = lambda *s: (torch.randn(s, generator=g, device="cuda") / math.sqrt(s[0])).to(BF)  # noqa: E731
+
+    class Layer:
+        def __init__(self):
+            self.w, self.o = r(dim, (Hq + 2 * Hkv) * D), r(Hq * D, dim)
+            self.q_weight, self.k_weight = r(1, D)[0].abs() + 0.5, r(1, D)[0].abs() + 0.5
+            self.seen = []
+
+        def project(self, x):
+            q, k, v = (x @ self.w).split((Hq * D, Hkv * D, Hkv * D), -1)
+            self.seen.append((k.unflatten(-1, (Hkv, D)), v.unflatten(-1, (Hkv, D))))
+            return q.unflatten(-1, (Hq, D)), *self.seen[-1]
+
+        def finish(self, x, attn):
+            return x + attn.flatten(2) @ self.o
+
+    rs = np.random.RandomState(1)
+    table, emb, unembed = gpu(rs.permutation(B * 4).astype(np.int32).reshape(B, 4)), r(V, dim), r(dim, V)
+    parents = ref.random_parents(B, 6, rs)
+    given = dict(layers=[Layer() for _ in range(3)], num_pages=B * 4, kv_heads=Hkv, page_size=page, head_dim=D, page_table=table,
+                 lengths=torch.zeros(B, dtype=torch.int32, device="cuda"), inv_freq=gpu(ref.inv_freq(D)), max_depth=6,
+                 embed=lambda t: emb[t.long()], head=lambda x: x @ unembed, parents=gpu(parents),
+                 prompt=torch.randint(0, V, (B, 37), generator=g, device="cuda"), count=gpu(np.array([37, 15, 31], dtype=np.int32)),
+                 draft_tokens=torch.randint(0, V, (B, 6), generator=g, device="cuda", dtype=torch.int32))
+    exec(compile(program, "README.md", "exec"), given)
+    space = types.SimpleNamespace(**{n: x for n, x in given.items() if n.isidentifier()})
+    taken = (space.num + 1).clamp(min=0)
+    assert torch.equal(space.lengths, space.count + taken)
+    for layer, cache in zip(space.layers, space.caches):
+        own = spec.KvCache.allocate(B * 4, Hkv, page, D, table, torch.zeros(B, dtype=torch.int32, device="cuda"))
+        for (k, v), num, index in zip(layer.seen, (space.count - 1, space.num), (None, space.index)):
+            if index is None:
+                pos, _ = spec.spec_tree_plan(None, own.lengths, N=k.shape[1])
+            else:
+                pos, _ = spec.spec_tree_plan(space.parents, own.lengths, 6)
+            k = spec.spec_qk_norm_rope(k, k, pos, space.inv_freq, q_weight=layer.q_weight, k_weight=layer.k_weight)[1]
+            spec.spec_kv_append(k, v, num, own, accept_index=index)
+        assert torch.equal(own.lengths, space.lengths)
+        for name in ("k_pages", "v_pages", "k_scale", "v_scale", "k_open", "v_open"):
+            assert torch.equal(getattr(own, name).view(torch.uint8), getattr(cache, name).view(torch.uint8)), name
