@@ -17,7 +17,8 @@ all of them are through.
 
 Argument checks happen before anything is enqueued.  Calls run on
 ``torch.cuda.current_stream`` of the tensors' device unless a stream is given;
-outputs are allocated on that stream.  Without a ``workspace`` each (device,
+outputs are allocated on that stream, and tensors may be dropped as soon as a call
+returns, whichever stream it runs on.  Without a ``workspace`` each (device,
 stream) has one of its own, whose status word ``spec_cache_status`` reads, and a
 call that is being captured into a CUDA graph gets one that belongs to the
 graph (give it a ``workspace`` to read the status of its replays).
@@ -158,6 +159,11 @@ class KvCache:
         ring = [torch.zeros((n, kv_heads, 2 * page_size, head_dim), dtype=torch.bfloat16, device=dev) for _ in range(2)]
         return cls(*pool, *scale, *ring, page_table, lengths, slots)
 
+    def tensors(self):
+        """What the cache holds."""
+        return (self.k_pages, self.v_pages, self.k_scale, self.v_scale, self.k_open, self.v_open, self.page_table,
+                self.lengths, self.slots)
+
     def batch(self, page_table, lengths, slots=None):
         """The same pages and rings for another batch of sequences."""
         return KvCache(self.k_pages, self.v_pages, self.k_scale, self.v_scale, self.k_open, self.v_open, page_table,
@@ -187,6 +193,20 @@ def _on(device, stream):
         return stream.cuda_stream, torch.cuda.stream(stream)
     handle = torch._C._cuda_getCurrentRawStream(device.index)
     return handle, _same if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
+
+
+def _share(device, stream, used, made):
+    """Of a call on a stream that is not the current one: the memory of the tensors that it uses is not handed out again
+    before it is through, nor that of the outputs that it allocated while the current stream reads them."""
+    if stream is None:
+        return
+    current = torch.cuda.current_stream(device)
+    if current.cuda_stream != stream.cuda_stream:
+        for t in used:
+            if t is not None:
+                t.record_stream(stream)
+        for t in made:
+            t.record_stream(current)
 
 
 def _workspace(workspace, device, handle, B, N, q_heads, head_dim):
@@ -247,19 +267,22 @@ def spec_tree_plan(parents, lengths, max_depth: int = 64, *, N: int | None = Non
     elif N is None:
         raise ValueError("give parents, or N for chains")
     s, current = _on(dev, stream)
+    given, made = [out_positions, out_ancestors], []
     with current:
         if out_positions is None:
-            out_positions = lengths.new_empty((B, N))
+            made.append(out_positions := lengths.new_empty((B, N)))
         else:
             _need(out_positions, "out_positions", _I32, (B, N), dev)
         if out_ancestors is None:
-            out_ancestors = lengths.new_empty((B, N, (N + 31) // 32))
+            made.append(out_ancestors := lengths.new_empty((B, N, (N + 31) // 32)))
         else:
             _need(out_ancestors, "out_ancestors", _I32, (B, N, (N + 31) // 32), dev)
         ws = _workspace(workspace, dev, s, 1, 1, 1, 64)
         _check(lib().spec_tree_plan(B, N, int(max_depth), None if parents is None else parents.data_ptr(),
                                     lengths.data_ptr(), out_positions.data_ptr(), out_ancestors.data_ptr(),
                                     ws.data_ptr(), ws.numel(), s), "spec_tree_plan")
+    if stream is not None:
+        _share(dev, stream, (parents, lengths, workspace, *given), made)
     return out_positions, out_ancestors
 
 
@@ -309,20 +332,23 @@ def spec_qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None
     wdt, (qw, kw) = _weights((("q_weight", q_weight), ("k_weight", k_weight)), D, dev)
     freq, rot = _frequencies(inv_freq, dev)
     s, current = _on(dev, stream)
+    given, made = (q_out, k_out), []
     with current:
         if q_out is None:
-            q_out = q.new_empty((B, N, Hq, D))
+            made.append(q_out := q.new_empty((B, N, Hq, D)))
             qop, qos = q_out.data_ptr(), _packed(N, Hq, D)
         else:
             qop, qos = _rows4(q_out, "q_out", (B, N, Hq, D), q.dtype, dev)
         if k_out is None:
-            k_out = q.new_empty((B, N, Hk, D))
+            made.append(k_out := q.new_empty((B, N, Hk, D)))
             kop, kos = k_out.data_ptr(), _packed(N, Hk, D)
         else:
             kop, kos = _rows4(k_out, "k_out", (B, N, Hk, D), q.dtype, dev)
         _check(lib().spec_qk_norm_rope(B, N, Hq, Hk, D, qp, qs, kp, ks, dt, positions.data_ptr(), freq, rot,
                                        int(bool(interleaved)), qw, kw, wdt, eps, qop, qos, kop, kos, s),
                "spec_qk_norm_rope")
+    if stream is not None:
+        _share(dev, stream, (q, k, positions, inv_freq, q_weight, k_weight, *given), made)
     return q_out, k_out
 
 
@@ -344,21 +370,24 @@ def spec_tree_attention(q, k, v, cache: KvCache, ancestors=None, *, scale: float
     if ancestors is not None:
         _need(ancestors, "ancestors", _I32, (B, N, (N + 31) // 32), dev)
     s, current = _on(dev, stream)
+    given, made = (out, lse), []
     with current:
         if out is None:
-            out = q.new_empty((B, N, Hq, D))
+            made.append(out := q.new_empty((B, N, Hq, D)))
         else:
             _need(out, "out", bf, (B, N, Hq, D), dev)
         if lse is not None:
             _need(lse, "lse", _F32, (B, N, Hq), dev)
         elif return_lse:
-            lse = q.new_empty((B, N, Hq), dtype=_F32)
+            made.append(lse := q.new_empty((B, N, Hq), dtype=_F32))
         ws = _workspace(workspace, dev, s, B, N, Hq, D)
         _check(lib().spec_tree_attention(B, N, Hq, cache._ref, qp, qs, kp, ks, vp, vs,
                                          None if ancestors is None else ancestors.data_ptr(),
                                          1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(),
                                          None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
                                          s), "spec_tree_attention")
+    if stream is not None:
+        _share(dev, stream, (q, k, v, ancestors, workspace, *given, *cache.tensors()), made)
     return (out, lse) if return_lse else out
 
 
@@ -400,4 +429,6 @@ def spec_kv_append(k, v, num_accepted, cache: KvCache, *, accept_index=None, inv
                                     None if accept_index is None else accept_index.data_ptr(), freq, rot,
                                     int(bool(interleaved)), kw, wdt, eps, out_lengths.data_ptr(), ws.data_ptr(),
                                     ws.numel(), s), "spec_kv_append")
+    if stream is not None:
+        _share(dev, stream, (k, v, num_accepted, accept_index, inv_freq, k_weight, out_lengths, workspace, *cache.tensors()), ())
     return out_lengths

@@ -162,6 +162,35 @@ def test_only_a_workspaces_state_has_to_be_zero(spec):
         assert spec.spec_read_device_status(ws) == 0
 
 
+@pytest.mark.parametrize("N", [1, 40])
+def test_tensors_may_be_dropped_after_a_call_on_another_stream(spec, N):
+    """The memory of the inputs is not used again before the other stream has read it, nor that of the outputs before the
+    current one has."""
+    c, r, q, k, v, mask = attention_inputs(spec, 2, N, 8, 2, 128, 16, [100, 300], 2)
+    side, main = torch.cuda.Stream(), torch.cuda.current_stream()
+    anc = ref.pack(mask).cuda()
+    want = spec.spec_tree_attention(q.cuda(), k.cuda(), v.cuda(), c, anc)
+    others = (-q).cuda(), k.cuda(), v.cuda()
+    assert not torch.equal(want, spec.spec_tree_attention(*others, c, anc))
+    for _ in range(2):
+        args = [x.cuda() for x in (q, k, v)] + [anc.clone()]
+        shapes = [(x.shape, x.dtype) for x in args]
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)                     # some 10 ms
+        out = spec.spec_tree_attention(*args[:3], c.batch(c.page_table.clone(), c.lengths.clone()), args[3], stream=side)
+        del args
+        junk = [torch.full(s, -1, dtype=d, device="cuda") for s, d in shapes for _ in range(4)]
+        junk += [torch.full_like(c.page_table, -1) for _ in range(4)] + [torch.full_like(c.lengths, -1) for _ in range(4)]
+        main.wait_stream(side)
+        torch.cuda._sleep(20_000_000)
+        got = out.clone()
+        del out
+        keep = [spec.spec_tree_attention(*others, c, anc, stream=side) for _ in range(3)]
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and len(junk) + len(keep) > 0
+
+
 # ----------------------------------------------------------------------------- several layers
 
 def test_rounds_of_several_layers_as_documented(spec):
