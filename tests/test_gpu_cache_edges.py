@@ -240,3 +240,36 @@ def test_rounds_of_several_layers_as_documented(spec):
         assert torch.equal(own.lengths, space.lengths)
         for name in ("k_pages", "v_pages", "k_scale", "v_scale", "k_open", "v_open"):
             assert torch.equal(getattr(own, name).view(torch.uint8), getattr(cache, name).view(torch.uint8)), name
+
+
+# ----------------------------------------------------------------------------- large pools, items in many parts
+
+@pytest.mark.parametrize("N,Hq,Hkv,D,length", [(1, 4, 1, 128, 40000), (2, 8, 1, 64, 30000), (24, 4, 1, 128, 25000),
+                                               (80, 4, 1, 64, 25000)])
+def test_attention_of_items_in_many_parts(spec, N, Hq, Hkv, D, length):
+    """One kv head over a long cache: every CTA holds a part of the same item, and the join goes over more than 32 of them."""
+    c, r, q, k, v, mask = attention_inputs(spec, 1, N, Hq, Hkv, D, 32, [length], N)
+    out, lse = spec.spec_tree_attention(q.cuda(), k.cuda(), v.cuda(), c, ref.pack(mask).cuda(), return_lse=True)
+    check_attention(r, [length], q, k, v, mask, out, lse, 1 / math.sqrt(D))
+
+
+def test_a_pool_of_more_than_4_gb(spec):
+    """Page ids whose bytes lie behind 2^32 give what low ones give, in the append and in both attention kernels."""
+    Hkv, D, page, P, L = 8, 128, 128, 33000, 600
+    g = torch.Generator("cuda").manual_seed(0)
+    assert P * Hkv * page * D > 1 << 32
+    lengths = torch.zeros(2, dtype=torch.int32, device="cuda")
+    big = spec.KvCache.allocate(P, Hkv, page, D, gpu(np.array([[P - 1, 5, P - 7, 20000, P - 2]] * 2, dtype=np.int32)), lengths)
+    big.page_table[1] = gpu(np.array([P - 11, 17000, 3, P - 4, 16999], dtype=np.int32))
+    low = spec.KvCache.allocate(10, Hkv, page, D, gpu(np.arange(10, dtype=np.int32).reshape(2, 5)), lengths.clone())
+    k, v = (torch.randn((2, L, Hkv, D), generator=g, device="cuda").to(BF) for _ in range(2))
+    for c in (big, low):
+        spec.spec_kv_append(k, v, None, c)
+    assert big.lengths.tolist() == low.lengths.tolist() == [L, L]
+    for name in ("k_pages", "v_pages", "k_scale", "v_scale"):
+        x, y = (getattr(c, name).view(torch.uint8)[c.page_table[:, :L // page].long()] for c in (big, low))
+        assert torch.equal(x, y), name
+    for N in (1, 12):
+        q = torch.randn((2, N, 2 * Hkv, D), generator=g, device="cuda").to(BF)
+        outs = [spec.spec_tree_attention(q, k[:, :N], v[:, :N], c, return_lse=True) for c in (big, low)]
+        assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
