@@ -1,5 +1,5 @@
-// cache_device.cuh -- device helpers of the cache kernels: rows of 8-element
-// vectors, the RMS norm and the rotation of a head row, e4m3.
+// cache_device.cuh -- device helpers of the cache kernels: rows in vectors of
+// elements, the RMS norm and the rotation of a head row, e4m3.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -25,46 +25,11 @@ __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
     return r;
 }
 
-// Eight consecutive elements as they lie in memory.
-template <int DT> struct Vec8;
-template <> struct Vec8<SPEC_BF16> {
-    static constexpr int ESZ = 2;
+// Eight consecutive bf16 elements as they lie in memory.
+struct Bf16x8 {
     uint4 a;
-    __device__ __forceinline__ void load(const char* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
-    __device__ __forceinline__ void load_plain(const char* p) { a = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void load(const char* p) { a = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        x[0] = bf_lo(a.x); x[1] = bf_hi(a.x); x[2] = bf_lo(a.y); x[3] = bf_hi(a.y);
-        x[4] = bf_lo(a.z); x[5] = bf_hi(a.z); x[6] = bf_lo(a.w); x[7] = bf_hi(a.w);
-    }
-    __device__ __forceinline__ void set(const float (&x)[8]) {
-        a = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-    }
-    __device__ __forceinline__ void store(char* p) const { *reinterpret_cast<uint4*>(p) = a; }
-};
-template <> struct Vec8<SPEC_F32> {
-    static constexpr int ESZ = 4;
-    float4 a, b;
-    __device__ __forceinline__ void load(const char* p) {
-        a = __ldg(reinterpret_cast<const float4*>(p));
-        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    }
-    __device__ __forceinline__ void load_plain(const char* p) {
-        a = reinterpret_cast<const float4*>(p)[0];
-        b = reinterpret_cast<const float4*>(p)[1];
-    }
-    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    }
-    __device__ __forceinline__ void set(const float (&x)[8]) {
-        a = make_float4(x[0], x[1], x[2], x[3]);
-        b = make_float4(x[4], x[5], x[6], x[7]);
-    }
-    __device__ __forceinline__ void store(char* p) const {
-        reinterpret_cast<float4*>(p)[0] = a;
-        reinterpret_cast<float4*>(p)[1] = b;
-    }
 };
 
 // cos and sin of pos * f.  The angle is formed in f64, in turns, and reduced to
@@ -81,6 +46,7 @@ __device__ __forceinline__ float2 cos_sin(int pos, float f) {
 // Four consecutive elements.
 template <int DT> struct Quad;
 template <> struct Quad<SPEC_BF16> {
+    static constexpr int ESZ = 2;
     uint2 a;
     __device__ __forceinline__ void load(const char* p) { a = *reinterpret_cast<const uint2*>(p); }
     __device__ __forceinline__ void load_bf16(const char* p) { load(p); }
@@ -90,6 +56,7 @@ template <> struct Quad<SPEC_BF16> {
     __device__ __forceinline__ void store(char* p) const { *reinterpret_cast<uint2*>(p) = a; }
 };
 template <> struct Quad<SPEC_F32> {
+    static constexpr int ESZ = 4;
     float4 a;
     __device__ __forceinline__ void load(const char* p) { a = *reinterpret_cast<const float4*>(p); }
     __device__ __forceinline__ void load_bf16(const char* p) {

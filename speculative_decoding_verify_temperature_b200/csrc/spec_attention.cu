@@ -804,14 +804,14 @@ struct TcConv {
     // A loop that stays small: its code runs once per item and is never in the instruction caches.  (16 lanes to a row
     // and a piece each: 1100 cycles for 16 rows, nearly all of it waiting for shuffles.)
     static constexpr int QV = D / 32, QP = TC_CONV / 4;
-    __device__ __forceinline__ void load_q(const Seg& g, int rows, int p, Vec8<SPEC_BF16> (&w)[QV]) {
+    __device__ __forceinline__ void load_q(const Seg& g, int rows, int p, Bf16x8 (&w)[QV]) {
         const int r = min(tid / 4 + p * QP, rows - 1);    // rows behind the last repeat it
         const int row = g.mt * 256 + r, n = row / P.G, h = g.h * P.G + row - n * P.G;
         const char* src = P.q.p + g.b * P.q.b + n * P.q.n + h * P.q.h + 16 * (tid % 4);
 #pragma unroll
-        for (int i = 0; i < QV; ++i) w[i].load_plain(src + 64 * i);
+        for (int i = 0; i < QV; ++i) w[i].load(src + 64 * i);
     }
-    __device__ __forceinline__ void put_q_rows(Vec8<SPEC_BF16> (&w)[QV], int p, float* rq) {
+    __device__ __forceinline__ void put_q_rows(Bf16x8 (&w)[QV], int p, float* rq) {
         const int r = tid / 4 + p * QP;
         uint32_t all[QV * 4];
 #pragma unroll
@@ -837,11 +837,11 @@ struct TcConv {
         // the rows behind the last are whatever they are: their results are not looked at
         const int rows = min(256, P.R - g.mt * 256), np = (rows + QP - 1) / QP;
         float* rq = sh.rq[seg & 3];
-        Vec8<SPEC_BF16> w[QV];
+        Bf16x8 w[QV];
         load_q(g, rows, 0, w);
 #pragma unroll 1
         for (int p = 0; p < np; ++p) {
-            Vec8<SPEC_BF16> x[QV];
+            Bf16x8 x[QV];
 #pragma unroll
             for (int i = 0; i < QV; ++i) x[i] = w[i];
             load_q(g, rows, p + 1, w);                    // behind the last pass: the last row again
@@ -850,7 +850,7 @@ struct TcConv {
     }
     // Row e of the tail: open tokens from the ring, then the nodes.  One load for every row, from a place that is
     // there (a query where there is no key): a branch per row would wait for each load in turn.
-    __device__ __forceinline__ void load_tail(const TileIter& u, int p, Vec8<SPEC_BF16>& k, Vec8<SPEC_BF16>& v) {
+    __device__ __forceinline__ void load_tail(const TileIter& u, int p, Bf16x8& k, Bf16x8& v) {
         const int l = tid % LPR;
         const Seq& q = u.g.q;
         const int e = (u.t - q.nct) * TILE + tid / LPR + p * RP;
@@ -860,14 +860,14 @@ struct TcConv {
         const int64_t n = e - q.open;
         const char* kp = open ? static_cast<const char*>(P.c.k_open) + at : P.k.p + u.g.b * P.k.b + n * P.k.n + u.g.h * P.k.h;
         const char* vp = open ? static_cast<const char*>(P.c.v_open) + at : P.v.p + u.g.b * P.v.b + n * P.v.n + u.g.h * P.v.h;
-        k.load_plain((in ? kp : P.q.p) + 16 * l);
-        v.load_plain((in ? vp : P.q.p) + 16 * l);
+        k.load((in ? kp : P.q.p) + 16 * l);
+        v.load((in ? vp : P.q.p) + 16 * l);
         if (!in) {
             k.zero();
             v.zero();
         }
     }
-    __device__ __forceinline__ void put_tail_row(const TileIter& u, Vec8<SPEC_BF16> k, Vec8<SPEC_BF16> v, int p, uint32_t khi,
+    __device__ __forceinline__ void put_tail_row(const TileIter& u, Bf16x8 k, Bf16x8 v, int p, uint32_t khi,
                                                  uint32_t klo, uint32_t vd, float* meta) {
         const int l = tid % LPR, r = tid / LPR + p * RP;
         bool bad;
@@ -894,7 +894,7 @@ struct TcConv {
         constexpr int KR = Tc<D>::KR;
         const int m = u.gt & (TC_META - 1);
         const int k0 = nk % KR, k1 = (nk + 1) % KR;
-        Vec8<SPEC_BF16> ka{}, va{}, kb{}, vb{};
+        Bf16x8 ka{}, va{}, kb{}, vb{};
         bar_wait(&sh.me[m], ((u.gt / TC_META) & 1) ^ 1, sh);
         bar_wait(&sh.ke[k0], ((nk / KR) & 1) ^ 1, sh);
         bar_wait(&sh.ke[k1], (((nk + 1) / KR) & 1) ^ 1, sh);
@@ -910,7 +910,7 @@ struct TcConv {
         for (int r = np * RP + tid; r < TILE; r += TC_CONV) meta[r] = meta[TILE + r] = meta[2 * TILE + r] = 1.f;
 #pragma unroll 1
         for (int p = -2; p < np; ++p) {
-            const Vec8<SPEC_BF16> k = ka, v = va;
+            const Bf16x8 k = ka, v = va;
             ka = kb;
             va = vb;
             load_tail(u, p + 2, kb, vb);
@@ -2023,7 +2023,7 @@ template <int D, int NQ> struct alignas(16) MmShared {
     float4 o[2][4][32];                                   // output fragments of two warps, four blocks at a time
     float m[MM_WARPS][8 * NQ], l[MM_WARPS][8 * NQ];
     uint32_t bad_v[12];
-    int bad, late;
+    int bad;
     MmAhead now, ahead[MM_WARPS];                         // the segment being computed; of each warp's next chunk
 };
 
@@ -2175,7 +2175,7 @@ __global__ void __launch_bounds__(MM_BT, MM_CTAS_SM) k_attention_mma(const Att P
     if (threadIdx.x == 0) P.cut[blockIdx.x].parts = 0;
     if (st.lo >= st.hi) return;
     if (threadIdx.x < 12) sh.bad_v[threadIdx.x] = 0;
-    if (threadIdx.x == 12) sh.bad = sh.late = 0;
+    if (threadIdx.x == 12) sh.bad = 0;
     if (threadIdx.x == 32) {
         sh.now.it.begin(P, st);
         sh.now.more = sh.now.it.next(P, sh.now.s);

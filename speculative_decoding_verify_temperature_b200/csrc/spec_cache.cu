@@ -90,7 +90,7 @@ __device__ __forceinline__ float weight_at(const char* w, int f32, int e) {
 template <int DT>
 __global__ void __launch_bounds__(NR_BT) k_norm_rope(const NormRope P) {
     __shared__ __align__(16) float cs[2][128], wt[2][256];
-    constexpr int ESZ = Vec8<DT>::ESZ;
+    constexpr int ESZ = Quad<DT>::ESZ;
     const int tok = blockIdx.x, b = tok / P.N, n = tok - b * P.N;
     const int GW = P.GW, l = threadIdx.x & (GW - 1);
     const int groups = NR_BT / GW, grp = threadIdx.x / GW;
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(AP_BT, R <= 4 ? 3 : 2) k_append(const Append P
             const Quads at(l, which ? 0 : P.rot, P.interleaved);
             const int64_t sn = which ? P.v.n : P.k.n;
             const char* src = which ? P.v.p + b * P.v.b + h * P.v.h : P.k.p + b * P.k.b + h * P.k.h;
-            const int o0 = at.q0 * 4 * Vec8<DT>::ESZ, o1 = at.q1 * 4 * Vec8<DT>::ESZ;
+            const int o0 = at.q0 * 4 * Quad<DT>::ESZ, o1 = at.q1 * 4 * Quad<DT>::ESZ;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 raw[i][0].zero();
