@@ -200,14 +200,14 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t m) {
 // rows before lengths[b] come from the ring, the others from k and v.  A full
 // block is reduced to its largest magnitude, scaled and written as a page; else
 // the new rows go to the ring.  Bound by latency for a round's few rows (11 us a call, the host's
-// part of it), by instructions for prompts: 8 x 2048 tokens (8 heads of 128, normed and rotated) take 39 us, 1.9 TB/s, with about 59% of
-// the issue slots filled and a barrier in the middle for the block's maximum.
+// part of it), by instructions for prompts: 8 x 2048 tokens (8 heads of 128, normed and rotated) take 40 us, 1.9 TB/s, with about 59% of
+// the issue slots filled and a barrier in the middle for the block's maximum.  (Angles made of three partial rotations, in f32, took
+// 39 us, but turned some keys to the other side of a rounding.)
 template <int DT, int R>
 __global__ void __launch_bounds__(AP_BT, R <= 4 ? 3 : 2) k_append(const Append P) {
-    // cosines, then sines [row of the block][pair]; the partial rotations that they are made of
+    // cosines, then sines [row of the block][pair]
     extern __shared__ __align__(16) float ct[];
     float* st = ct + P.page * (P.rot / 2);
-    float2* tr = reinterpret_cast<float2*>(st + P.page * (P.rot / 2));
     __shared__ __align__(16) float wt[128];
     __shared__ uint32_t red[2][AP_BT / 32];
     __shared__ int sh_len;
@@ -273,24 +273,14 @@ __global__ void __launch_bounds__(AP_BT, R <= 4 ? 3 : 2) k_append(const Append P
         const bool full = start + page <= newlen;
         int page_id = 0;
         if (full) page_id = P.c.page_table[b * P.c.page_table_stride + blk];
-        if (half) {
-            // The angle of row r is the block's first plus 8 (r / 8) steps plus r mod 8: 1 + page / 8 + 8 sines and
-            // cosines per pair and a product of three rotations for each row, instead of `page` of them.
-            const int parts = 1 + (page >> 3) + 8;
-            for (int m = tid >> 5; m < parts; m += AP_BT / 32) {
-                const int steps = m == 0 ? start : m <= (page >> 3) ? 8 * (m - 1) : m - 1 - (page >> 3);
-                for (int j = lane; j < half; j += 32) tr[m * half + j] = cos_sin(steps, P.inv_freq[j]);
-            }
-            __syncthreads();
-            for (int r = tid >> 5; r < page; r += AP_BT / 32) {
-                const float2* u8 = tr + (1 + (r >> 3)) * half;
-                const float2* v8 = tr + (1 + (page >> 3) + (r & 7)) * half;
-                for (int j = lane; j < half; j += 32) {
-                    const float2 a = tr[j], u = u8[j], v = v8[j];
-                    const float2 w = make_float2(a.x * u.x - a.y * u.y, a.x * u.y + a.y * u.x);
-                    ct[r * half + j] = w.x * v.x - w.y * v.y;
-                    st[r * half + j] = w.x * v.y + w.y * v.x;
-                }
+        // Each angle on its own, as the norm and rotation call forms it: an appended key is the one that it would have written.
+        const int r0 = max(len - start, 0), r1 = min(newlen - start, page);              // the rows that come from k
+        for (int j = lane; j < half; j += 32) {
+            const float f = P.inv_freq[j];
+            for (int r = r0 + (tid >> 5); r < r1; r += AP_BT / 32) {
+                const float2 v = cos_sin(start + r, f);
+                ct[r * half + j] = v.x;
+                st[r * half + j] = v.y;
             }
         }
         // where the rows of the block come from: a row of k and v, the ring (-1), nowhere (-2)
@@ -415,10 +405,10 @@ __global__ void __launch_bounds__(AP_BT, R <= 4 ? 3 : 2) k_append(const Append P
 
 template <int DT, int R>
 spec_status launch_append_rows(const Append& P, dim3 grid, cudaStream_t st) {
-    const size_t smem = (size_t)(P.page + 1 + P.page / 8 + 8) * (P.rot / 2) * sizeof(float2);   // up to 76.5 KB
+    const size_t smem = (size_t)P.page * (P.rot / 2) * sizeof(float2);       // up to 64 KB
     // asked for whatever this call needs: the kernel's static shared memory counts towards the 48 KB too
     static std::atomic<uint64_t> done{0};
-    if (const spec_status s = sv_host::allow_smem(reinterpret_cast<const void*>(k_append<DT, R>), "k_append", 80 * 1024, done)) return s;
+    if (const spec_status s = sv_host::allow_smem(reinterpret_cast<const void*>(k_append<DT, R>), "k_append", 64 * 1024, done)) return s;
     k_append<DT, R><<<grid, AP_BT, smem, st>>>(P);
     return sv_host::launched("k_append");
 }
@@ -617,8 +607,9 @@ spec_status spec_kv_append(int B, int T, int width, const spec_kv_cache* cache,
     P.status = reinterpret_cast<unsigned*>(ws + sv_host::CACHE_WS_STATUS);
     P.cnt = reinterpret_cast<unsigned*>(ws + sv_host::CACHE_WS_SEQ);
     const int blocks = (page - 1 + width - 1) / page + 1;          // touched at most
-    // a CTA takes several heads (they share the angles) once there are CTAs enough for four per SM: 8 x 2048 tokens took 43 us
-    // with eight, 39 with four, 45 with three; 1 x 2048 13.3 us with each of them, 15 with two heads to a CTA
+    // a CTA takes several heads (they share the angles) once there are CTAs enough for four per SM: with the angles made of partial
+    // rotations 8 x 2048 tokens took 43 us with eight, 39 with four, 45 with three; 1 x 2048 13.3 us with each of them, 15 with two
+    // heads to a CTA
     const long long units = (long long)blocks * B * Hkv;
     long long per = (units + 4LL * sv_host::num_sms() - 1) / (4LL * sv_host::num_sms());
     P.heads_per_cta = (int)(per < 1 ? 1 : per > Hkv ? Hkv : per);

@@ -81,6 +81,31 @@ def test_append_every_rotated_width(spec, rot, dt):
     assert ((got - e[page:]).abs() <= e[page:].abs() * 2.0 ** -8 + mag[page:] * 2.0 ** -19).all()
 
 
+@pytest.mark.parametrize("D,page,rot,inter,weights,dt", [(128, 64, 128, False, True, BF), (128, 128, 128, False, True, BF),
+                                                         (64, 16, 32, False, True, torch.float32), (128, 32, 96, True, False, BF),
+                                                         (64, 128, 64, True, True, torch.float32), (128, 16, 128, False, False, BF)])
+def test_append_rotates_as_the_norm_and_rotation_call_does(spec, D, page, rot, inter, weights, dt):
+    """Raw keys appended with a norm and a rotation leave what that call's output leaves, bit for bit: bf16 keys, which it rounds
+    as the append does."""
+    B, Hkv, first, T = 3, 4, 1000, 2 * page + 41
+    g = torch.Generator("cuda").manual_seed(D + page)
+    freq = gpu(ref.inv_freq(rot, 1e4))
+    w = (torch.rand((D,), generator=g, device="cuda") + 0.5).to(dt) if weights else None
+    raw, ready = (make_cache(spec, B, Hkv, D, page, (first + T) // page + 1, np.random.RandomState(5)) for _ in range(2))
+    v0 = torch.randn((B, first, Hkv, D), generator=g, device="cuda").to(dt)
+    k, v = ((torch.randn((B, T, Hkv, D), generator=g, device="cuda") * 3).to(dt) for _ in range(2))
+    num = gpu(np.array([T, T - 5, T - 30], dtype=np.int32)) - 1
+    for c in (raw, ready):
+        spec.spec_kv_append(v0, v0, gpu(np.array([first - 1, first // 2, 6], dtype=np.int32)), c)
+    pos = raw.lengths[:, None] + torch.arange(T, device="cuda", dtype=torch.int32)
+    turned = spec.spec_qk_norm_rope(k, k, pos, freq, q_weight=w, k_weight=w, eps=1e-6, interleaved=inter)[1]
+    spec.spec_kv_append(k, v, num, raw, inv_freq=freq, k_weight=w, eps=1e-6, interleaved=inter)
+    spec.spec_kv_append(turned, v, num, ready)
+    assert torch.equal(raw.lengths, ready.lengths)
+    for name in ("k_pages", "v_pages", "k_scale", "v_scale", "k_open", "v_open"):
+        assert torch.equal(getattr(raw, name).view(torch.uint8), getattr(ready, name).view(torch.uint8)), name
+
+
 # ----------------------------------------------------------------------------- plan
 
 def test_plan_of_a_row_without_a_sequence(spec):
