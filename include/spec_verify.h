@@ -674,7 +674,16 @@ spec_status spec_qk_norm_rope(int B, int N, int q_heads, int kv_heads, int D,
  * lse            nullable, [B, N, q_heads] f32.
  * 1 <= N <= SPEC_MAX_NODES; q_heads a multiple of kv_heads.
  * workspace      >= spec_cache_workspace_bytes(B, N, q_heads, D).
- * Products and sums in f32 (the probabilities enter the second product as f16).
+ * Products and sums in f32.  What enters them has fewer bits: the probabilities
+ * are rounded to f16 before the second product (2^-11 of each; the sum under them
+ * is that of the unrounded ones).  q, and the keys that are not in a page yet, are
+ * exact but for small elements: with more than 16 rows (nodes times query
+ * heads) per kv head, elements below 2^-9 of their row's largest are rounded at
+ * 2^-18 of it (two e4m3 rows), else those below 2^-14 of it at 2^-24 of it (f16 after a power of two,
+ * as are the values that are not in a page yet).
+ * The same call gives the same bits.  In another batch a sequence's keys are split
+ * over the GPU elsewhere and its sums are joined elsewhere: they may differ by
+ * their rounding.
  */
 spec_status spec_tree_attention(int B, int N, int q_heads, const spec_kv_cache* cache,
                                 const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides,
@@ -792,7 +801,9 @@ unsigned long long spec_launch_count(void);
  * (libspecverify_debug.so), every data-driven index the kernels use -- a
  * gathered token id, a parent link, a drawn chunk -- is range-checked on the
  * device; a failed check is counted and the access skipped (a token gathered
- * out of range reads as NaN, which invalidates its sequence).  This call
+ * out of range reads as NaN, which invalidates its sequence).  The cache calls
+ * count nothing here: they check page ids, slots, lengths, rows and parents in
+ * every build.  This call
  * synchronises the device, stores the count since the last call in *hits and
  * clears it.  A library built without the flag returns SPEC_ERR_UNSUPPORTED
  * (and *hits = 0).  The checks cost time; they are for debugging.

@@ -1,5 +1,5 @@
-"""Build libspecverify.so (and its bounds-checked twin libspecverify_debug.so)
-in-tree with nvcc for sm_100a: one object per translation unit, compiled in
+"""Build libspecverify.so (and libspecverify_debug.so, whose verify calls count
+failed bounds checks; the cache calls check theirs in both) in-tree with nvcc for sm_100a: one object per translation unit, compiled in
 parallel, then one link."""
 from __future__ import annotations
 

@@ -259,10 +259,10 @@ __device__ __forceinline__ uint32_t tail_bits(const Att& P, int b, int n, int op
 // another scale on, a row's l is summed from exponentials of its own, 2^(x_j - r), with r a whole number that
 // follows the largest x_j ("far"; r = M - P_BIAS otherwise), and out = O / l 2^(M - P_BIAS - r).  That costs a second
 // exponential per key, in code that trained values do not reach; the others pay for it in an item's own steps (64 chains of 6
-// over ragged lengths up to 4096 197 -> 203 us; 549 and 105 us, see below, as before).
+// over ragged lengths up to 4096 198 -> 204 us; 32 trees of 64 and one tree of 32, see below, as before).
 //
 // Measured (B200, D = 128, 64 query on 8 kv heads): 32 trees of 64 nodes over ragged lengths up to 8192 550 us, 630 TFLOP/s;
-// 64 chains of 6 over ragged lengths up to 4096 197 us; one tree of 32 over 131072 tokens (32 query heads of 64) 106 us.  Bound by the
+// 64 chains of 6 over ragged lengths up to 4096 206 us; one tree of 32 over 131072 tokens (32 query heads of 64) 106 us.  Bound by the
 // chain of one stream's steps, about 5400 cycles a tile: softmax 3100 (its own warp's latencies: MUFU a third busy), the
 // product with values 700, the scores of the next tile 850, barriers the rest; the two streams run side by side and tensor
 // memory (S0 S1 O0 O1 fill it at D = 128) has no room for a third.  An item costs another 25000 cycles or so.  Tried and slower:
