@@ -679,8 +679,8 @@ spec_status spec_qk_norm_rope(int B, int N, int q_heads, int kv_heads, int D,
  * is that of the unrounded ones).  q, and the keys that are not in a page yet, are
  * exact but for small elements: with more than 16 rows (nodes times query
  * heads) per kv head, elements below 2^-9 of their row's largest are rounded at
- * 2^-18 of it (two e4m3 rows), else those below 2^-14 of it at 2^-24 of it (f16 after a power of two,
- * as are the values that are not in a page yet).
+ * 2^-18 of it (two e4m3 rows), else those below 2^-17 of it at 2^-25 of it (f16
+ * after a power of two, as are the values that are not in a page yet).
  * The same call gives the same bits.  In another batch a sequence's keys are split
  * over the GPU elsewhere and its sums are joined elsewhere: they may differ by
  * their rounding.

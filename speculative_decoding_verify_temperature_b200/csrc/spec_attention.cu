@@ -241,7 +241,10 @@ __device__ __forceinline__ uint32_t tail_bits(const Att& P, int b, int n, int op
 // largest magnitude to [128, 256), is the sum of two e4m3 rows (four bits of
 // its eight each; an element below 2^-9 of the largest is rounded at 2^-18 of it), so a score is
 // two products.  The tail's keys are split the same way, four products.
-// Values are turned into f16 (which holds every e4m3 value; the tail's rows are divided by a power of two that brings them to [1, 2)).
+// Values are turned into f16, which holds every e4m3 value; the tail's rows are divided by a power of two that brings their
+// largest magnitude to [1, 2), so elements below 2^-17 of it are rounded at 2^-25 of it.  Brought higher, rows would keep more of
+// themselves but weigh the rounding of their P more, which are that much smaller: the bound below, 2^-36 of the leading
+// weight times |v| / s_v for each key, would be passed (it was, with [2^14, 2^15)).
 //
 // The scales come back in f32: with a_j the key's scale times the row's and
 // s_v,j the value's, x_j = S_j a_j is the score in base 2 and

@@ -64,6 +64,40 @@ def test_attention_of_far_values(spec, N, Hq, Hkv, D, page, length, blocks, tail
     assert spec.spec_read_device_status(ws) == 0
 
 
+@pytest.mark.parametrize("length", [0, 7, 40])
+@pytest.mark.parametrize("N,Hq,Hkv,D", [(1, 4, 2, 128), (1, 16, 1, 64), (5, 8, 2, 128), (30, 8, 2, 128), (40, 8, 1, 64)])
+def test_attention_of_small_elements_of_open_values(spec, N, Hq, Hkv, D, length):
+    """A value row that is not in a page yet is rounded at 2^-25 of its largest element at worst (half of f16's smallest step,
+    2^-24, of a row that was brought to [1, 2)); the probabilities' weights sum to 1, so the outputs are off by no more than
+    that of the largest row, beside what the other tests allow."""
+    g = torch.Generator().manual_seed(N + length)
+    page, full = 32, length // 32 * 32
+    c, r = make_cache(spec, 1, Hkv, D, page, 2, np.random.RandomState(0)), ref.Cache(1, Hkv, D, page)
+    rows = lambda n, h: torch.randn((1, n, h, D), generator=g)  # noqa: E731
+
+    def values(n):
+        v = rows(n, Hkv) * torch.exp2(-29 * torch.rand((1, n, Hkv, D), generator=g))
+        v[..., 0] = 1.5
+        return v.to(BF)
+
+    if length:
+        k, v = rows(length, Hkv).to(BF), torch.cat((rows(full, Hkv).to(BF) * 0, values(length - full)), 1)
+        spec.spec_kv_append(k.cuda(), v.cuda(), None, c)
+        r.append(0, k[0], v[0])
+    q, k, v = (rows(N, Hq) * 4).to(BF), rows(N, Hkv).to(BF), values(N)
+    mask = torch.tril(torch.ones(N, N, dtype=torch.bool))[None]
+    out = spec.spec_tree_attention(q.cuda(), k.cuda(), v.cuda(), c, ref.pack(mask).cuda())[0].cpu().double()
+    cached = [torch.cat(((b.view(torch.float8_e4m3fn).double() * s[..., None, None]).transpose(1, 2).reshape(-1, Hkv, D),
+                         r.open_rows(0, i).double())) for i in range(2) for b, s in [r.blocks(0, i)]]
+    scales = torch.cat((torch.ones(full, Hkv), ref.row_scale(r.open_rows(0, 1).double())))
+    e, _, pv, mag, small, lost = ref.attention(q[0].double(), k[0].double(), v[0].double(), *cached, mask[0], 1 / math.sqrt(D), scales,
+                                               full)
+    ds = (D + 8) * 2.0 ** -23 * mag + lost
+    tol = e.abs() * 2.0 ** -8 + pv * (2.0 ** -11 + 2 * ds + 2.0 ** -20)[..., None] + small * 2.0 ** -36
+    largest = max(float(x.abs().max()) for x in (v, r.open_rows(0, 1)) if x.numel())
+    assert ((out - e).abs() <= tol + largest * 2.0 ** -25).all()
+
+
 # ----------------------------------------------------------------------------- append
 
 @pytest.mark.parametrize("rot", range(0, 129, 16))
