@@ -250,6 +250,31 @@ def test_tensors_may_be_dropped_after_a_call_on_another_stream(spec, N):
         assert torch.equal(got, want) and len(junk) + len(keep) > 0
 
 
+def test_a_captured_branch_on_another_stream(spec):
+    """Two branches of one graph, each with calls on a stream of its own and temporaries that are dropped at once."""
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    inputs = [attention_inputs(spec, 2, N, 8, 2, 128, 16, [900, 40], N) for N in (3, 40)]
+    args = [(q.cuda(), k.cuda(), v.cuda(), c, ref.pack(mask).cuda()) for c, r, q, k, v, mask in inputs]
+    want = [spec.spec_tree_attention(*a) for a in args]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main, outs = torch.cuda.current_stream(), []
+        for side, a in zip(sides, args):
+            outs.append([])
+            for _ in range(3):
+                temps = [x * 1 for x in a[:3]]
+                side.wait_stream(main)
+                outs[-1].append(spec.spec_tree_attention(*temps, *a[3:], stream=side))
+        for side in sides:
+            main.wait_stream(side)
+        got = [[o * 1 for o in branch] for branch in outs]
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, e) for branch, e in zip(got, want) for o in branch)
+
+
 # ----------------------------------------------------------------------------- several layers
 
 def test_rounds_of_several_layers_as_documented(spec):
