@@ -570,20 +570,24 @@ __device__ void tc_copy_pages(const Att& P, const CUtensorMap* kmap, TcShared& s
     u.begin(P, st);
     const uint32_t bytes = (uint32_t)D << P.pshift;
     int nk = 0, nv = 0, ahead = -2, ahead_t = -1, ahead_b = -1;
-    unsigned k_sent = 0, v_sent = 0;                      // of the last units, bit 0 the last: whether a copy was sent there
-    bool ok = true;                                       // no wait of the CTA has been given up
+    unsigned k_sent = 0;                                  // of the units of keys before nk, bit 0 the last: whether a copy was sent
+    // Whether no wait of the CTA has been given up.  This warp stops at the first: what it has sent are the last units then.
     auto wait = [&](uint64_t* b, uint32_t parity) {
         bar_wait(b, parity, sh);
-        ok = __all_sync(FULL, ok && !aborted(sh));
+        return __all_sync(FULL, !aborted(sh)) != 0;
     };
-    while (u.next(P)) {
+    bool ok = true;
+    while (ok && u.next(P)) {
         // The tail does not lie in pages; it takes two units of keys, which this warp sees pass: a barrier's parity
         // says nothing to a waiter that is two phases behind or ahead.  So it also arrives at the units, which cannot be
         // used, and their barriers cannot go on, before it has.
         if (!u.cached()) {
-            for (int i = 0; i < 2; ++i, ++nk, k_sent <<= 1) {
-                wait(&sh.ke[nk % KR], ((nk / KR) & 1) ^ 1);
-                if (lane == 0 && ok) bar_arrive(&sh.kf[nk % KR]);
+            for (int i = 0; ok && i < 2; ++i) {
+                ok = wait(&sh.ke[nk % KR], ((nk / KR) & 1) ^ 1);
+                if (!ok) break;
+                if (lane == 0) bar_arrive(&sh.kf[nk % KR]);
+                k_sent <<= 1;
+                ++nk;
             }
             continue;
         }
@@ -596,29 +600,30 @@ __device__ void tc_copy_pages(const Att& P, const CUtensorMap* kmap, TcShared& s
         const uint32_t all = __popc(__ballot_sync(FULL, there)) * bytes;
         const int ks = nk % KR, vs = nv % VR;
         const int64_t ph = (int64_t)page * P.Hkv + u.g.h;
-        wait(&sh.ke[ks], ((nk / KR) & 1) ^ 1);
-        k_sent = k_sent << 1 | ok;
-        if (lane == 0 && ok) {
+        ok = wait(&sh.ke[ks], ((nk / KR) & 1) ^ 1);
+        if (!ok) break;
+        if (lane == 0) {
             bar_arrive(&sh.kf[ks]);                       // in the place of the operand warps
             bar_expect(&sh.kf[ks], all);
         }
         __syncwarp();
-        if (ok && there) tensor_copy(base + Tc<D>::K + ks * Tc<D>::RAW_B + lane * bytes, kmap, (int)(ph << P.pshift), &sh.kf[ks]);
-        wait(&sh.re[vs], ((nv / VR) & 1) ^ 1);
-        v_sent = v_sent << 1 | ok;
-        if (lane == 0 && ok) bar_expect(&sh.rf[vs], all);
-        __syncwarp();
-        if (ok && there) bulk_copy(base + Tc<D>::RAW + vs * Tc<D>::RAW_B + lane * bytes, static_cast<const char*>(P.c.v_pages) + ph * bytes,
-                          bytes, &sh.rf[vs]);
+        if (there) tensor_copy(base + Tc<D>::K + ks * Tc<D>::RAW_B + lane * bytes, kmap, (int)(ph << P.pshift), &sh.kf[ks]);
+        k_sent = k_sent << 1 | 1u;
         ++nk;
+        ok = wait(&sh.re[vs], ((nv / VR) & 1) ^ 1);
+        if (!ok) break;
+        if (lane == 0) bar_expect(&sh.rf[vs], all);
+        __syncwarp();
+        if (there) bulk_copy(base + Tc<D>::RAW + vs * Tc<D>::RAW_B + lane * bytes, static_cast<const char*>(P.c.v_pages) + ph * bytes,
+                             bytes, &sh.rf[vs]);
         ++nv;
     }
     // also after a wait that gave up: no copy is in flight when the CTA ends
     bool landed = true;
     for (int i = nk - 1; i >= max(0, nk - KR); --i, k_sent >>= 1)
         if (k_sent & 1) landed &= bar_try(&sh.kf[i % KR], (i / KR) & 1) || bar_wait_slow(&sh.kf[i % KR], (i / KR) & 1, nullptr);
-    for (int i = nv - 1; i >= max(0, nv - VR); --i, v_sent >>= 1)
-        if (v_sent & 1) landed &= bar_try(&sh.rf[i % VR], (i / VR) & 1) || bar_wait_slow(&sh.rf[i % VR], (i / VR) & 1, nullptr);
+    for (int i = nv - 1; i >= max(0, nv - VR); --i)
+        landed &= bar_try(&sh.rf[i % VR], (i / VR) & 1) || bar_wait_slow(&sh.rf[i % VR], (i / VR) & 1, nullptr);
     if (!landed) atomicOr(P.status, 1u << SPEC_ERR_COPY_IN_FLIGHT);
 }
 
